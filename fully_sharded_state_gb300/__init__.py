@@ -4,7 +4,9 @@ dim-0 sharding (FSDP1 FlatParameter or FSDP2 per-parameter), parameter
 all-gather + unflatten, and the fixed-order fp32 gradient reduce-scatter
 fused with the sharded AdamW step, over R virtual ranks held in one GPU's
 HBM. The compute path is the CUDA library ``_lib/libfsdp_shard.so``
-(C ABI in ``include/fsdp_shard.h``); ``capi`` binds it with ctypes.
+(C ABI in ``include/fsdp_shard.h``); ``capi`` binds it with ctypes. The
+operators of a training step around the unit (layer norm, the loss of a
+linear head, Newton-Schulz, Muon) are in ``ops`` (``include/fsdp_ops.h``).
 """
 from .capi import (FSDP_BF16, FSDP_F32, FSDP_FLAT, FSDP_PER_PARAM, FSDP_ZERO3, AdamWHP, FsdpError,
                    FsdpArgumentError, LibraryNotBuilt, fsdp_accumulate_grad,
@@ -28,7 +30,9 @@ __all__ = ["FSDP_BF16", "FSDP_F32", "FSDP_FLAT", "FSDP_PER_PARAM", "FSDP_ZERO3",
            "prepare_fsdp_reduce_scatter_adamw", "prepare_fsdp_reduce_scatter_adamw_units",
            "ShardedUnit",
            "all_gather_units", "reduce_scatter_adamw_units", "prepare_all_gather_units",
-           "prepare_reduce_scatter_adamw_units"]
+           "prepare_reduce_scatter_adamw_units",
+           "layer_norm", "layer_norm_backward", "linear_cross_entropy", "linear_cross_entropy_grad",
+           "newton_schulz", "muon_step", "MuonHP", "ops_wait_timeouts"]
 
 
 def __getattr__(name):
@@ -37,4 +41,8 @@ def __getattr__(name):
                 "prepare_all_gather_units", "prepare_reduce_scatter_adamw_units"):
         from . import unit
         return getattr(unit, name)
+    if name in ("layer_norm", "layer_norm_backward", "linear_cross_entropy", "linear_cross_entropy_grad",
+                "newton_schulz", "muon_step", "MuonHP", "ops_wait_timeouts"):
+        from . import ops
+        return getattr(ops, name)
     raise AttributeError(name)

@@ -1,7 +1,7 @@
 """Build the shard engine's CUDA library in-tree.
 
-Compiles ``csrc/fsdp_kernels.cu`` (nvcc, sm_103a) and ``csrc/fsdp_capi.cpp``
-(g++) in parallel and links ``_lib/libfsdp_shard.so`` with the CUDA runtime
+Compiles the kernels, ``csrc/*.cu`` (nvcc, sm_103a), and the host code,
+``csrc/*.cpp`` (g++), in parallel and links ``_lib/libfsdp_shard.so`` with the CUDA runtime
 linked statically. No cmake, no torch extension machinery: the library has a
 plain C ABI (``include/fsdp_shard.h``).
 
@@ -25,8 +25,10 @@ LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libfsdp_shard.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = ["fsdp_kernels.cu", "fsdp_capi.cpp"]
-HEADERS = [os.path.join(CSRC, "fsdp_internal.h"), os.path.join(INCLUDE, "fsdp_shard.h")]
+SOURCES = ["fsdp_kernels.cu", "fsdp_norm.cu", "fsdp_loss.cu", "fsdp_muon.cu", "fsdp_capi.cpp",
+           "fsdp_ops_capi.cpp"]
+HEADERS = [os.path.join(CSRC, h) for h in ("fsdp_internal.h", "fsdp_ops_internal.h", "fsdp_tc.cuh")] + \
+          [os.path.join(INCLUDE, h) for h in ("fsdp_shard.h", "fsdp_ops.h")]
 
 
 def _cuda_home() -> str:
@@ -43,19 +45,24 @@ def _nvcc() -> str:
     return os.path.join(_cuda_home(), "bin", "nvcc")
 
 
+def _object(name: str) -> str:
+    return os.path.join(BUILD, os.path.splitext(name)[0] + ".o")
+
+
 def compile_commands(ptxas_verbose: bool = False) -> dict:
     cuda_inc = os.path.join(_cuda_home(), "include")
     inc = ["-I", INCLUDE, "-I", CSRC]
     cmds = {}
-    cu = os.path.join(CSRC, "fsdp_kernels.cu")
-    cmds[cu] = [_nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
-                "-Xcompiler", "-fPIC,-ffp-contract=off", *inc, "-c", cu,
-                "-o", os.path.join(BUILD, "fsdp_kernels.o")]
-    if ptxas_verbose:
-        cmds[cu].insert(1, "-Xptxas=-v")
-    cpp = os.path.join(CSRC, "fsdp_capi.cpp")
-    cmds[cpp] = ["g++", "-O2", "-std=c++17", "-fPIC", "-ffp-contract=off", "-Wall", *inc,
-                 "-I", cuda_inc, "-c", cpp, "-o", os.path.join(BUILD, "fsdp_capi.o")]
+    for name in SOURCES:
+        src, obj = os.path.join(CSRC, name), _object(name)
+        if name.endswith(".cu"):
+            cmds[src] = [_nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
+                         "-Xcompiler", "-fPIC,-ffp-contract=off", *inc, "-c", src, "-o", obj]
+            if ptxas_verbose:
+                cmds[src].insert(1, "-Xptxas=-v")
+        else:
+            cmds[src] = ["g++", "-O2", "-std=c++17", "-fPIC", "-ffp-contract=off", "-Wall", *inc,
+                         "-I", cuda_inc, "-c", src, "-o", obj]
     return cmds
 
 
@@ -91,7 +98,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
             raise RuntimeError(f"build failed: {' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
     tmp = LIB + f".tmp{os.getpid()}"
     link = [_nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp,
-            os.path.join(BUILD, "fsdp_kernels.o"), os.path.join(BUILD, "fsdp_capi.o")]
+            *[_object(name) for name in SOURCES]]
     if verbose:
         print(" ".join(link), flush=True)
     res = subprocess.run(link, capture_output=True, text=True)

@@ -19,6 +19,7 @@ FSDP_FLAT, FSDP_PER_PARAM, FSDP_ZERO3 = 1, 2, 3
 FSDP_F32, FSDP_BF16 = 0, 1
 FSDP_MAX_RANKS = 64
 FSDP_SEG_ALIGN = 8
+FSDP_MUON_MAX_MATRICES = 64
 
 (Q_FULL_NUMEL, Q_SHARD_NUMEL, Q_PADDED_NUMEL, Q_N_PARAMS, Q_RANKS, Q_MODE, Q_PARAM_DTYPE,
  Q_GRAD_DTYPE, Q_PARAM_FULL_OFFSET, Q_PARAM_SHARD_OFFSET, Q_PARAM_SHARD_ROWS,
@@ -49,6 +50,13 @@ class FsdpArgumentError(FsdpError, ValueError):
 class AdamWHP(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double)]
+
+
+class MuonHPStruct(ctypes.Structure):
+    """fsdp_muon_hp; users build it through ``MuonHP``."""
+    _fields_ = [("lr", ctypes.c_double), ("momentum", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("eps", ctypes.c_double), ("update_scale", ctypes.c_double), ("nesterov", ctypes.c_int),
+                ("steps", ctypes.c_int), ("a", ctypes.c_double), ("b", ctypes.c_double), ("c", ctypes.c_double)]
 
 
 _lib = None
@@ -115,12 +123,36 @@ def load(path: str = LIB_PATH):
     L.fsdp_stage_wait_timeouts.argtypes = [ctypes.c_int, ctypes.POINTER(ctypes.c_uint64)]
     L.fsdp_stage_wait_selftest.restype = ctypes.c_int
     L.fsdp_stage_wait_selftest.argtypes = [ctypes.c_int, ctypes.POINTER(ctypes.c_uint64)]
+    _declare_ops(L)
     L.fsdp_last_error.restype = ctypes.c_char_p
     L.fsdp_last_error.argtypes = []
     L.fsdp_version.restype = ctypes.c_char_p
     L.fsdp_version.argtypes = []
     _lib = L
     return L
+
+
+def _declare_ops(L) -> None:
+    """The training-step operators (``include/fsdp_ops.h``), which ``ops`` calls."""
+    i64, i32, f64 = ctypes.c_int64, ctypes.c_int, ctypes.c_double
+    pp = ctypes.POINTER(_vp)
+    for name, args in {
+        "fsdp_layer_norm": [i64, i64, _vp, i64, i32, _vp, _vp, i32, f64, _vp, i64, _vp, _vp, _vp],
+        "fsdp_layer_norm_backward": [i64, i64, _vp, i64, _vp, i64, i32, _vp, i32, _vp, _vp, _vp, i64, _vp, _vp, _vp,
+                                     i64, _vp],
+        "fsdp_layer_norm_backward_workspace": [i64, i64, _i64p],
+        "fsdp_linear_cross_entropy": [i64, i64, i64, _vp, i64, _vp, i64, _vp, i64, i32, f64, _vp, _vp, _vp, i64, _vp,
+                                      i64, i64, _vp, i64, _vp],
+        "fsdp_linear_cross_entropy_workspace": [i64, i64, i64, i32, i64, _i64p],
+        "fsdp_newton_schulz": [i64, i64, i64, _vp, i64, i64, i32, _vp, i64, i64, i32, f64, f64, f64, f64, _vp, i64,
+                               _vp],
+        "fsdp_newton_schulz_workspace": [i64, i64, i64, _i64p],
+        "fsdp_muon": [i32, i64, i64, i32, pp, i32, pp, pp, pp, ctypes.POINTER(MuonHPStruct), _vp, i64, _vp],
+        "fsdp_muon_workspace": [i32, i64, i64, _i64p],
+        "fsdp_ops_wait_timeouts": [i32, ctypes.POINTER(ctypes.c_uint64)],
+    }.items():
+        f = getattr(L, name)
+        f.restype, f.argtypes = ctypes.c_int, args
 
 
 def _check(status: int) -> None:

@@ -1,0 +1,653 @@
+// fsdp_loss.cu -- softmax cross entropy of a linear head, with its gradients,
+// for sm_103a, without the rows x vocab logits.
+//
+//   prep      keeps the rows that count, one after the other (zeros past
+//             them), so ignored rows cost no products and what they hold
+//             reaches nothing; their own outputs are written here
+//   logits    z = hidden weight^T on the tensor cores; the epilogue turns each
+//             128-column piece of a row into its maximum, its sum of
+//             exp(z - maximum) and, for the gradients, those exponentials in
+//             fp16 (2^-11 of a number in (0, 1]; the logits themselves are
+//             never stored)
+//   rows      joins a row's pieces: log-sum-exp and loss; for the gradients it
+//             turns the exponentials into G = (softmax - onehot) * scale, in
+//             place, as bf16: the one rounding of G
+//   dhidden   G weight, and dweight = G^T hidden, on the tensor cores, reading
+//             weight, G and hidden as they lie (no transposes)
+//
+// 6 * rows * cols * vocab flops for a step: nothing is computed twice.
+#include <math_constants.h>
+
+#include "fsdp_tc.cuh"
+
+namespace fsdp {
+namespace {
+
+using namespace tc;
+
+constexpr int kTileN = 256;
+constexpr int kPieceCols = kTileN / 2;  // columns of one (maximum, sum)
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// ------------------------------------------------------------------ prep ----
+
+struct PrepParams {
+    int64_t rows, ldh, lddh, ldx;
+    int cols, vocab, chunk;
+    const uint16_t *hidden;
+    const int64_t *targets;
+    int64_t ignore;
+    uint16_t *x;      // kept rows, at most ceil64(rows) of them
+    int *source, *target;
+    int *meta;        // [0] rows kept, [1] rows that count
+    float *row_loss;
+    uint16_t *dhidden;
+};
+
+__device__ __forceinline__ bool kept(int64_t t, const PrepParams &p)
+{
+    return t != p.ignore && t >= 0 && t < p.vocab;
+}
+
+// A warp copies one row (or zeros it, src NULL).
+__device__ __forceinline__ void copy_row(uint16_t *dst, const uint16_t *src, int n, int lane)
+{
+    if (aligned(dst, 16) && (!src || aligned(src, 16))) {
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        for (int c = lane * 8; c + 8 <= n; c += 256)
+            *reinterpret_cast<uint4 *>(dst + c) = src ? *reinterpret_cast<const uint4 *>(src + c) : zero;
+        for (int c = n / 8 * 8 + lane; c < n; c += 32)
+            dst[c] = src ? src[c] : 0;
+    } else {
+        for (int c = lane; c < n; c += 32)
+            dst[c] = src ? src[c] : 0;
+    }
+}
+
+// Block b packs rows [b * chunk, (b + 1) * chunk). It counts the rows before
+// them itself, so one launch does.
+__global__ void __launch_bounds__(256) prep_kernel(const PrepParams p)
+{
+    __shared__ int sums[2];
+    __shared__ int place[256];
+    __shared__ int warps[8];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int64_t lo = (int64_t)blockIdx.x * p.chunk;
+    const int64_t hi = lo + p.chunk < p.rows ? lo + p.chunk : p.rows;
+    if (threadIdx.x < 2)
+        sums[threadIdx.x] = 0;
+    __syncthreads();
+    int nk = 0, nc = 0;
+    for (int64_t r = threadIdx.x; r < lo; r += 256) {
+        const int64_t t = p.targets[r];
+        nk += kept(t, p);
+        nc += t != p.ignore;
+    }
+    nk = __reduce_add_sync(0xffffffffu, nk);
+    nc = __reduce_add_sync(0xffffffffu, nc);
+    if (lane == 0) {
+        atomicAdd(&sums[0], nk);  // whole numbers: the order is of no matter
+        atomicAdd(&sums[1], nc);
+    }
+    __syncthreads();
+    int at = sums[0], count = sums[1];
+    for (int64_t r0 = lo; r0 < hi; r0 += 256) {
+        const int64_t r = r0 + threadIdx.x;
+        const int64_t t = r < hi ? p.targets[r] : p.ignore;
+        const bool k = r < hi && kept(t, p), c = r < hi && t != p.ignore;
+        const unsigned mask = __ballot_sync(0xffffffffu, k);
+        if (lane == 0)
+            warps[warp] = __popc(mask);
+        const int counted = __syncthreads_count(c);
+        int mine = at, all = 0;
+        for (int w = 0; w < 8; w++) {
+            mine += w < warp ? warps[w] : 0;
+            all += warps[w];
+        }
+        mine += __popc(mask & ((1u << lane) - 1));
+        place[threadIdx.x] = k ? mine : -1;
+        if (k) {
+            p.source[mine] = (int)r;
+            p.target[mine] = (int)t;
+        } else if (r < hi) {
+            p.row_loss[r] = c ? CUDART_NAN_F : 0.0f;
+        }
+        __syncthreads();
+        const int n = (int)(hi - r0 < 256 ? hi - r0 : 256);
+        for (int i = warp; i < n; i += 8) {
+            if (place[i] >= 0)
+                copy_row(p.x + (int64_t)place[i] * p.ldx, p.hidden + (r0 + i) * p.ldh, p.cols, lane);
+            else if (p.dhidden)
+                copy_row(p.dhidden + (r0 + i) * p.lddh, nullptr, p.cols, lane);
+        }
+        __syncthreads();
+        at += all;
+        count += counted;
+    }
+    if (hi == p.rows && lo < p.rows) {
+        // the last block knows the totals; the rows up to the next whole K
+        // block are zero, for the products over the rows
+        if (threadIdx.x == 0) {
+            p.meta[0] = at;
+            p.meta[1] = count;
+        }
+        const int end = (at + 63) / 64 * 64;
+        for (int i = at + warp; i < end; i += 8)
+            copy_row(p.x + (int64_t)i * p.ldx, nullptr, p.cols, lane);
+    }
+}
+
+// [rows, cols] with any stride or alignment -> stride ldd, for the tensor maps.
+__global__ void __launch_bounds__(256) pack_rows_kernel(const uint16_t *src, int64_t lds, uint16_t *dst, int64_t ldd,
+                                                        int64_t rows, int cols)
+{
+    const int lane = threadIdx.x % 32;
+    for (int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; r < rows; r += (int64_t)gridDim.x * 8)
+        copy_row(dst + r * ldd, src + r * lds, cols, lane);
+}
+
+// ---------------------------------------------------------------- logits ----
+
+// Each thread has a row of the tile and 128 of its columns, which it reads
+// from tensor memory twice: for the maximum, then for the exponentials.
+struct LogitsEpi {
+    struct Params {
+        uint16_t *e;      // NULL: loss alone
+        int64_t lde;
+        float2 *stats;    // [rows][pieces]
+        int pieces;
+        const int *target;
+        float *tlogit;
+    };
+    template <int COLS>
+    static __device__ __forceinline__ void run(const Params &p, const Slot &x)
+    {
+        static_assert(COLS == kPieceCols, "one thread's columns are one piece");
+        const bool live = x.row < x.M && x.col < x.N;
+        const int t = live ? p.target[x.row] - x.col : -1;
+        float top = -CUDART_INF_F, at = 0.0f;
+#pragma unroll
+        for (int c = 0; c < COLS / 32; c++) {
+            float v[32];
+            x.load(c, v);
+            if (t >= c * 32 && t < c * 32 + 32) {
+#pragma unroll
+                for (int i = 0; i < 32; i++)
+                    at = t == c * 32 + i ? v[i] : at;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i++)
+                if (x.col + c * 32 + i < x.N)
+                    top = fmaxf(top, v[i]);
+        }
+        // a piece of -inf alone: exp(-inf - 0) = 0, not exp(-inf + inf)
+        const float ref = top == -CUDART_INF_F ? 0.0f : top;
+        const float shift = ref * kLog2e;
+        float sum = 0.0f;
+#pragma unroll
+        for (int c = 0; c < COLS / 32; c++) {
+            float v[32];
+            x.load(c, v);
+#pragma unroll
+            for (int i = 0; i < 32; i++) {
+                v[i] = x.col + c * 32 + i < x.N ? exp2_fast(fmaf(v[i], kLog2e, -shift)) : 0.0f;
+                sum += v[i];
+            }
+            if (p.e && live)
+                store16<false>(p.e + (int64_t)x.row * p.lde + x.col + c * 32, v, (int)(p.lde - x.col - c * 32));
+        }
+        if (live) {
+            p.stats[(int64_t)x.row * p.pieces + x.col / COLS] = make_float2(top, sum);
+            if (t >= 0 && t < COLS)
+                p.tlogit[x.row] = at;
+        }
+    }
+};
+
+// ------------------------------------------------------------------ rows ----
+
+struct RowsParams {
+    const int *meta;
+    int base, piece_rows;  // this piece's first kept row; its buffer's rows
+    int vocab, pieces;
+    int64_t lde;
+    uint16_t *e;           // exponentials in, G out; NULL: loss alone
+    const float2 *stats;
+    const int *source, *target;
+    const float *tlogit;
+    float *row_loss;
+    float grad_scale;
+    int mean;
+};
+
+__device__ __forceinline__ float reduce_max(float v, float *sh)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if (threadIdx.x % 32 == 0)
+        sh[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = sh[0];
+    for (int i = 1; i < 8; i++)
+        v = fmaxf(v, sh[i]);
+    __syncthreads();
+    return v;
+}
+__device__ __forceinline__ float reduce_sum(float v, float *sh)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (threadIdx.x % 32 == 0)
+        sh[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = sh[0];
+    for (int i = 1; i < 8; i++)
+        v += sh[i];
+    __syncthreads();
+    return v;
+}
+
+__global__ void __launch_bounds__(256) rows_kernel(const RowsParams p)
+{
+    __shared__ float sh[8];
+    const int n = min(max(p.meta[0] - p.base, 0), p.piece_rows);
+    // rows up to the next whole K block are zeros of G
+    const int end = p.e ? (n + 63) / 64 * 64 : n;
+    const float scale = p.mean ? p.grad_scale / (float)max(p.meta[1], 1) : p.grad_scale;
+    for (int r = blockIdx.x; r < end; r += gridDim.x) {
+        uint16_t *e = p.e + (int64_t)r * p.lde;
+        if (r >= n) {
+            for (int64_t c = threadIdx.x * 8; c < p.lde; c += 256 * 8)
+                *reinterpret_cast<uint4 *>(e + c) = make_uint4(0, 0, 0, 0);
+            continue;
+        }
+        const float2 *st = p.stats + (int64_t)r * p.pieces;
+        float top = -CUDART_INF_F;
+        for (int i = threadIdx.x; i < p.pieces; i += 256)
+            top = fmaxf(top, st[i].x);
+        top = reduce_max(top, sh);
+        const float ref = top == -CUDART_INF_F ? 0.0f : top;
+        float sum = 0.0f;
+        for (int i = threadIdx.x; i < p.pieces; i += 256) {
+            const float2 q = st[i];
+            // a piece without a finite maximum has its exponentials about 0
+            sum += q.y * expf((q.x == -CUDART_INF_F ? 0.0f : q.x) - ref);
+        }
+        sum = reduce_sum(sum, sh);
+        const float lse = ref + logf(sum);
+        if (threadIdx.x == 0)
+            p.row_loss[p.source[p.base + r]] = lse - p.tlogit[r];
+        if (!p.e)
+            continue;
+        const int t = p.target[p.base + r];
+        const float inv = 1.0f / sum;
+        for (int c = threadIdx.x * 8; c < p.lde; c += 256 * 8) {
+            uint4 u = *reinterpret_cast<const uint4 *>(e + c);
+            const float q = st[c / kPieceCols].x;
+            const float f = expf((q == -CUDART_INF_F ? 0.0f : q) - ref) * inv;
+            uint32_t *w = reinterpret_cast<uint32_t *>(&u);
+            const bool here = t >= c && t < c + 8;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+                float a = v.x * f, b = v.y * f;
+                if (here) {
+                    a -= c + 2 * i == t ? 1.0f : 0.0f;
+                    b -= c + 2 * i + 1 == t ? 1.0f : 0.0f;
+                }
+                w[i] = pack_bf16(a * scale, b * scale);
+            }
+            *reinterpret_cast<uint4 *>(e + c) = u;
+        }
+    }
+}
+
+// loss: the rows' sum (in a fixed order), over their count for the mean.
+__global__ void __launch_bounds__(1024) loss_kernel(const float *row_loss, int64_t rows, const int *meta, int mean,
+                                                    float *loss)
+{
+    __shared__ float sh[32];
+    float s = 0.0f;
+    for (int64_t r = threadIdx.x; r < rows; r += 1024)
+        s += row_loss[r];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (threadIdx.x % 32 == 0)
+        sh[threadIdx.x / 32] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        s = sh[0];
+        for (int i = 1; i < 32; i++)
+            s += sh[i];
+        *loss = mean ? s / (float)max(meta[1], 1) : s;
+    }
+}
+
+// ------------------------------------------------------------- gradients ----
+
+// dhidden rows back at their own places, bf16.
+struct HiddenEpi {
+    struct Params {
+        uint16_t *out;
+        int64_t ld;
+        const int *source;
+    };
+    template <int COLS>
+    static __device__ __forceinline__ void run(const Params &p, const Slot &x)
+    {
+        const bool live = x.row < x.M;
+        uint16_t *row = p.out + (live ? (int64_t)p.source[x.row] : 0) * p.ld;
+#pragma unroll 1
+        for (int c = 0; c < COLS / 32; c++) {
+            float v[32];
+            x.load(c, v);
+            if (live)
+                store16<true>(row + x.col + c * 32, v, x.N - x.col - c * 32);
+        }
+    }
+};
+
+// Partial sums of split products, fp32.
+struct PartEpi {
+    struct Params {
+        float *out;  // [splits][rows][ld]
+        int64_t ld, split_stride;
+    };
+    template <int COLS>
+    static __device__ __forceinline__ void run(const Params &p, const Slot &x)
+    {
+        float *row = p.out + x.split * p.split_stride + (int64_t)x.row * p.ld;
+#pragma unroll 1
+        for (int c = 0; c < COLS / 32; c++) {
+            float v[32];
+            x.load(c, v);
+            if (x.row < x.M)
+                store_f32(row + x.col + c * 32, v, x.N - x.col - c * 32);
+        }
+    }
+};
+
+__global__ void __launch_bounds__(256) join_hidden_kernel(const float *parts, int splits, int64_t split_stride,
+                                                          int64_t ldp, const int *meta, int base, int piece_rows,
+                                                          int cols, const int *source, uint16_t *out, int64_t ld)
+{
+    const int n = min(max(meta[0] - base, 0), piece_rows);
+    for (int r = blockIdx.x; r < n; r += gridDim.x) {
+        uint16_t *row = out + (int64_t)source[r] * ld;
+        const float *src = parts + (int64_t)r * ldp;
+        for (int c = threadIdx.x; c < cols; c += 256) {
+            float s = 0.0f;
+            for (int q = 0; q < splits; q++)
+                s += src[q * split_stride + c];
+            row[c] = to_bf16(s);
+        }
+    }
+}
+
+// dweight, over the pieces of the rows in fp32 where there are several.
+struct WeightEpi {
+    struct Params {
+        uint16_t *out;
+        int64_t ld;
+        float *sum;  // NULL: one piece
+        int64_t lds;
+        int first, last;
+    };
+    template <int COLS>
+    static __device__ __forceinline__ void run(const Params &p, const Slot &x)
+    {
+        const bool live = x.row < x.M;
+#pragma unroll 1
+        for (int c = 0; c < COLS / 32; c++) {
+            float v[32];
+            x.load(c, v);
+            const int n = x.N - x.col - c * 32;
+            if (!live || n <= 0)
+                continue;
+            if (p.sum) {
+                float *s = p.sum + (int64_t)x.row * p.lds + x.col + c * 32;
+                if (!p.first) {
+                    float o[32];
+                    load_f32(s, o, n);
+#pragma unroll
+                    for (int i = 0; i < 32; i++)
+                        v[i] += o[i];
+                }
+                if (!p.last)
+                    store_f32(s, v, n);
+            }
+            if (p.last)
+                store16<true>(p.out + (int64_t)x.row * p.ld + x.col + c * 32, v, n);
+        }
+    }
+};
+
+// The workspace of one call, and how the call is cut.
+struct Plan {
+    int64_t piece, pieces, lde, ldx, ldw, ldp;
+    int stat_pieces, splits, split_blocks;
+    int *meta, *source, *target;
+    float *tlogit;
+    float2 *stats;
+    uint16_t *x, *w, *e;
+    float *parts, *dw;
+    int64_t bytes;
+};
+
+bool map_ok(const void *p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0; }
+
+constexpr int kPairs = 76;  // tiles that keep the multiprocessors busy
+
+Plan plan_of(const LossArgs &a, bool grad, void *base, bool with_weight)
+{
+    Plan q{};
+    q.lde = ceil_to(a.vocab, 8);
+    int64_t piece = a.piece_rows;
+    if (piece <= 0) {
+        piece = (int64_t(1) << 31) / (2 * q.lde);
+        piece = piece / 256 * 256;
+    }
+    if (!grad)
+        piece = a.rows;  // nothing of a piece's size is kept
+    piece = ceil_to(piece < 1 ? 1 : piece, 64);
+    q.piece = piece < a.rows ? piece : a.rows;
+    q.pieces = a.rows ? (a.rows + q.piece - 1) / q.piece : 0;
+    q.ldx = ceil_to(a.cols, 16);
+    q.stat_pieces = (int)((a.vocab + kPieceCols - 1) / kPieceCols);
+    // dhidden sums over the vocabulary: where its tiles are few, the sum is
+    // cut so that about all multiprocessors have a part of it
+    const int64_t tiles = (q.piece + 127) / 128 * ((a.cols + kTileN - 1) / kTileN);
+    const int64_t blocks = (a.vocab + kBK - 1) / kBK;
+    int64_t splits = tiles ? 2 * kPairs / tiles : 1;
+    if (splits > blocks / 8)
+        splits = blocks / 8;
+    if (splits < 1)
+        splits = 1;
+    q.split_blocks = (int)((blocks + splits - 1) / splits);
+    q.splits = (int)((blocks + q.split_blocks - 1) / q.split_blocks);
+    q.ldp = ceil_to(a.cols, 8);
+
+    Carver c(base);
+    q.meta = c.take<int>(2);
+    q.source = c.take<int>(a.rows);
+    q.target = c.take<int>(a.rows);
+    q.tlogit = c.take<float>(a.rows);
+    q.x = c.take<uint16_t>(ceil_to(a.rows, 64) * q.ldx);
+    q.stats = c.take<float2>(q.piece * q.stat_pieces);
+    q.w = c.take<uint16_t>(with_weight ? a.vocab * q.ldx : 0);
+    if (grad) {
+        q.e = c.take<uint16_t>(ceil_to(q.piece, 64) * q.lde);
+        if (q.splits > 1)
+            q.parts = c.take<float>(q.splits * q.piece * q.ldp);
+        if (q.pieces > 1)
+            q.dw = c.take<float>(a.vocab * q.ldp);
+    }
+    q.bytes = c.used();
+    return q;
+}
+
+fsdp_status launched(const char *what)
+{
+    const cudaError_t err = cudaGetLastError();
+    return err == cudaSuccess ? FSDP_OK
+                              : set_error(FSDP_ECUDA, "%s launch failed: %s", what, cudaGetErrorString(err));
+}
+
+}  // namespace
+
+int64_t loss_workspace(const LossArgs &a, bool grad) { return plan_of(a, grad, nullptr, true).bytes; }
+
+fsdp_status launch_linear_cross_entropy(const LossArgs &a, void *workspace, int dev, void *stream)
+{
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool grad = a.dweight != nullptr;
+    const int sms = device_sms(dev);
+    const bool direct = map_ok(a.weight, a.ldw);
+    const Plan q = plan_of(a, grad, workspace, !direct);
+    fsdp_status st;
+    if (a.rows == 0) {
+        cudaError_t err = cudaMemsetAsync(a.loss, 0, sizeof(float), s);
+        if (err == cudaSuccess && grad)
+            err = cudaMemset2DAsync(a.dweight, (size_t)a.lddw * 2, 0, (size_t)a.cols * 2, (size_t)a.vocab, s);
+        return err == cudaSuccess ? FSDP_OK
+                                  : set_error(FSDP_ECUDA, "linear_cross_entropy: %s", cudaGetErrorString(err));
+    }
+
+    PrepParams pp{};
+    pp.rows = a.rows;
+    pp.ldh = a.ldh;
+    pp.lddh = a.lddh;
+    pp.ldx = q.ldx;
+    pp.cols = (int)a.cols;
+    pp.vocab = (int)a.vocab;
+    pp.hidden = static_cast<const uint16_t *>(a.hidden);
+    pp.targets = a.targets;
+    pp.ignore = a.ignore_index;
+    pp.x = q.x;
+    pp.source = q.source;
+    pp.target = q.target;
+    pp.meta = q.meta;
+    pp.row_loss = a.row_loss;
+    pp.dhidden = static_cast<uint16_t *>(a.dhidden);
+    int64_t chunk = (a.rows + 4 * sms - 1) / (4 * sms);
+    pp.chunk = (int)(chunk < 8 ? 8 : chunk);
+    const unsigned prep_grid = (unsigned)((a.rows + pp.chunk - 1) / pp.chunk);
+    prep_kernel<<<prep_grid, 256, 0, s>>>(pp);
+    if ((st = launched("linear_cross_entropy (rows kept)")) != FSDP_OK)
+        return st;
+
+    const uint16_t *w = static_cast<const uint16_t *>(a.weight);
+    int64_t ldw = a.ldw;
+    if (!direct) {
+        const int64_t blocks = (a.vocab + 7) / 8;
+        pack_rows_kernel<<<(unsigned)(blocks < 8 * sms ? blocks : 8 * sms), 256, 0, s>>>(w, ldw, q.w, q.ldx, a.vocab,
+                                                                                      (int)a.cols);
+        if ((st = launched("linear_cross_entropy (weight)")) != FSDP_OK)
+            return st;
+        w = q.w;
+        ldw = q.ldx;
+    }
+
+    for (int64_t piece = 0; piece < q.pieces; piece++) {
+        const int64_t row0 = piece * q.piece;
+        const int rows = (int)(a.rows - row0 < q.piece ? a.rows - row0 : q.piece);
+        const uint16_t *x = q.x + row0 * q.ldx;
+        Shape sh{};
+        sh.M = rows;
+        sh.N = (int)a.vocab;
+        sh.K = (int)a.cols;
+        sh.batch = 1;
+        sh.dyn = q.meta;
+        sh.dyn_base = (int)row0;
+        const Operand ox{x, a.cols, ceil_to(rows, 64), q.ldx, 0};
+        const Operand ow{w, a.cols, a.vocab, ldw, 0};
+        const LogitsEpi::Params le{q.e, q.lde, q.stats, q.stat_pieces, q.target + row0, q.tlogit + row0};
+        if ((st = product<1, kTileN, false, false, LogitsEpi>(sh, ox, ow, true, le, dev, s,
+                                                              "linear_cross_entropy (logits)")) != FSDP_OK)
+            return st;
+
+        RowsParams rp{};
+        rp.meta = q.meta;
+        rp.base = (int)row0;
+        rp.piece_rows = rows;
+        rp.vocab = (int)a.vocab;
+        rp.pieces = q.stat_pieces;
+        rp.lde = q.lde;
+        rp.e = q.e;
+        rp.stats = q.stats;
+        rp.source = q.source;
+        rp.target = q.target;
+        rp.tlogit = q.tlogit + row0;
+        rp.row_loss = a.row_loss;
+        rp.grad_scale = a.grad_scale;
+        rp.mean = a.mean;
+        const int64_t rows_grid = ceil_to(rows, 64) < 8 * sms ? ceil_to(rows, 64) : 8 * sms;
+        rows_kernel<<<(unsigned)rows_grid, 256, 0, s>>>(rp);
+        if ((st = launched("linear_cross_entropy (rows)")) != FSDP_OK)
+            return st;
+        if (!grad)
+            continue;
+
+        // dhidden = G weight: K = vocab, adjacent in G; weight has its columns adjacent
+        const Operand og{q.e, a.vocab, ceil_to(rows, 64), q.lde, 0};
+        const Operand owt{w, a.cols, a.vocab, ldw, 0};
+        Shape sd{};
+        sd.M = rows;
+        sd.N = (int)a.cols;
+        sd.K = (int)a.vocab;
+        sd.batch = 1;
+        sd.dyn = q.meta;
+        sd.dyn_base = (int)row0;
+        sd.splits = q.splits;
+        sd.split_blocks = q.split_blocks;
+        uint16_t *dh = static_cast<uint16_t *>(a.dhidden);
+        if (q.splits > 1) {
+            const int64_t stride = q.piece * q.ldp;
+            st = product<1, kTileN, false, true, PartEpi>(sd, og, owt, true, {q.parts, q.ldp, stride}, dev, s,
+                                                          "linear_cross_entropy (dhidden)");
+            if (st != FSDP_OK)
+                return st;
+            join_hidden_kernel<<<(unsigned)(rows < 8 * sms ? rows : 8 * sms), 256, 0, s>>>(
+                q.parts, q.splits, stride, q.ldp, q.meta, (int)row0, rows, (int)a.cols, q.source + row0, dh, a.lddh);
+            st = launched("linear_cross_entropy (dhidden, sum)");
+        } else {
+            st = product<1, kTileN, false, true, HiddenEpi>(sd, og, owt, true, {dh, a.lddh, q.source + row0}, dev, s,
+                                                            "linear_cross_entropy (dhidden)");
+        }
+        if (st != FSDP_OK)
+            return st;
+
+        // dweight = G^T hidden: K = rows, adjacent in neither
+        const Operand ogt{q.e, a.vocab, ceil_to(rows, 64), q.lde, 0};
+        const Operand oxt{x, a.cols, ceil_to(rows, 64), q.ldx, 0};
+        Shape sw{};
+        sw.M = (int)a.vocab;
+        sw.N = (int)a.cols;
+        sw.K = rows;
+        sw.batch = 1;
+        sw.dyn = q.meta;
+        sw.dyn_base = (int)row0;
+        sw.dyn_is_k = 1;
+        const WeightEpi::Params we{static_cast<uint16_t *>(a.dweight), a.lddw, q.dw, q.ldp, piece == 0,
+                                   piece + 1 == q.pieces};
+        if ((st = product<1, kTileN, true, true, WeightEpi>(sw, ogt, oxt, true, we, dev, s,
+                                                            "linear_cross_entropy (dweight)")) != FSDP_OK)
+            return st;
+    }
+    loss_kernel<<<1, 1024, 0, s>>>(a.row_loss, a.rows, q.meta, a.mean, a.loss);
+    return launched("linear_cross_entropy (loss)");
+}
+
+cudaError_t loss_wait_timeouts(unsigned long long *n) { return tc::wait_timeouts(n); }
+
+}  // namespace fsdp

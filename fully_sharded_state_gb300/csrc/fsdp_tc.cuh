@@ -1,0 +1,713 @@
+// fsdp_tc.cuh -- the matrix product of the operators, on the 5th-generation
+// tensor cores of sm_103a:  D[M, N] = A[M, K] B[N, K]^T  in fp32, from two
+// bf16 or two fp16 operands, with an epilogue of the operator's own.
+//
+// One CTA (or a pair of CTAs on two SMs, kCtas = 2) works on one output tile
+// of 128 * kCtas rows and TN columns at a time:
+//   warp 0    TMA: 64-wide K blocks of A and B into a ring of 128-byte
+//             swizzled shared-memory stages (zeros past every edge, so any
+//             M, N, K works)
+//   warp 1    one thread issues tcgen05.mma; the accumulator is TN columns of
+//             tensor memory, double-buffered
+//   warps 4.. eight epilogue warps read the finished accumulator (a thread
+//             holds one row of the tile, TN / 2 columns of it) while the next
+//             tile is being multiplied
+// The grid is persistent. An operand may be stored with K adjacent
+// (row-major [rows, K]) or with its rows adjacent ([K, rows], "MN-major"),
+// which the descriptors express; nothing is transposed in memory.
+//
+// Every wait is bounded (kWaitNs); a role that gives up leaves its loop, and
+// the block counts itself.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+
+#include "fsdp_ops_internal.h"
+
+namespace fsdp {
+namespace tc {
+namespace {
+
+constexpr int kBK = 64;        // K elements of a stage: 128 bytes, one swizzle row
+constexpr int kTM = 128;       // rows of a CTA's tile: the lanes of tensor memory
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 128 + 32 * kEpiWarps;
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+__device__ unsigned long long g_wait_timeouts;
+
+// ------------------------------------------------------------- barriers ----
+
+__device__ __forceinline__ uint32_t saddr(const void *p)
+{
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ void bar_init(uint64_t *bar, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(saddr(bar)), "r"(count) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t *bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(saddr(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+__device__ __forceinline__ uint64_t now_ns()
+{
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+// Waits for the phase of `parity` at most kWaitNs (and 2^27 polls, should the
+// timer stand still); false if it gave up.
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity)
+{
+    if (bar_try(bar, parity))
+        return true;
+    const uint64_t t0 = now_ns();
+    for (uint32_t round = 0; round < (1u << 22); round++) {
+        for (int k = 0; k < 32; k++)
+            if (bar_try(bar, parity))
+                return true;
+        if (now_ns() - t0 > kWaitNs)
+            return false;
+    }
+    return false;
+}
+__device__ __forceinline__ void bar_expect(uint64_t *bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(saddr(bar)), "r"(bytes)
+                 : "memory");
+}
+// One arrival on the barrier at the same place in CTA `rank` of the cluster.
+__device__ __forceinline__ void bar_arrive_at(uint64_t *bar, uint32_t rank)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr(bar)), "r"(rank));
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(a) : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                     : "memory");
+}
+
+// ------------------------------------------------------------ copies, MMA ----
+
+// A box of a 3-D tensor map (x innermost) into shared memory, completing on
+// `bar` (of the pair's even CTA when the CTA is one of two).
+template <int kCtas>
+__device__ __forceinline__ void tma_load(void *dst, const CUtensorMap *map, int x, int y, int z,
+                                         uint64_t *bar)
+{
+    if (kCtas == 2) {
+        // the same offset in the even CTA: its address has the rank bit clear
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(saddr(dst)),
+            "l"(map), "r"(x), "r"(y), "r"(z), "r"(saddr(bar) & 0xFEFFFFFFu)
+            : "memory");
+    } else {
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(saddr(dst)),
+            "l"(map), "r"(x), "r"(y), "r"(z), "r"(saddr(bar))
+            : "memory");
+    }
+}
+
+template <int kCtas>
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    if (kCtas == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+            : "memory");
+}
+
+// One arrival on `bar` (in both CTAs of a pair) when all MMAs issued so far
+// are done.
+template <int kCtas>
+__device__ __forceinline__ void mma_commit(uint64_t *bar)
+{
+    if (kCtas == 2)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+            " [%0], %1;" ::"r"(saddr(bar)),
+            "h"((uint16_t)3)
+            : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                         saddr(bar))
+                     : "memory");
+}
+
+template <int kCtas>
+__device__ __forceinline__ void tmem_alloc(uint32_t *where, uint32_t cols)
+{
+    if (kCtas == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(where)),
+                     "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(where)),
+                     "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+}
+template <int kCtas>
+__device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols)
+{
+    if (kCtas == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols));
+    else
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols));
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 32 columns of this warp's 32 lanes: thread t gets row t's.
+__device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32])
+{
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+          "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; i++)
+        v[i] = __uint_as_float(r[i]);
+}
+
+// Shared-memory matrix descriptor of a 128-byte swizzled operand tile.
+//   K adjacent: rows of 128 bytes (64 of K); 8-row groups 1024 bytes apart.
+//     The next 16 of K start 32 bytes on.
+//   rows adjacent: blocks of [64 of K][64 rows] (8192 bytes, one after the
+//     other along the rows); 8-K groups 1024 bytes apart. The next 16 of K
+//     start 2048 bytes on.
+template <bool kMN>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr)
+{
+    const uint64_t lead = kMN ? (kBK * 128) >> 4 : 1;
+    return (uint64_t)((addr >> 4) & 0x3FFF) | (lead << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+template <bool kMN>
+__host__ __device__ constexpr uint32_t k_step()
+{
+    return (kMN ? 2048 : 32) >> 4;
+}
+
+// ---------------------------------------------------------------- shapes ----
+
+struct Shape {
+    int M, N, K;      // K: the whole contraction
+    int batch;        // matrices, on the maps' third axis
+    int splits;       // parts of K, each its own tile (its results are partial sums)
+    int split_blocks; // K blocks of a part
+    int sym;          // only the 256-squares on and above the diagonal (M = N)
+    int group;        // row tiles that are walked together, for reuse in L2
+    uint32_t idesc;
+    const int *dyn;   // NULL, or a device count that limits M or K:
+    int dyn_base;     //   rows = clamp(*dyn - dyn_base, 0, M or K)
+    int dyn_is_k;
+};
+
+struct Work {
+    int z, split;
+    int row, col;     // first row and column of the (pair's) tile
+    int kb, nkb;      // first K block and their number
+};
+
+template <int kCtas, int TN>
+struct Tiles {
+    static constexpr int kRows = kTM * kCtas;
+    static constexpr int kSquare = 256;  // of sym
+    int m_tiles, n_tiles, M, K;
+    int64_t per_z, total;
+
+    __device__ __forceinline__ Tiles(const Shape &s)
+    {
+        M = s.M;
+        K = s.K;
+        if (s.dyn) {
+            int n = *s.dyn - s.dyn_base;
+            int &lim = s.dyn_is_k ? K : M;
+            lim = n < 0 ? 0 : n < lim ? n : lim;
+        }
+        m_tiles = (M + kRows - 1) / kRows;
+        n_tiles = (s.N + TN - 1) / TN;
+        if (s.sym) {
+            const int64_t q = (M + kSquare - 1) / kSquare;
+            per_z = q * (q + 1) / 2 * (kSquare / kRows) * (kSquare / TN);
+        } else {
+            per_z = (int64_t)m_tiles * n_tiles;
+        }
+        total = per_z * s.batch * s.splits;
+    }
+
+    __device__ __forceinline__ Work at(const Shape &s, int64_t t) const
+    {
+        Work w;
+        const int64_t zs = t / per_z;
+        int i = (int)(t - zs * per_z);
+        w.split = (int)(zs % s.splits);
+        w.z = (int)(zs / s.splits);
+        if (s.sym) {
+            constexpr int kSubM = kSquare / kRows, kSubN = kSquare / TN;
+            const int sub = i % (kSubM * kSubN);
+            const int sq = i / (kSubM * kSubN);
+            int c = (int)((sqrtf(8.0f * (float)sq + 1.0f) - 1.0f) * 0.5f);
+            while ((c + 1) * (c + 2) / 2 <= sq)
+                c++;
+            while (c * (c + 1) / 2 > sq)
+                c--;
+            const int r = sq - c * (c + 1) / 2;
+            w.row = r * kSquare + (sub % kSubM) * kRows;
+            w.col = c * kSquare + (sub / kSubM) * TN;
+        } else {
+            const int in_group = s.group * n_tiles;
+            const int g = i / in_group;
+            i -= g * in_group;
+            const int left = m_tiles - g * s.group;
+            const int rows = left < s.group ? left : s.group;
+            w.row = (g * s.group + i % rows) * kRows;
+            w.col = i / rows * TN;
+        }
+        const int nk = (K + kBK - 1) / kBK;
+        w.kb = w.split * s.split_blocks;
+        int n = nk - w.kb;
+        w.nkb = n < 0 ? 0 : n < s.split_blocks ? n : s.split_blocks;
+        return w;
+    }
+};
+
+// What an epilogue thread is given: its row and the first of its TN / 2
+// columns, and where they are in tensor memory.
+struct Slot {
+    int z, split, row, col, M, N;
+    uint32_t tmem;
+    bool mirror;  // sym: also store the transposed element
+    bool empty;   // K was empty: the accumulator holds nothing, the sum is 0
+
+    __device__ __forceinline__ void load(int chunk, float (&v)[32]) const
+    {
+        __syncwarp();  // the load is the whole warp's
+        tmem_load32(tmem + chunk * 32, v);
+        if (empty) {
+#pragma unroll
+            for (int i = 0; i < 32; i++)
+                v[i] = 0.0f;
+        }
+    }
+};
+
+template <int kCtas, int TN>
+struct Ring {
+    static constexpr int kRowsB = TN / kCtas;
+    static constexpr int kBytesA = kTM * kBK * 2;
+    static constexpr int kBytesB = kRowsB * kBK * 2;
+    static constexpr int kStageBytes = kBytesA + kBytesB;
+    static constexpr int kFit = 196 * 1024 / kStageBytes;
+    static constexpr int kStages = kFit < 8 ? kFit : 8;
+    static constexpr int kBarriers = 2 * kStages + 4;
+    // 1024 bytes for the swizzle's alignment, the barriers, the TMEM address
+    static constexpr int kSmem = 1024 + kStages * kStageBytes + kBarriers * 8 + 16;
+};
+
+template <int kCtas, int TN, bool kAMN, bool kBMN, class Epi>
+__global__ void __launch_bounds__(kThreads, 1)
+    product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                   const __grid_constant__ Shape s, const __grid_constant__ typename Epi::Params ep)
+{
+    using R = Ring<kCtas, TN>;
+    extern __shared__ unsigned char raw[];
+    // the same offset in both CTAs of a pair: dynamic shared memory starts at
+    // one address in every CTA
+    unsigned char *ring = raw + ((1024 - (saddr(raw) & 1023)) & 1023);
+    uint64_t *full = reinterpret_cast<uint64_t *>(ring + R::kStages * R::kStageBytes);
+    uint64_t *empty = full + R::kStages;
+    uint64_t *acc_full = empty + R::kStages;
+    uint64_t *acc_empty = acc_full + 2;
+    uint32_t *tmem_at = reinterpret_cast<uint32_t *>(acc_empty + 2);
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = kCtas == 2 ? cluster_rank() : 0;
+    const Tiles<kCtas, TN> tiles(s);
+    const int64_t first = blockIdx.x / kCtas, step = gridDim.x / kCtas;
+
+    if (warp == 2)
+        tmem_alloc<kCtas>(tmem_at, 2 * TN);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < R::kStages; i++) {
+            bar_init(full + i, 1);
+            bar_init(empty + i, 1);
+        }
+        for (int i = 0; i < 2; i++) {
+            bar_init(acc_full + i, 1);
+            bar_init(acc_empty + i, kEpiWarps * kCtas);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    fence_before();
+    if (kCtas == 2)
+        cluster_sync();
+    else
+        __syncthreads();
+    fence_after();
+    const uint32_t tmem = *tmem_at;
+    bool ok = true;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int64_t t = first; ok && t < tiles.total; t += step) {
+                const Work w = tiles.at(s, t);
+                const int row = w.row + (int)rank * kTM, col = w.col + (int)rank * R::kRowsB;
+                for (int kb = 0; kb < w.nkb; kb++) {
+                    if (!(ok = bar_wait(empty + stage, phase ^ 1)))
+                        break;
+                    if (rank == 0)
+                        bar_expect(full + stage, R::kStageBytes * kCtas);
+                    unsigned char *a = ring + stage * R::kStageBytes, *b = a + R::kBytesA;
+                    const int k = (w.kb + kb) * kBK;
+                    if (kAMN) {
+                        for (int i = 0; i < kTM / 64; i++)
+                            tma_load<kCtas>(a + i * 8192, &map_a, row + i * 64, k, w.z, full + stage);
+                    } else {
+                        tma_load<kCtas>(a, &map_a, k, row, w.z, full + stage);
+                    }
+                    if (kBMN) {
+                        for (int i = 0; i < R::kRowsB / 64; i++)
+                            tma_load<kCtas>(b + i * 8192, &map_b, col + i * 64, k, w.z, full + stage);
+                    } else {
+                        tma_load<kCtas>(b, &map_b, k, col, w.z, full + stage);
+                    }
+                    if (++stage == R::kStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            if (!ok) {
+                // copies may be in flight: give them time before the block ends
+                const uint64_t t0 = now_ns();
+                for (int i = 0; i < (1 << 20) && now_ns() - t0 < 10000000ull; i++)
+                    __nanosleep(1000);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            for (int64_t t = first; ok && t < tiles.total; t += step) {
+                const Work w = tiles.at(s, t);
+                if (!(ok = bar_wait(acc_empty + acc, acc_phase ^ 1)))
+                    break;
+                fence_after();
+                const uint32_t d = tmem + acc * TN;
+                for (int kb = 0; kb < w.nkb; kb++) {
+                    if (!(ok = bar_wait(full + stage, phase)))
+                        break;
+                    fence_after();
+                    const uint32_t a = saddr(ring + stage * R::kStageBytes);
+                    uint64_t da = operand_desc<kAMN>(a), db = operand_desc<kBMN>(a + R::kBytesA);
+#pragma unroll
+                    for (int k = 0; k < kBK / 16; k++)
+                        mma_f16<kCtas>(d, da + k * k_step<kAMN>(), db + k * k_step<kBMN>(), s.idesc,
+                                       kb > 0 || k > 0);
+                    mma_commit<kCtas>(empty + stage);
+                    if (++stage == R::kStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                mma_commit<kCtas>(acc_full + acc);
+                if (++acc == 2) {
+                    acc = 0;
+                    acc_phase ^= 1;
+                }
+            }
+        }
+    } else if (warp >= 4) {
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        const int quarter = warp % 4, half = (warp - 4) / 4;
+        for (int64_t t = first; t < tiles.total; t += step) {
+            const Work w = tiles.at(s, t);
+            ok = bar_wait(acc_full + acc, acc_phase);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok)
+                break;
+            fence_after();
+            Slot x;
+            x.z = w.z;
+            x.split = w.split;
+            x.row = w.row + (int)rank * kTM + quarter * 32 + lane;
+            x.col = w.col + half * (TN / 2);
+            x.M = tiles.M;
+            x.N = s.N;
+            x.tmem = tmem + acc * TN + half * (TN / 2) + ((uint32_t)(quarter * 32) << 16);
+            x.mirror = s.sym && w.row / 256 != w.col / 256;
+            x.empty = w.nkb == 0;
+            Epi::template run<TN / 2>(ep, x);
+            fence_before();
+            __syncwarp();
+            if (lane == 0)
+                bar_arrive_at(acc_empty + acc, 0);
+            if (++acc == 2) {
+                acc = 0;
+                acc_phase ^= 1;
+            }
+        }
+    }
+    if (!ok && lane == 0)
+        atomicAdd(&g_wait_timeouts, 1ull);
+    __syncwarp();
+    fence_before();
+    if (kCtas == 2)
+        cluster_sync();
+    else
+        __syncthreads();
+    fence_after();
+    if (warp == 2)
+        tmem_free<kCtas>(tmem, 2 * TN);
+}
+
+// ------------------------------------------------------------- launching ----
+
+// An operand: [outer, inner] with row stride ld, `batch` of them. K adjacent
+// means inner = K, outer = rows; otherwise inner = rows, outer = K.
+struct Operand {
+    const void *p;
+    int64_t inner, outer, ld, batch_stride;
+};
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
+                              CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                              CUtensorMapFloatOOBfill);
+
+inline EncodeFn encode_fn()
+{
+    static const EncodeFn fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
+}
+
+inline fsdp_status make_map(CUtensorMap *map, const Operand &o, int batch, int box_outer, bool bf16)
+{
+    EncodeFn fn = encode_fn();
+    if (!fn)
+        return set_error(FSDP_ECUDA, "the driver has no cuTensorMapEncodeTiled");
+    const cuuint64_t dims[3] = {(cuuint64_t)o.inner, (cuuint64_t)o.outer, (cuuint64_t)batch};
+    const cuuint64_t strides[2] = {(cuuint64_t)o.ld * 2,
+                                   (cuuint64_t)(batch > 1 ? o.batch_stride : o.ld * o.outer) * 2};
+    const cuuint32_t box[3] = {(cuuint32_t)kBK, (cuuint32_t)box_outer, 1};
+    const cuuint32_t es[3] = {1, 1, 1};
+    const CUresult r =
+        fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+           const_cast<void *>(o.p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return set_error(FSDP_ECUDA, "cuTensorMapEncodeTiled: error %d (%lld x %lld, ld %lld)", (int)r,
+                         (long long)o.inner, (long long)o.outer, (long long)o.ld);
+    return FSDP_OK;
+}
+
+// Launches D = A B^T. `s` needs M, N, K, batch, sym, dyn* and, for split
+// sums, splits and split_blocks; the rest is filled in here.
+template <int kCtas, int TN, bool kAMN, bool kBMN, class Epi>
+fsdp_status product(Shape s, const Operand &a, const Operand &b, bool bf16, const typename Epi::Params &ep,
+                    int dev, cudaStream_t stream, const char *what)
+{
+    using R = Ring<kCtas, TN>;
+    auto kernel = product_kernel<kCtas, TN, kAMN, kBMN, Epi>;
+    static std::atomic<uint64_t> ready{0};  // devices (of the first 64) whose attribute is set
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmem);
+        if (e != cudaSuccess)
+            return set_error(FSDP_ECUDA, "%s: cudaFuncSetAttribute: %s", what, cudaGetErrorString(e));
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
+    CUtensorMap ma, mb;
+    fsdp_status st = make_map(&ma, a, s.batch, kAMN ? kBK : kTM, bf16);
+    if (st == FSDP_OK)
+        st = make_map(&mb, b, s.batch, kBMN ? kBK : R::kRowsB, bf16);
+    if (st != FSDP_OK)
+        return st;
+    if (s.splits < 1)
+        s.splits = 1;
+    if (s.splits == 1)
+        s.split_blocks = (s.K + kBK - 1) / kBK;
+    s.group = s.group > 0 ? s.group : 8;
+    // D fp32; A, B bf16 (1) or fp16 (0); majors; N / 8; M / 16
+    s.idesc = (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((kAMN ? 1u : 0u) << 15) |
+              ((kBMN ? 1u : 0u) << 16) | ((uint32_t)(TN / 8) << 17) | ((uint32_t)(kTM * kCtas / 16) << 24);
+    const int64_t mt = (s.M + kTM * kCtas - 1) / (kTM * kCtas), nt = (s.N + TN - 1) / TN;
+    int64_t total = mt * nt;
+    if (s.sym) {
+        const int64_t q = (s.M + 255) / 256;
+        total = q * (q + 1) / 2 * (256 / (kTM * kCtas)) * (256 / TN);
+    }
+    total *= (int64_t)s.batch * s.splits;
+    const int64_t most = device_sms(dev) / kCtas;
+    if (total < 1)
+        return FSDP_OK;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((total < most ? total : most) * kCtas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = R::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = kCtas;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = kCtas == 2 ? 1 : 0;
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, ma, mb, s, ep);
+    if (err != cudaSuccess)
+        return set_error(FSDP_ECUDA, "%s launch failed: %s", what, cudaGetErrorString(err));
+    return FSDP_OK;
+}
+
+inline cudaError_t wait_timeouts(unsigned long long *n)
+{
+    return cudaMemcpyFromSymbol(n, g_wait_timeouts, sizeof *n);
+}
+
+// ------------------------------------------------- rows of an epilogue ----
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float bf16_at(const uint16_t *p) { return __uint_as_float((uint32_t)*p << 16); }
+__device__ __forceinline__ uint16_t to_bf16(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+
+__device__ __forceinline__ bool aligned(const void *p, unsigned bytes)
+{
+    return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
+}
+
+// Stores `n` (of 32) values as 16-bit ones at p, in 16-byte pieces where p
+// is aligned.
+template <bool kBf16>
+__device__ __forceinline__ void store16(uint16_t *p, const float (&v)[32], int n)
+{
+    if (n <= 0)
+        return;
+    if (aligned(p, 16)) {
+#pragma unroll
+        for (int g = 0; g < 4; g++) {
+            if (g * 8 + 8 <= n) {
+                uint4 u;
+                uint32_t *w = reinterpret_cast<uint32_t *>(&u);
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    w[i] = kBf16 ? pack_bf16(v[g * 8 + 2 * i], v[g * 8 + 2 * i + 1])
+                                 : pack_f16(v[g * 8 + 2 * i], v[g * 8 + 2 * i + 1]);
+                *reinterpret_cast<uint4 *>(p + g * 8) = u;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    if (g * 8 + i < n)
+                        p[g * 8 + i] = kBf16 ? to_bf16(v[g * 8 + i])
+                                             : __half_as_ushort(__float2half_rn(v[g * 8 + i]));
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; i++)
+            if (i < n)
+                p[i] = kBf16 ? to_bf16(v[i]) : __half_as_ushort(__float2half_rn(v[i]));
+    }
+}
+
+// fp32 rows, in 16-byte pieces where p is aligned.
+__device__ __forceinline__ void load_f32(const float *p, float (&v)[32], int n)
+{
+    if (aligned(p, 16) && n >= 32) {
+#pragma unroll
+        for (int g = 0; g < 8; g++) {
+            const float4 f = reinterpret_cast<const float4 *>(p)[g];
+            v[4 * g] = f.x;
+            v[4 * g + 1] = f.y;
+            v[4 * g + 2] = f.z;
+            v[4 * g + 3] = f.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; i++)
+            v[i] = i < n ? p[i] : 0.0f;
+    }
+}
+__device__ __forceinline__ void store_f32(float *p, const float (&v)[32], int n)
+{
+    if (aligned(p, 16) && n >= 32) {
+#pragma unroll
+        for (int g = 0; g < 8; g++)
+            reinterpret_cast<float4 *>(p)[g] = make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; i++)
+            if (i < n)
+                p[i] = v[i];
+    }
+}
+
+}  // namespace
+}  // namespace tc
+}  // namespace fsdp

@@ -1,0 +1,300 @@
+"""The operators of a training step around a sharded unit.
+
+``layer_norm`` and ``linear_cross_entropy_grad`` with their gradients, whose
+outputs can be views of a unit's full gradient buffers; ``newton_schulz`` and
+``muon_step``, the matrix-aware update that uses them. Each function checks
+its tensors, allocates its outputs and workspace with torch on the stream
+that the kernels run on, and makes one call of the CUDA library (C ABI in
+``include/fsdp_ops.h``, where the formulas are). Nothing synchronises.
+
+Tensors are CUDA tensors of one device whose rows' elements are adjacent
+(``stride(-1) == 1``); rows may be further apart. ``stream`` defaults to the
+current stream of the tensors' device; tensors that another stream writes or
+frees are the caller's to order, as everywhere in this package.
+"""
+from __future__ import annotations
+
+import ctypes
+from contextlib import nullcontext
+from dataclasses import dataclass
+
+import torch
+
+from . import capi
+from .capi import FsdpArgumentError
+
+_vp, _i64 = ctypes.c_void_p, ctypes.c_int64
+_DT = {torch.bfloat16: capi.FSDP_BF16, torch.float32: capi.FSDP_F32}
+NEWTON_SCHULZ_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def _need(ok, message):
+    if not ok:
+        raise FsdpArgumentError(message)
+
+
+def _matrix(t, name, rows=None, cols=None, dtype=None, device=None):
+    """Checks a 2-D tensor; returns its row stride."""
+    _need(isinstance(t, torch.Tensor) and t.is_cuda, f"{name} is not a CUDA tensor")
+    _need(t.dim() == 2, f"{name} has {t.dim()} dimensions, needs 2")
+    _need(device is None or t.device == device, f"{name} is on {t.device}, other tensors on {device}")
+    _need(dtype is None or t.dtype == dtype, f"{name} has dtype {t.dtype}, needs {dtype}")
+    r, c = t.shape
+    _need((rows is None or r == rows) and (cols is None or c == cols),
+          f"{name} has shape {tuple(t.shape)}, needs ({'any' if rows is None else rows}, "
+          f"{'any' if cols is None else cols})")
+    s0, s1 = t.stride()
+    if r == 0 or c == 0:
+        return c
+    _need(s1 == 1 or c == 1, f"{name}: the elements of a row are not adjacent")
+    _need(r == 1 or s0 >= c, f"{name}: its rows overlap")
+    return s0 if r > 1 else c
+
+
+def _vector(t, name, n, dtype, device):
+    _need(isinstance(t, torch.Tensor) and t.is_cuda, f"{name} is not a CUDA tensor")
+    _need(t.device == device, f"{name} is on {t.device}, other tensors on {device}")
+    _need(t.dim() == 1 and t.shape[0] == n, f"{name} has shape {tuple(t.shape)}, needs ({n},)")
+    _need(t.dtype == dtype, f"{name} has dtype {t.dtype}, needs {dtype}")
+    _need(n <= 1 or t.stride(0) == 1, f"{name} is not contiguous")
+    return t.data_ptr()
+
+
+def _on(stream, device):
+    """The stream's handle, and the context in which memory is allocated for it."""
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream, nullcontext()
+    return stream.cuda_stream, torch.cuda.stream(stream)
+
+
+def _workspace(query, *sizes, device):
+    n = _i64(0)
+    capi._check(query(*sizes, ctypes.byref(n)))
+    return torch.empty(max(n.value, 1), dtype=torch.uint8, device=device), n.value
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+# -- layer norm --------------------------------------------------------------------
+
+def _norm_inputs(x, gamma):
+    ldx = _matrix(x, "x")
+    _need(x.dtype in _DT, f"x has dtype {x.dtype}, needs bfloat16 or float32")
+    _need(x.shape[1] > 0, "x has no columns")
+    _need(isinstance(gamma, torch.Tensor) and gamma.dtype in _DT, "gamma needs dtype bfloat16 or float32")
+    _vector(gamma, "gamma", x.shape[1], gamma.dtype, x.device)
+    return ldx
+
+
+def layer_norm(x, gamma, beta=None, eps: float = 1e-5, out=None, stream=None):
+    """Layer norm of the rows of ``x`` [rows, cols]; ``beta`` None: no offset.
+    Returns (y, mean, rstd): y in x's dtype (``out`` if given), the rows'
+    statistics in fp32, which ``layer_norm_backward`` takes."""
+    lib = capi.load()
+    ldx = _norm_inputs(x, gamma)
+    rows, cols = x.shape
+    if beta is not None:
+        _vector(beta, "beta", cols, gamma.dtype, x.device)
+    handle, ctx = _on(stream, x.device)
+    with ctx:
+        y = torch.empty_like(x, memory_format=torch.contiguous_format) if out is None else out
+        stats = torch.empty((2, rows), dtype=torch.float32, device=x.device)
+    ldy = _matrix(y, "out", rows, cols, x.dtype, x.device)
+    mean, rstd = stats[0], stats[1]
+    capi._check(lib.fsdp_layer_norm(rows, cols, x.data_ptr(), ldx, _DT[x.dtype], gamma.data_ptr(), _ptr(beta),
+                                    _DT[gamma.dtype], eps, y.data_ptr(), ldy, stats.data_ptr(),
+                                    stats.data_ptr() + 4 * rows, handle))
+    return y, mean, rstd
+
+
+def layer_norm_backward(dy, x, gamma, mean, rstd, with_beta: bool = True, dx=None, dgamma=None, dbeta=None,
+                        stream=None):
+    """The gradients of ``layer_norm`` from ``dy``: (dx, dgamma, dbeta). dgamma
+    and dbeta have gamma's dtype; they can be given, e.g. as views of a unit's
+    gradient buffer. dbeta is None where ``with_beta`` is false."""
+    lib = capi.load()
+    ldx = _norm_inputs(x, gamma)
+    rows, cols = x.shape
+    dev = x.device
+    lddy = _matrix(dy, "dy", rows, cols, x.dtype, dev)
+    pm = _vector(mean, "mean", rows, torch.float32, dev)
+    pr = _vector(rstd, "rstd", rows, torch.float32, dev)
+    handle, ctx = _on(stream, dev)
+    with ctx:
+        if dx is None:
+            dx = torch.empty_like(x, memory_format=torch.contiguous_format)
+        if dgamma is None:
+            dgamma = torch.empty(cols, dtype=gamma.dtype, device=dev)
+        if with_beta and dbeta is None:
+            dbeta = torch.empty(cols, dtype=gamma.dtype, device=dev)
+        ws, nws = _workspace(lib.fsdp_layer_norm_backward_workspace, rows, cols, device=dev)
+    _need(with_beta or dbeta is None, "dbeta is given, but with_beta is false")
+    lddx = _matrix(dx, "dx", rows, cols, x.dtype, dev)
+    _vector(dgamma, "dgamma", cols, gamma.dtype, dev)
+    if dbeta is not None:
+        _vector(dbeta, "dbeta", cols, gamma.dtype, dev)
+    capi._check(lib.fsdp_layer_norm_backward(
+        rows, cols, dy.data_ptr(), lddy, x.data_ptr(), ldx, _DT[x.dtype], gamma.data_ptr(), _DT[gamma.dtype], pm, pr,
+        dx.data_ptr(), lddx, dgamma.data_ptr(), _ptr(dbeta), ws.data_ptr(), nws, handle))
+    return dx, dgamma, dbeta
+
+
+# -- the loss of a linear head -----------------------------------------------------
+
+def _loss_call(hidden, weight, targets, ignore_index, reduction, grad, grad_scale, dhidden, dweight, piece_rows,
+               stream):
+    lib = capi.load()
+    ldh = _matrix(hidden, "hidden", dtype=torch.bfloat16)
+    rows, cols = hidden.shape
+    dev = hidden.device
+    ldw = _matrix(weight, "weight", None, cols, torch.bfloat16, dev)
+    vocab = weight.shape[0]
+    _need(cols > 0 and vocab > 0, "hidden and weight need at least one column and one row")
+    _need(reduction in ("mean", "sum"), f"reduction {reduction!r} is not 'mean' or 'sum'")
+    pt = _vector(targets, "targets", rows, torch.int64, dev)
+    handle, ctx = _on(stream, dev)
+    with ctx:
+        loss = torch.empty((), dtype=torch.float32, device=dev)
+        row_loss = torch.empty(rows, dtype=torch.float32, device=dev)
+        if grad:
+            if dhidden is None:
+                dhidden = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+            if dweight is None:
+                dweight = torch.empty((vocab, cols), dtype=torch.bfloat16, device=dev)
+        ws, nws = _workspace(lib.fsdp_linear_cross_entropy_workspace, rows, cols, vocab, int(grad), piece_rows,
+                             device=dev)
+    lddh = lddw = cols
+    if grad:
+        lddh = _matrix(dhidden, "dhidden", rows, cols, torch.bfloat16, dev)
+        lddw = _matrix(dweight, "dweight", vocab, cols, torch.bfloat16, dev)
+    capi._check(lib.fsdp_linear_cross_entropy(
+        rows, cols, vocab, hidden.data_ptr(), ldh, weight.data_ptr(), ldw, pt, int(ignore_index),
+        0 if reduction == "mean" else 1, float(grad_scale), loss.data_ptr(), row_loss.data_ptr(), _ptr(dhidden), lddh,
+        _ptr(dweight), lddw, piece_rows, ws.data_ptr(), nws, handle))
+    return loss, row_loss, dhidden, dweight
+
+
+def linear_cross_entropy(hidden, weight, targets, ignore_index: int = -100, reduction: str = "mean", stream=None):
+    """Cross entropy of ``hidden`` [rows, cols] @ ``weight`` [vocab, cols]^T
+    against ``targets`` (int64), without the logits: (loss, row_loss), fp32.
+    Rows whose target is ``ignore_index`` count for nothing."""
+    return _loss_call(hidden, weight, targets, ignore_index, reduction, False, 1.0, None, None, 0, stream)[:2]
+
+
+def linear_cross_entropy_grad(hidden, weight, targets, ignore_index: int = -100, reduction: str = "mean",
+                              grad_scale: float = 1.0, dhidden=None, dweight=None, piece_rows: int = 0, stream=None):
+    """``linear_cross_entropy`` and its gradients times ``grad_scale``:
+    (loss, row_loss, dhidden, dweight), the gradients in bf16. ``dweight`` can
+    be a view of a unit's gradient buffer. ``piece_rows`` bounds the rows that
+    are worked on at a time, and with them the workspace (0: 2 GiB of it)."""
+    return _loss_call(hidden, weight, targets, ignore_index, reduction, True, grad_scale, dhidden, dweight,
+                      int(piece_rows), stream)
+
+
+# -- Newton-Schulz and Muon ----------------------------------------------------------
+
+def newton_schulz(g, steps: int = 5, eps: float = 1e-7, coefficients=NEWTON_SCHULZ_COEFFICIENTS, out=None,
+                  stream=None):
+    """Orthogonalises ``g`` [m, n], or each matrix of [batch, m, n], by
+    Newton-Schulz iteration; returns bf16 of the same shape. With the default
+    coefficients and steps the singular values end between about 0.7 and 1.2."""
+    lib = capi.load()
+    _need(isinstance(g, torch.Tensor) and g.is_cuda, "g is not a CUDA tensor")
+    _need(g.dtype in _DT, f"g has dtype {g.dtype}, needs bfloat16 or float32")
+    _need(g.dim() in (2, 3), f"g has {g.dim()} dimensions, needs 2 or 3")
+    handle, ctx = _on(stream, g.device)
+    with ctx:
+        if out is None:
+            out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
+        g3 = g if g.dim() == 3 else g.unsqueeze(0)
+        batch, m, n = g3.shape
+        _need(m > 0 and n > 0, "g has no rows or no columns")
+        ws, nws = _workspace(lib.fsdp_newton_schulz_workspace, batch, m, n, device=g.device)
+    _need(isinstance(out, torch.Tensor) and out.shape == g.shape and out.dtype == torch.bfloat16 and
+          out.device == g.device, f"out needs shape {tuple(g.shape)}, bfloat16, on {g.device}")
+    o3 = out if out.dim() == 3 else out.unsqueeze(0)
+    if batch == 0:
+        return out
+    ldg = _matrix(g3[0], "g")
+    ldo = _matrix(o3[0], "out")
+    a, b, c = coefficients
+    capi._check(lib.fsdp_newton_schulz(batch, m, n, g.data_ptr(), ldg, g3.stride(0), _DT[g.dtype], out.data_ptr(), ldo,
+                                       o3.stride(0), steps, eps, a, b, c, ws.data_ptr(), nws, handle))
+    return out
+
+
+@dataclass
+class MuonHP:
+    """Hyper-parameters of ``muon_step``. ``update_scale`` multiplies ``lr`` in
+    the update; None: sqrt(max(1, m / n)) of an [m, n] matrix."""
+    lr: float
+    momentum: float = 0.95
+    weight_decay: float = 0.0
+    nesterov: bool = True
+    eps: float = 1e-7
+    update_scale: float | None = None
+    steps: int = 5
+    coefficients: tuple = NEWTON_SCHULZ_COEFFICIENTS
+
+    def _c(self, m, n):
+        scale = self.update_scale if self.update_scale is not None else max(1.0, m / n) ** 0.5
+        return capi.MuonHPStruct(self.lr, self.momentum, self.weight_decay, self.eps, scale, int(self.nesterov),
+                                 self.steps, *self.coefficients)
+
+
+def muon_step(grads, master, momentum, params, hp: MuonHP, stream=None) -> None:
+    """One Muon step of a list of matrices, in place. ``grads[i]``: the R
+    ranks' gradients of matrix i (bf16 or fp32), folded in rank order and
+    averaged; ``master[i]``, ``momentum[i]``: fp32; ``params``: None, or bf16
+    matrices that receive the rounded master. Matrices of one shape go through
+    the kernels together."""
+    lib = capi.load()
+    count = len(master)
+    _need(len(grads) == count and len(momentum) == count and (params is None or len(params) == count),
+          f"grads, master, momentum and params need one entry per matrix ({count})")
+    groups = {}
+    for i, w in enumerate(master):
+        _need(isinstance(w, torch.Tensor) and w.is_cuda and w.dim() == 2, f"master[{i}] is not a 2-D CUDA tensor")
+        _need(len(grads[i]) > 0, f"grads[{i}] is empty")
+        groups.setdefault((w.shape[0], w.shape[1], len(grads[i]), grads[i][0].dtype), []).append(i)
+    if not groups:
+        return
+    dev = master[0].device
+
+    def ptr(t, name, m, n, dtype):
+        ld = _matrix(t, name, m, n, dtype, dev)
+        _need(m <= 1 or ld == n, f"{name} is not contiguous")
+        return t.data_ptr()
+
+    calls = []
+    for (m, n, R, dt), ids in groups.items():
+        _need(m > 0 and n > 0, "a matrix has no rows or no columns")
+        _need(dt in _DT, f"grads have dtype {dt}, need bfloat16 or float32")
+        _need(R <= capi.FSDP_MAX_RANKS, f"{R} ranks, at most {capi.FSDP_MAX_RANKS}")
+        per = min(capi.FSDP_MUON_MAX_MATRICES, 1024 // R)
+        for lo in range(0, len(ids), per):
+            part = ids[lo:lo + per]
+            k = len(part)
+            g = (_vp * (k * R))(*[ptr(t, f"grads[{i}][{q}]", m, n, dt) for i in part for q, t in enumerate(grads[i])])
+            mo = (_vp * k)(*[ptr(momentum[i], f"momentum[{i}]", m, n, torch.float32) for i in part])
+            ma = (_vp * k)(*[ptr(master[i], f"master[{i}]", m, n, torch.float32) for i in part])
+            po = None if params is None else (_vp * k)(*[ptr(params[i], f"params[{i}]", m, n, torch.bfloat16)
+                                                         for i in part])
+            calls.append((k, m, n, R, g, _DT[dt], mo, ma, po))
+    handle, ctx = _on(stream, dev)
+    for k, m, n, R, g, dt, mo, ma, po in calls:
+        with ctx:
+            ws, nws = _workspace(lib.fsdp_muon_workspace, k, m, n, device=dev)
+        c = hp._c(m, n)
+        capi._check(lib.fsdp_muon(k, m, n, R, g, dt, mo, ma, po, ctypes.byref(c), ws.data_ptr(), nws, handle))
+
+
+def ops_wait_timeouts(device=None) -> int:
+    """Thread blocks of the matrix kernels on ``device`` (default: the current
+    CUDA device) that gave up a wait since the library was loaded; 0 in every
+    valid run. Synchronises the device."""
+    n = ctypes.c_uint64(0)
+    capi._check(capi.load().fsdp_ops_wait_timeouts(capi._device_index(device), ctypes.byref(n)))
+    return int(n.value)
