@@ -35,14 +35,19 @@ __all__ = ["FSDP_BF16", "FSDP_F32", "FSDP_FLAT", "FSDP_PER_PARAM", "FSDP_ZERO3",
            "newton_schulz", "muon_step", "MuonHP", "ops_wait_timeouts"]
 
 
+_UNIT = ("ShardedUnit", "all_gather_units", "reduce_scatter_adamw_units", "prepare_all_gather_units",
+         "prepare_reduce_scatter_adamw_units")
+_OPS = ("layer_norm", "layer_norm_backward", "linear_cross_entropy", "linear_cross_entropy_grad", "newton_schulz",
+        "muon_step", "MuonHP", "ops_wait_timeouts")
+
+
 def __getattr__(name):
     # these import torch; keep the package importable without it
-    if name in ("ShardedUnit", "all_gather_units", "reduce_scatter_adamw_units",
-                "prepare_all_gather_units", "prepare_reduce_scatter_adamw_units"):
-        from . import unit
-        return getattr(unit, name)
-    if name in ("layer_norm", "layer_norm_backward", "linear_cross_entropy", "linear_cross_entropy_grad",
-                "newton_schulz", "muon_step", "MuonHP", "ops_wait_timeouts"):
-        from . import ops
-        return getattr(ops, name)
-    raise AttributeError(name)
+    if name in _UNIT:
+        from . import unit as module
+    elif name in _OPS:
+        from . import ops as module
+    else:
+        raise AttributeError(name)
+    value = globals()[name] = getattr(module, name)  # found directly from now on
+    return value

@@ -46,7 +46,7 @@ struct PrepParams {
     int64_t ignore;
     uint16_t *x;      // kept rows, at most ceil64(rows) of them
     int *source, *target;
-    int *meta;        // [0] rows kept, [1] rows that count
+    int *meta;        // [0] rows kept, [1] rows that count, [2] a counter, zeroed
     float *row_loss;
     uint16_t *dhidden;
 };
@@ -78,6 +78,8 @@ __global__ void __launch_bounds__(256) prep_kernel(const PrepParams p)
     __shared__ int sums[2];
     __shared__ int place[256];
     __shared__ int warps[8];
+    launch_wait();
+    launch_next();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int64_t lo = (int64_t)blockIdx.x * p.chunk;
     const int64_t hi = lo + p.chunk < p.rows ? lo + p.chunk : p.rows;
@@ -137,6 +139,7 @@ __global__ void __launch_bounds__(256) prep_kernel(const PrepParams p)
         if (threadIdx.x == 0) {
             p.meta[0] = at;
             p.meta[1] = count;
+            p.meta[2] = 0;
         }
         const int end = (at + 63) / 64 * 64;
         for (int i = at + warp; i < end; i += 8)
@@ -148,6 +151,8 @@ __global__ void __launch_bounds__(256) prep_kernel(const PrepParams p)
 __global__ void __launch_bounds__(256) pack_rows_kernel(const uint16_t *src, int64_t lds, uint16_t *dst, int64_t ldd,
                                                         int64_t rows, int cols)
 {
+    launch_wait();
+    launch_next();
     const int lane = threadIdx.x % 32;
     for (int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; r < rows; r += (int64_t)gridDim.x * 8)
         copy_row(dst + r * ldd, src + r * lds, cols, lane);
@@ -156,8 +161,10 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(const uint16_t *src, int
 // ---------------------------------------------------------------- logits ----
 
 // Each thread has a row of the tile and 128 of its columns, which it reads
-// from tensor memory twice: for the maximum, then for the exponentials.
+// from tensor memory twice: for the maximum, then for the exponentials. The
+// exponentials leave by the warp's stage, 64 columns of 32 rows at a time.
 struct LogitsEpi {
+    static constexpr int kLeastTN = kTileN;
     struct Params {
         uint16_t *e;      // NULL: loss alone
         int64_t lde;
@@ -170,8 +177,17 @@ struct LogitsEpi {
     static __device__ __forceinline__ void run(const Params &p, const Slot &x)
     {
         static_assert(COLS == kPieceCols, "one thread's columns are one piece");
-        const bool live = x.row < x.M && x.col < x.N;
-        const int t = live ? p.target[x.row] - x.col : -1;
+        // the columns past the vocabulary are compared only where there are some
+        if (x.N - x.col >= COLS)
+            piece<COLS, true>(p, x);
+        else if (x.col < x.N)
+            piece<COLS, false>(p, x);
+    }
+    template <int COLS, bool kWhole>
+    static __device__ __forceinline__ void piece(const Params &p, const Slot &x)
+    {
+        const bool live = x.row < x.M;
+        const int t = live ? p.target[x.row] - x.col : -1, n = x.N - x.col;
         float top = -CUDART_INF_F, at = 0.0f;
 #pragma unroll
         for (int c = 0; c < COLS / 32; c++) {
@@ -184,27 +200,44 @@ struct LogitsEpi {
             }
 #pragma unroll
             for (int i = 0; i < 32; i++)
-                if (x.col + c * 32 + i < x.N)
+                if (kWhole || c * 32 + i < n)
                     top = fmaxf(top, v[i]);
         }
         // a piece of -inf alone: exp(-inf - 0) = 0, not exp(-inf + inf)
         const float ref = top == -CUDART_INF_F ? 0.0f : top;
         const float shift = ref * kLog2e;
-        float sum = 0.0f;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int c = 0; c < COLS / 32; c++) {
             float v[32];
             x.load(c, v);
 #pragma unroll
             for (int i = 0; i < 32; i++) {
-                v[i] = x.col + c * 32 + i < x.N ? exp2_fast(fmaf(v[i], kLog2e, -shift)) : 0.0f;
-                sum += v[i];
+                v[i] = kWhole || c * 32 + i < n ? exp2_fast(fmaf(v[i], kLog2e, -shift)) : 0.0f;
+                sum[i % 4] += v[i];
             }
-            if (p.e && live)
-                store16<false>(p.e + (int64_t)x.row * p.lde + x.col + c * 32, v, (int)(p.lde - x.col - c * 32));
+            if (!p.e)
+                continue;
+#pragma unroll
+            for (int g = 0; g < 4; g++)
+                *x.piece(x.lane, c % 2 * 4 + g) =
+                    make_uint4(pack_f16(v[8 * g], v[8 * g + 1]), pack_f16(v[8 * g + 2], v[8 * g + 3]),
+                               pack_f16(v[8 * g + 4], v[8 * g + 5]), pack_f16(v[8 * g + 6], v[8 * g + 7]));
+            if (c % 2) {
+                __syncwarp();
+                const int col = x.col + (c - 1) * 32 + x.lane % 8 * 8;
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const int r = i * 4 + x.lane / 8, row = x.row - x.lane + r;
+                    if (row < x.M && col < p.lde)
+                        *reinterpret_cast<uint4 *>(p.e + (int64_t)row * p.lde + col) = *x.piece(r, x.lane % 8);
+                }
+                __syncwarp();
+            }
         }
         if (live) {
-            p.stats[(int64_t)x.row * p.pieces + x.col / COLS] = make_float2(top, sum);
+            p.stats[(int64_t)x.row * p.pieces + x.col / COLS] =
+                make_float2(top, (sum[0] + sum[1]) + (sum[2] + sum[3]));
             if (t >= 0 && t < COLS)
                 p.tlogit[x.row] = at;
         }
@@ -217,12 +250,14 @@ struct RowsParams {
     const int *meta;
     int base, piece_rows;  // this piece's first kept row; its buffer's rows
     int vocab, pieces;
-    int64_t lde;
+    int64_t lde, rows;
     uint16_t *e;           // exponentials in, G out; NULL: loss alone
     const float2 *stats;
     const int *source, *target;
     const float *tlogit;
     float *row_loss;
+    float *loss;           // the last piece: where the loss goes
+    int *done;             // blocks that are through (zero before)
     float grad_scale;
     int mean;
 };
@@ -256,17 +291,30 @@ __device__ __forceinline__ float reduce_sum(float v, float *sh)
     return v;
 }
 
+// Two exponentials as fp16 -> two elements of G as bf16; t: which of them is
+// the target's, if any.
+__device__ __forceinline__ uint32_t two_of_g(uint32_t e, float f, float scale, int t)
+{
+    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&e));
+    const float a = v.x * f - (t == 0 ? 1.0f : 0.0f), b = v.y * f - (t == 1 ? 1.0f : 0.0f);
+    return pack_bf16(a * scale, b * scale);
+}
+
 __global__ void __launch_bounds__(256) rows_kernel(const RowsParams p)
 {
     __shared__ float sh[8];
+    __shared__ bool last;
+    launch_wait();
+    launch_next();
     const int n = min(max(p.meta[0] - p.base, 0), p.piece_rows);
-    // rows up to the next whole K block are zeros of G
-    const int end = p.e ? (n + 63) / 64 * 64 : n;
+    const int end = p.e ? (n + 63) / 64 * 64 : n;  // up to the next whole K block: zeros of G
     const float scale = p.mean ? p.grad_scale / (float)max(p.meta[1], 1) : p.grad_scale;
+    const int cols = (p.vocab + 7) / 8 * 8;
+    constexpr int kStep = 256 * 8, kFlight = 4;
     for (int r = blockIdx.x; r < end; r += gridDim.x) {
         uint16_t *e = p.e + (int64_t)r * p.lde;
         if (r >= n) {
-            for (int64_t c = threadIdx.x * 8; c < p.lde; c += 256 * 8)
+            for (int c = threadIdx.x * 8; c < cols; c += kStep)
                 *reinterpret_cast<uint4 *>(e + c) = make_uint4(0, 0, 0, 0);
             continue;
         }
@@ -283,60 +331,60 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowsParams p)
             sum += q.y * expf((q.x == -CUDART_INF_F ? 0.0f : q.x) - ref);
         }
         sum = reduce_sum(sum, sh);
-        const float lse = ref + logf(sum);
         if (threadIdx.x == 0)
-            p.row_loss[p.source[p.base + r]] = lse - p.tlogit[r];
+            p.row_loss[p.source[r]] = ref + logf(sum) - p.tlogit[r];
         if (!p.e)
             continue;
-        const int t = p.target[p.base + r];
+        const int t = p.target[r];
         const float inv = 1.0f / sum;
-        for (int c = threadIdx.x * 8; c < p.lde; c += 256 * 8) {
-            uint4 u = *reinterpret_cast<const uint4 *>(e + c);
+        auto turn = [&](uint4 u, int c) {
             const float q = st[c / kPieceCols].x;
             const float f = expf((q == -CUDART_INF_F ? 0.0f : q) - ref) * inv;
-            uint32_t *w = reinterpret_cast<uint32_t *>(&u);
-            const bool here = t >= c && t < c + 8;
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-                float a = v.x * f, b = v.y * f;
-                if (here) {
-                    a -= c + 2 * i == t ? 1.0f : 0.0f;
-                    b -= c + 2 * i + 1 == t ? 1.0f : 0.0f;
-                }
-                w[i] = pack_bf16(a * scale, b * scale);
-            }
+            u.x = two_of_g(u.x, f, scale, t - c);
+            u.y = two_of_g(u.y, f, scale, t - c - 2);
+            u.z = two_of_g(u.z, f, scale, t - c - 4);
+            u.w = two_of_g(u.w, f, scale, t - c - 6);
             *reinterpret_cast<uint4 *>(e + c) = u;
-        }
-    }
-}
-
-// loss: the rows' sum (in a fixed order), over their count for the mean.
-__global__ void __launch_bounds__(1024) loss_kernel(const float *row_loss, int64_t rows, const int *meta, int mean,
-                                                    float *loss)
-{
-    __shared__ float sh[32];
-    float s = 0.0f;
-    for (int64_t r = threadIdx.x; r < rows; r += 1024)
-        s += row_loss[r];
+        };
+        int c = threadIdx.x * 8;
+        for (; c + (kFlight - 1) * kStep < cols; c += kFlight * kStep) {
+            uint4 u[kFlight];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (threadIdx.x % 32 == 0)
-        sh[threadIdx.x / 32] = s;
+            for (int k = 0; k < kFlight; k++)
+                u[k] = *reinterpret_cast<const uint4 *>(e + c + k * kStep);
+#pragma unroll
+            for (int k = 0; k < kFlight; k++)
+                turn(u[k], c + k * kStep);
+        }
+        for (; c < cols; c += kStep)
+            turn(*reinterpret_cast<const uint4 *>(e + c), c);
+    }
+    if (!p.loss)
+        return;
+    // The last block of the last piece's launch adds the rows' losses up, in
+    // their own order.
     __syncthreads();
     if (threadIdx.x == 0) {
-        s = sh[0];
-        for (int i = 1; i < 32; i++)
-            s += sh[i];
-        *loss = mean ? s / (float)max(meta[1], 1) : s;
+        __threadfence();
+        last = atomicAdd(p.done, 1) == (int)gridDim.x - 1;
     }
+    __syncthreads();
+    if (!last)
+        return;
+    __threadfence();
+    float s = 0.0f;
+    for (int64_t r = threadIdx.x; r < p.rows; r += 256)
+        s += __ldcg(p.row_loss + r);
+    s = reduce_sum(s, sh);
+    if (threadIdx.x == 0)
+        *p.loss = p.mean ? s / (float)max(p.meta[1], 1) : s;
 }
 
 // ------------------------------------------------------------- gradients ----
 
 // dhidden rows back at their own places, bf16.
 struct HiddenEpi {
+    static constexpr int kLeastTN = 64;
     struct Params {
         uint16_t *out;
         int64_t ld;
@@ -345,89 +393,97 @@ struct HiddenEpi {
     template <int COLS>
     static __device__ __forceinline__ void run(const Params &p, const Slot &x)
     {
-        const bool live = x.row < x.M;
-        uint16_t *row = p.out + (live ? (int64_t)p.source[x.row] : 0) * p.ld;
 #pragma unroll 1
         for (int c = 0; c < COLS / 32; c++) {
-            float v[32];
-            x.load(c, v);
-            if (live)
-                store16<true>(row + x.col + c * 32, v, x.N - x.col - c * 32);
+            float mine[32];
+            x.across<false>(c, mine, [&](int r, int i, float(&v)[4]) {
+                const int row = x.row - x.lane + r, col = x.col + c * 32 + i;
+                if (row < x.M && col < x.N)
+                    put4_16<true>(p.out + (int64_t)p.source[row] * p.ld + col, v, x.N - col);
+            });
         }
     }
 };
 
 // Partial sums of split products, fp32.
 struct PartEpi {
+    static constexpr int kLeastTN = 64;
     struct Params {
-        float *out;  // [splits][rows][ld]
+        float *out;  // [splits][rows][ld], ld a multiple of 8
         int64_t ld, split_stride;
     };
     template <int COLS>
     static __device__ __forceinline__ void run(const Params &p, const Slot &x)
     {
-        float *row = p.out + x.split * p.split_stride + (int64_t)x.row * p.ld;
 #pragma unroll 1
         for (int c = 0; c < COLS / 32; c++) {
-            float v[32];
-            x.load(c, v);
-            if (x.row < x.M)
-                store_f32(row + x.col + c * 32, v, x.N - x.col - c * 32);
+            float mine[32];
+            x.across<false>(c, mine, [&](int r, int i, float(&v)[4]) {
+                const int row = x.row - x.lane + r, col = x.col + c * 32 + i;
+                if (row < x.M && col < x.N)
+                    put4_f32(p.out + x.split * p.split_stride + (int64_t)row * p.ld + col, v, 4);
+            });
         }
     }
 };
 
-__global__ void __launch_bounds__(256) join_hidden_kernel(const float *parts, int splits, int64_t split_stride,
+__global__ void __launch_bounds__(128) join_hidden_kernel(const float *parts, int splits, int64_t split_stride,
                                                           int64_t ldp, const int *meta, int base, int piece_rows,
                                                           int cols, const int *source, uint16_t *out, int64_t ld)
 {
+    launch_wait();
+    launch_next();
     const int n = min(max(meta[0] - base, 0), piece_rows);
     for (int r = blockIdx.x; r < n; r += gridDim.x) {
         uint16_t *row = out + (int64_t)source[r] * ld;
         const float *src = parts + (int64_t)r * ldp;
-        for (int c = threadIdx.x; c < cols; c += 256) {
-            float s = 0.0f;
-            for (int q = 0; q < splits; q++)
-                s += src[q * split_stride + c];
-            row[c] = to_bf16(s);
+        for (int c = threadIdx.x * 4; c < cols; c += 128 * 4) {
+            float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+            for (int q = 0; q < splits; q++) {
+                const float4 f = *reinterpret_cast<const float4 *>(src + q * split_stride + c);
+                s[0] += f.x, s[1] += f.y, s[2] += f.z, s[3] += f.w;
+            }
+            put4_16<true>(row + c, s, cols - c);
         }
     }
 }
 
 // dweight, over the pieces of the rows in fp32 where there are several.
 struct WeightEpi {
+    static constexpr int kLeastTN = 64;
     struct Params {
         uint16_t *out;
         int64_t ld;
         float *sum;  // NULL: one piece
-        int64_t lds;
+        int64_t lds; // a multiple of 8
         int first, last;
     };
     template <int COLS>
     static __device__ __forceinline__ void run(const Params &p, const Slot &x)
     {
-        const bool live = x.row < x.M;
 #pragma unroll 1
         for (int c = 0; c < COLS / 32; c++) {
-            float v[32];
-            x.load(c, v);
-            const int n = x.N - x.col - c * 32;
-            if (!live || n <= 0)
-                continue;
-            if (p.sum) {
-                float *s = p.sum + (int64_t)x.row * p.lds + x.col + c * 32;
-                if (!p.first) {
-                    float o[32];
-                    load_f32(s, o, n);
+            float mine[32];
+            x.across<false>(c, mine, [&](int r, int i, float(&v)[4]) {
+                const int row = x.row - x.lane + r, col = x.col + c * 32 + i;
+                if (row >= x.M || col >= x.N)
+                    return;
+                if (p.sum) {
+                    float *s = p.sum + (int64_t)row * p.lds + col;
+                    if (!p.first) {
+                        float o[4];
+                        get4_f32(s, o, 4);
 #pragma unroll
-                    for (int i = 0; i < 32; i++)
-                        v[i] += o[i];
+                        for (int k = 0; k < 4; k++)
+                            v[k] += o[k];
+                    }
+                    if (!p.last)
+                        put4_f32(s, v, 4);
                 }
-                if (!p.last)
-                    store_f32(s, v, n);
-            }
-            if (p.last)
-                store16<true>(p.out + (int64_t)x.row * p.ld + x.col + c * 32, v, n);
+                if (p.last)
+                    put4_16<true>(p.out + (int64_t)row * p.ld + col, v, x.N - col);
+            });
         }
     }
 };
@@ -451,7 +507,7 @@ constexpr int kPairs = 76;  // tiles that keep the multiprocessors busy
 Plan plan_of(const LossArgs &a, bool grad, void *base, bool with_weight)
 {
     Plan q{};
-    q.lde = ceil_to(a.vocab, 8);
+    q.lde = ceil_to(a.vocab, 64);  // whole lines
     int64_t piece = a.piece_rows;
     if (piece <= 0) {
         piece = (int64_t(1) << 31) / (2 * q.lde);
@@ -478,7 +534,7 @@ Plan plan_of(const LossArgs &a, bool grad, void *base, bool with_weight)
     q.ldp = ceil_to(a.cols, 8);
 
     Carver c(base);
-    q.meta = c.take<int>(2);
+    q.meta = c.take<int>(3);
     q.source = c.take<int>(a.rows);
     q.target = c.take<int>(a.rows);
     q.tlogit = c.take<float>(a.rows);
@@ -494,13 +550,6 @@ Plan plan_of(const LossArgs &a, bool grad, void *base, bool with_weight)
     }
     q.bytes = c.used();
     return q;
-}
-
-fsdp_status launched(const char *what)
-{
-    const cudaError_t err = cudaGetLastError();
-    return err == cudaSuccess ? FSDP_OK
-                              : set_error(FSDP_ECUDA, "%s launch failed: %s", what, cudaGetErrorString(err));
 }
 
 }  // namespace
@@ -542,17 +591,16 @@ fsdp_status launch_linear_cross_entropy(const LossArgs &a, void *workspace, int 
     int64_t chunk = (a.rows + 4 * sms - 1) / (4 * sms);
     pp.chunk = (int)(chunk < 8 ? 8 : chunk);
     const unsigned prep_grid = (unsigned)((a.rows + pp.chunk - 1) / pp.chunk);
-    prep_kernel<<<prep_grid, 256, 0, s>>>(pp);
-    if ((st = launched("linear_cross_entropy (rows kept)")) != FSDP_OK)
+    if ((st = launch("linear_cross_entropy (rows kept)", prep_kernel, prep_grid, 256, 0, s, 1, pp)) != FSDP_OK)
         return st;
 
     const uint16_t *w = static_cast<const uint16_t *>(a.weight);
     int64_t ldw = a.ldw;
     if (!direct) {
         const int64_t blocks = (a.vocab + 7) / 8;
-        pack_rows_kernel<<<(unsigned)(blocks < 8 * sms ? blocks : 8 * sms), 256, 0, s>>>(w, ldw, q.w, q.ldx, a.vocab,
-                                                                                      (int)a.cols);
-        if ((st = launched("linear_cross_entropy (weight)")) != FSDP_OK)
+        if ((st = launch("linear_cross_entropy (weight)", pack_rows_kernel,
+                         (unsigned)(blocks < 8 * sms ? blocks : 8 * sms), 256, 0, s, 1, w, ldw, q.w, q.ldx, a.vocab,
+                         a.cols)) != FSDP_OK)
             return st;
         w = q.w;
         ldw = q.ldx;
@@ -572,7 +620,7 @@ fsdp_status launch_linear_cross_entropy(const LossArgs &a, void *workspace, int 
         const Operand ox{x, a.cols, ceil_to(rows, 64), q.ldx, 0};
         const Operand ow{w, a.cols, a.vocab, ldw, 0};
         const LogitsEpi::Params le{q.e, q.lde, q.stats, q.stat_pieces, q.target + row0, q.tlogit + row0};
-        if ((st = product<1, kTileN, false, false, LogitsEpi>(sh, ox, ow, true, le, dev, s,
+        if ((st = product<false, false, LogitsEpi>(sh, ox, ow, true, le, dev, s,
                                                               "linear_cross_entropy (logits)")) != FSDP_OK)
             return st;
 
@@ -585,15 +633,17 @@ fsdp_status launch_linear_cross_entropy(const LossArgs &a, void *workspace, int 
         rp.lde = q.lde;
         rp.e = q.e;
         rp.stats = q.stats;
-        rp.source = q.source;
-        rp.target = q.target;
+        rp.source = q.source + row0;
+        rp.target = q.target + row0;
+        rp.rows = a.rows;
+        rp.loss = piece + 1 == q.pieces ? a.loss : nullptr;
+        rp.done = q.meta + 2;
         rp.tlogit = q.tlogit + row0;
         rp.row_loss = a.row_loss;
         rp.grad_scale = a.grad_scale;
         rp.mean = a.mean;
         const int64_t rows_grid = ceil_to(rows, 64) < 8 * sms ? ceil_to(rows, 64) : 8 * sms;
-        rows_kernel<<<(unsigned)rows_grid, 256, 0, s>>>(rp);
-        if ((st = launched("linear_cross_entropy (rows)")) != FSDP_OK)
+        if ((st = launch("linear_cross_entropy (rows)", rows_kernel, (unsigned)rows_grid, 256, 0, s, 1, rp)) != FSDP_OK)
             return st;
         if (!grad)
             continue;
@@ -613,15 +663,15 @@ fsdp_status launch_linear_cross_entropy(const LossArgs &a, void *workspace, int 
         uint16_t *dh = static_cast<uint16_t *>(a.dhidden);
         if (q.splits > 1) {
             const int64_t stride = q.piece * q.ldp;
-            st = product<1, kTileN, false, true, PartEpi>(sd, og, owt, true, {q.parts, q.ldp, stride}, dev, s,
+            st = product<false, true, PartEpi>(sd, og, owt, true, {q.parts, q.ldp, stride}, dev, s,
                                                           "linear_cross_entropy (dhidden)");
             if (st != FSDP_OK)
                 return st;
-            join_hidden_kernel<<<(unsigned)(rows < 8 * sms ? rows : 8 * sms), 256, 0, s>>>(
-                q.parts, q.splits, stride, q.ldp, q.meta, (int)row0, rows, (int)a.cols, q.source + row0, dh, a.lddh);
-            st = launched("linear_cross_entropy (dhidden, sum)");
+            st = launch("linear_cross_entropy (dhidden, sum)", join_hidden_kernel,
+                        (unsigned)(rows < 16 * sms ? rows : 16 * sms), 128, 0, s, 1, q.parts, q.splits, stride, q.ldp,
+                        q.meta, row0, rows, a.cols, q.source + row0, dh, a.lddh);
         } else {
-            st = product<1, kTileN, false, true, HiddenEpi>(sd, og, owt, true, {dh, a.lddh, q.source + row0}, dev, s,
+            st = product<false, true, HiddenEpi>(sd, og, owt, true, {dh, a.lddh, q.source + row0}, dev, s,
                                                             "linear_cross_entropy (dhidden)");
         }
         if (st != FSDP_OK)
@@ -640,14 +690,13 @@ fsdp_status launch_linear_cross_entropy(const LossArgs &a, void *workspace, int 
         sw.dyn_is_k = 1;
         const WeightEpi::Params we{static_cast<uint16_t *>(a.dweight), a.lddw, q.dw, q.ldp, piece == 0,
                                    piece + 1 == q.pieces};
-        if ((st = product<1, kTileN, true, true, WeightEpi>(sw, ogt, oxt, true, we, dev, s,
+        if ((st = product<true, true, WeightEpi>(sw, ogt, oxt, true, we, dev, s,
                                                             "linear_cross_entropy (dweight)")) != FSDP_OK)
             return st;
     }
-    loss_kernel<<<1, 1024, 0, s>>>(a.row_loss, a.rows, q.meta, a.mean, a.loss);
-    return launched("linear_cross_entropy (loss)");
+    return FSDP_OK;
 }
 
-cudaError_t loss_wait_timeouts(unsigned long long *n) { return tc::wait_timeouts(n); }
+cudaError_t loss_wait_timeouts(unsigned long long *n) { return wait::wait_timeouts(n); }
 
 }  // namespace fsdp

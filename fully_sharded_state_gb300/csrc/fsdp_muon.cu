@@ -3,7 +3,8 @@
 //
 //   start    one pass over the input: the norm's partial sums; for the Muon
 //            step also the fold of the R ranks' gradients and the momentum
-//   scale    x = u / (||u||_F + eps), in fp32 and, for the products, fp16
+//   scale    x = u / (||u||_F + eps) in fp16, for the products; the fp32 u
+//            is scaled where it is read next, in the first step's epilogue
 //   steps x  S = x x^T (or x^T x: the smaller side), P = b S + c S^2 and
 //            x = a x + P x, three products on the tensor cores. S and P are
 //            symmetric: only the squares on and above the diagonal are
@@ -23,9 +24,8 @@ namespace {
 
 using namespace tc;
 
-constexpr int kTileN = 256;
 constexpr int kStartThreads = 256;
-constexpr int kMaxParts = 256;  // partial sums of one matrix's norm
+constexpr int kMaxParts = 1024;  // partial sums of one matrix's norm
 
 __device__ __forceinline__ float block_sum(float v, float *sh)
 {
@@ -88,7 +88,7 @@ __device__ __forceinline__ void store8(float *p, int left, const float (&v)[8])
 struct StartParams {
     int m, n, groups;       // groups of 8 columns per row
     int64_t ldx;            // stride of x
-    int parts;
+    int vec;                // every row of every input starts on 16 bytes
     float *x32;             // [batch][m][ldx]: u
     float *partial;         // [batch][kMaxParts]
     // newton_schulz
@@ -102,31 +102,74 @@ struct StartParams {
     const void *grads[kMuonMaxGrads];
 };
 
+// The sum of R ranks' 8 elements, in rank order. The loads of four ranks are
+// under way together.
+template <bool kBf16>
+__device__ __forceinline__ void fold_vec(const void *const *grads, int R, int64_t at, float (&u)[8])
+{
+    constexpr int kWords = kBf16 ? 1 : 2, kFlight = 4;
+    for (int q0 = 0; q0 < R; q0 += kFlight) {
+        uint4 w[kFlight][kWords];
+#pragma unroll
+        for (int k = 0; k < kFlight; k++)
+            if (q0 + k < R) {
+                const char *p = static_cast<const char *>(grads[q0 + k]) + at * (kBf16 ? 2 : 4);
+#pragma unroll
+                for (int i = 0; i < kWords; i++)
+                    w[k][i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+            }
+#pragma unroll
+        for (int k = 0; k < kFlight; k++)
+            if (q0 + k < R) {
+                const uint32_t *e = reinterpret_cast<const uint32_t *>(w[k]);
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const float o = !kBf16 ? __uint_as_float(e[i])
+                                    : i % 2 ? __uint_as_float(e[i / 2] & 0xffff0000u)
+                                            : __uint_as_float(e[i / 2] << 16);
+                    u[i] = q0 + k == 0 ? o : __fadd_rn(u[i], o);
+                }
+            }
+    }
+}
+
 // Grid (parts, batch). A block's share of a matrix and so the norm's order
 // depend on the sizes alone.
 template <bool kMuon>
 __global__ void __launch_bounds__(kStartThreads) start_kernel(const __grid_constant__ StartParams p)
 {
     __shared__ float sh[kStartThreads / 32];
+    launch_wait();
+    launch_next();
     const int z = blockIdx.y;
     float *x = p.x32 + (int64_t)z * p.m * p.ldx;
     const int64_t total = (int64_t)p.m * p.groups;
     float sq = 0.0f;
     for (int64_t i = (int64_t)blockIdx.x * kStartThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kStartThreads) {
-        const int r = (int)(i / p.groups), c = (int)(i - (int64_t)r * p.groups) * 8, left = p.n - c;
+        const int r = (int)((uint64_t)i < 0x80000000u ? (uint32_t)i / (uint32_t)p.groups : i / p.groups);
+        const int c = (int)(i - (int64_t)r * p.groups) * 8, left = p.n - c;
         float u[8];
         if (kMuon) {
             const int64_t at = (int64_t)r * p.n + c;
-            load8(p.grads[z * p.R], at, left, p.bf16, u);
-            for (int q = 1; q < p.R; q++) {
-                float o[8];
-                load8(p.grads[z * p.R + q], at, left, p.bf16, o);
-#pragma unroll
-                for (int k = 0; k < 8; k++)
-                    u[k] = __fadd_rn(u[k], o[k]);
-            }
+            const void *const *grads = p.grads + z * p.R;
             float m[8];
-            load8(p.momentum[z], at, left, false, m);
+            if (p.vec && left >= 8) {
+                load8(p.momentum[z], at, 8, false, m);
+                if (p.bf16)
+                    fold_vec<true>(grads, p.R, at, u);
+                else
+                    fold_vec<false>(grads, p.R, at, u);
+            } else {
+                load8(p.momentum[z], at, left, false, m);
+                load8(grads[0], at, left, p.bf16, u);
+                for (int q = 1; q < p.R; q++) {
+                    float o[8];
+                    load8(grads[q], at, left, p.bf16, o);
+#pragma unroll
+                    for (int k = 0; k < 8; k++)
+                        u[k] = __fadd_rn(u[k], o[k]);
+                }
+            }
 #pragma unroll
             for (int k = 0; k < 8; k++) {
                 u[k] = __fmul_rn(u[k], p.inv_r);
@@ -147,32 +190,40 @@ __global__ void __launch_bounds__(kStartThreads) start_kernel(const __grid_const
         p.partial[z * kMaxParts + blockIdx.x] = sq;
 }
 
-__global__ void __launch_bounds__(kStartThreads) scale_kernel(float *x32, uint16_t *x16, const float *partial, int parts,
-                                                              float eps, int64_t count)
+// x16 = u / (||u||_F + eps); inv[z]: that factor.
+__global__ void __launch_bounds__(kStartThreads) scale_kernel(const float *x32, uint16_t *x16, const float *partial,
+                                                              int parts, float eps, int64_t count, float *inv_out)
 {
     __shared__ float sh[kStartThreads / 32];
+    launch_wait();
+    launch_next();
     const int z = blockIdx.y;
-    const float sq = block_sum(threadIdx.x < parts ? partial[z * kMaxParts + threadIdx.x] : 0.0f, sh);
+    float sq = 0.0f;
+    for (int i = threadIdx.x; i < parts; i += kStartThreads)
+        sq += partial[z * kMaxParts + i];
+    sq = block_sum(sq, sh);
     const float inv = 1.0f / (sqrtf(sq) + eps);
-    for (int64_t i = ((int64_t)blockIdx.x * kStartThreads + threadIdx.x) * 8; i < count;
-         i += (int64_t)gridDim.x * kStartThreads * 8) {
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        inv_out[z] = inv;
+    const float *src = x32 + z * count;
+    uint16_t *dst = x16 + z * count;
+    const int64_t step = (int64_t)gridDim.x * kStartThreads * 8;
+    for (int64_t i = ((int64_t)blockIdx.x * kStartThreads + threadIdx.x) * 8; i < count; i += step) {
         float v[8];
-        load8(x32 + z * count, i, 8, false, v);
+        load8(src, i, 8, false, v);
         uint4 u;
         uint32_t *w = reinterpret_cast<uint32_t *>(&u);
 #pragma unroll
-        for (int k = 0; k < 8; k++)
-            v[k] *= inv;
-#pragma unroll
         for (int k = 0; k < 4; k++)
-            w[k] = pack_f16(v[2 * k], v[2 * k + 1]);
-        store8(x32 + z * count + i, 8, v);
-        *reinterpret_cast<uint4 *>(x16 + z * count + i) = u;
+            w[k] = pack_f16(v[2 * k] * inv, v[2 * k + 1] * inv);
+        *reinterpret_cast<uint4 *>(dst + i) = u;
     }
 }
 
-// S, or P = b S + c S^2 (from != NULL), in fp16, both triangles.
+// S, or P = b S + c S^2 (from != NULL), in fp16, both triangles. Strides are
+// multiples of 16, so groups of 4 and pairs of rows stay inside a padded row.
 struct SquareEpi {
+    static constexpr int kLeastTN = 64;
     struct Params {
         uint16_t *out;
         const uint16_t *from;
@@ -183,133 +234,110 @@ struct SquareEpi {
     static __device__ __forceinline__ void run(const Params &p, const Slot &x)
     {
         uint16_t *out = p.out + x.z * p.stride;
-        const int64_t row = (int64_t)x.row * p.ld;
+        const uint16_t *from = p.from ? p.from + x.z * p.stride : nullptr;
+        const int row0 = x.row - x.lane;
 #pragma unroll 1
         for (int c = 0; c < COLS / 32; c++) {
-            float v[32];
-            x.load(c, v);
-            const int col = x.col + c * 32, n = x.N - col;
-            if (x.row >= x.M || n <= 0)
+            const int col0 = x.col + c * 32;
+            float mine[32];
+            auto direct = [&](int r, int i, float(&v)[4]) {
+                const int row = row0 + r, col = col0 + i;
+                if (row >= x.M || col >= x.N)
+                    return;
+                const int64_t at = row * p.ld + col;
+                if (from) {
+                    float f[4];
+                    get4_f16(from + at, f);
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        v[k] = fmaf(p.c, v[k], p.b * f[k]);
+                }
+                put4_16<false>(out + at, v, 4);
+            };
+            if (!x.mirror) {
+                x.across<false>(c, mine, direct);
                 continue;
-            if (p.from) {
-                const uint16_t *f = p.from + x.z * p.stride + row + col;
-#pragma unroll
-                for (int i = 0; i < 32; i++)
-                    if (i < n)
-                        v[i] = fmaf(p.c, v[i], p.b * __half2float(__ushort_as_half(f[i])));
             }
-            store16<false>(out + row + col, v, n);
-            if (x.mirror) {
+            x.across<true>(c, mine, direct);
+            // the transposed elements: two rows' on a pair of lanes make one
+            // 32-bit store, of column j on the even and j + 1 on the odd lane
+            const int odd = x.lane & 1, row = x.row & ~1;
 #pragma unroll
-                for (int i = 0; i < 32; i++)
-                    if (i < n)
-                        out[(int64_t)(col + i) * p.ld + x.row] = __half_as_ushort(__float2half_rn(v[i]));
+            for (int j = 0; j < 32; j += 2) {
+                const float other = __shfl_xor_sync(0xffffffffu, odd ? mine[j] : mine[j + 1], 1);
+                const int col = col0 + j + odd;
+                const uint32_t pair = odd ? pack_f16(other, mine[j + 1]) : pack_f16(mine[j], other);
+                if (row < x.M && col < x.N)
+                    *reinterpret_cast<uint32_t *>(out + col * p.ld + row) = pair;
             }
         }
     }
 };
 
-// x = a x + (P x): fp32 in place and the next step's fp16 operand.
+// x = a x + (P x), x the fp32 one. What becomes of it:
+//   kKeep    fp32 in place, and the next step's fp16 operand
+//   kOut     the result, in bf16
+//   kMaster  w = w decay - lr x, and the bf16 parameter
+enum class Then { kKeep, kOut, kMaster };
+
 struct StepEpi {
+    static constexpr int kLeastTN = 64;
     struct Params {
         float *x32;
+        const float *inv;  // the first step's factor of x32, per matrix; NULL: 1
+        int64_t ld, stride;
+        float a;
+        Then then;
         uint16_t *x16;
-        int64_t ld, stride;
-        float a;
-    };
-    template <int COLS>
-    static __device__ __forceinline__ void run(const Params &p, const Slot &x)
-    {
-        const int64_t at = x.z * p.stride + (int64_t)x.row * p.ld + x.col;
-#pragma unroll 1
-        for (int c = 0; c < COLS / 32; c++) {
-            float v[32], o[32];
-            x.load(c, v);
-            const int n = x.N - x.col - c * 32;
-            if (x.row >= x.M || n <= 0)
-                continue;
-            load_f32(p.x32 + at + c * 32, o, n);
-#pragma unroll
-            for (int i = 0; i < 32; i++)
-                v[i] = fmaf(p.a, o[i], v[i]);
-            store_f32(p.x32 + at + c * 32, v, n);
-            store16<false>(p.x16 + at + c * 32, v, n);
-        }
-    }
-};
-
-// The last step: the result in bf16.
-struct OutEpi {
-    struct Params {
-        const float *x32;
-        int64_t ld, stride;
-        float a;
         uint16_t *out;
-        int64_t ldo, out_stride;
-    };
-    template <int COLS>
-    static __device__ __forceinline__ void run(const Params &p, const Slot &x)
-    {
-        const int64_t at = x.z * p.stride + (int64_t)x.row * p.ld + x.col;
-        uint16_t *out = p.out + x.z * p.out_stride + x.row * p.ldo + x.col;
-#pragma unroll 1
-        for (int c = 0; c < COLS / 32; c++) {
-            float v[32], o[32];
-            x.load(c, v);
-            const int n = x.N - x.col - c * 32;
-            if (x.row >= x.M || n <= 0)
-                continue;
-            load_f32(p.x32 + at + c * 32, o, n);
-#pragma unroll
-            for (int i = 0; i < 32; i++)
-                v[i] = fmaf(p.a, o[i], v[i]);
-            store16<true>(out + c * 32, v, n);
-        }
-    }
-};
-
-// The last step of a Muon step: w = w decay - lr x.
-struct MasterEpi {
-    struct Params {
-        const float *x32;
-        int64_t ld, stride;
-        float a, decay, lr;
-        int64_t n;
+        int64_t ldo, out_stride, n;
+        float decay, lr;
         float *master[kMuonMaxMats];
         uint16_t *param[kMuonMaxMats];
     };
     template <int COLS>
     static __device__ __forceinline__ void run(const Params &p, const Slot &x)
     {
-        const int64_t at = x.z * p.stride + (int64_t)x.row * p.ld + x.col;
-        const int64_t to = (int64_t)x.row * p.n + x.col;
-        float *master = p.master[x.z];
-        uint16_t *param = p.param[x.z];
+        const float a = p.inv ? p.a * p.inv[x.z] : p.a;
+        float *x32 = p.x32 + x.z * p.stride;
+        float *master = p.then == Then::kMaster ? p.master[x.z] : nullptr;
+        uint16_t *param = p.then == Then::kMaster ? p.param[x.z] : nullptr;
 #pragma unroll 1
         for (int c = 0; c < COLS / 32; c++) {
-            float v[32], o[32];
-            x.load(c, v);
-            const int n = x.N - x.col - c * 32;
-            if (x.row >= x.M || n <= 0)
-                continue;
-            load_f32(p.x32 + at + c * 32, o, n);
+            float mine[32];
+            x.across<false>(c, mine, [&](int r, int i, float(&v)[4]) {
+                const int row = x.row - x.lane + r, col = x.col + c * 32 + i, left = x.N - col;
+                if (row >= x.M || left <= 0)
+                    return;
+                const int64_t at = row * p.ld + col;
+                float o[4];
+                get4_f32(x32 + at, o, 4);
 #pragma unroll
-            for (int i = 0; i < 32; i++)
-                v[i] = fmaf(p.a, o[i], v[i]);
-            load_f32(master + to + c * 32, o, n);
+                for (int k = 0; k < 4; k++)
+                    v[k] = fmaf(a, o[k], v[k]);
+                if (p.then == Then::kKeep) {
+                    put4_f32(x32 + at, v, 4);
+                    put4_16<false>(p.x16 + x.z * p.stride + at, v, 4);
+                } else if (p.then == Then::kOut) {
+                    put4_16<true>(p.out + x.z * p.out_stride + row * p.ldo + col, v, left);
+                } else {
+                    const int64_t to = row * p.n + col;
+                    get4_f32(master + to, o, left);
 #pragma unroll
-            for (int i = 0; i < 32; i++)
-                v[i] = fmaf(-p.lr, v[i], o[i] * p.decay);
-            store_f32(master + to + c * 32, v, n);
-            if (param)
-                store16<true>(param + to + c * 32, v, n);
+                    for (int k = 0; k < 4; k++)
+                        v[k] = fmaf(-p.lr, v[k], o[k] * p.decay);
+                    put4_f32(master + to, v, left);
+                    if (param)
+                        put4_16<true>(param + to, v, left);
+                }
+            });
         }
     }
 };
 
 // steps = 0: the scaled input is the result.
 struct FinishParams {
-    const float *x32;
+    const float *x32, *inv;
     int m, n, groups;
     int64_t ld;
     uint16_t *out;
@@ -321,12 +349,14 @@ struct FinishParams {
 template <bool kMuon>
 __global__ void __launch_bounds__(kStartThreads) finish_kernel(const __grid_constant__ FinishParams p)
 {
+    launch_wait();
+    launch_next();
     const int z = blockIdx.y;
     const float *x = p.x32 + (int64_t)z * p.m * p.ld;
     for (int64_t i = (int64_t)blockIdx.x * kStartThreads + threadIdx.x; i < (int64_t)p.m * p.n;
          i += (int64_t)gridDim.x * kStartThreads) {
         const int64_t r = i / p.n, c = i - r * p.n;
-        const float v = x[r * p.ld + c];
+        const float v = x[r * p.ld + c] * p.inv[z];
         if (kMuon) {
             const float w = fmaf(-p.lr, v, p.master[z][i] * p.decay);
             p.master[z][i] = w;
@@ -340,7 +370,7 @@ __global__ void __launch_bounds__(kStartThreads) finish_kernel(const __grid_cons
 
 struct Plan {
     int64_t ldx, ldk, k;
-    float *x32, *partial;
+    float *x32, *partial, *inv;
     uint16_t *x16[2], *s, *p;
     int64_t bytes;
 };
@@ -353,6 +383,7 @@ Plan plan_of(int64_t batch, int64_t m, int64_t n, void *base)
     q.ldk = ceil_to(q.k, 16);
     Carver c(base);
     q.partial = c.take<float>(batch * kMaxParts);
+    q.inv = c.take<float>(batch);
     q.x32 = c.take<float>(batch * m * q.ldx);
     q.x16[0] = c.take<uint16_t>(batch * m * q.ldx);
     q.x16[1] = c.take<uint16_t>(batch * m * q.ldx);
@@ -360,13 +391,6 @@ Plan plan_of(int64_t batch, int64_t m, int64_t n, void *base)
     q.p = c.take<uint16_t>(batch * q.k * q.ldk);
     q.bytes = c.used();
     return q;
-}
-
-fsdp_status launched(const char *what)
-{
-    const cudaError_t err = cudaGetLastError();
-    return err == cudaSuccess ? FSDP_OK
-                              : set_error(FSDP_ECUDA, "%s launch failed: %s", what, cudaGetErrorString(err));
 }
 
 }  // namespace
@@ -388,38 +412,45 @@ fsdp_status launch_newton_schulz(const SchulzArgs &a, void *workspace, int dev, 
     sp.groups = (int)(q.ldx / 8);
     sp.ldx = q.ldx;
     const int64_t need = (a.m * sp.groups + kStartThreads - 1) / kStartThreads;
-    const int64_t fill = (4 * sms + a.batch - 1) / a.batch;
+    const int64_t fill = (6 * sms + a.batch - 1) / a.batch;
     int64_t parts = need < fill ? need : fill;
-    sp.parts = (int)(parts < kMaxParts ? parts : kMaxParts);
+    parts = parts < kMaxParts ? parts : kMaxParts;
     sp.x32 = q.x32;
     sp.partial = q.partial;
     sp.bf16 = a.dtype == FSDP_BF16;
-    const dim3 grid(sp.parts, batch);
+    const dim3 grid((unsigned)parts, batch);
     if (muon) {
         sp.R = a.R;
         sp.nesterov = a.nesterov;
         sp.inv_r = 1.0f / (float)a.R;
         sp.mu = a.mu;
-        for (int i = 0; i < batch; i++)
+        uintptr_t low = (uintptr_t)(a.n * (sp.bf16 ? 2 : 4));
+        for (int i = 0; i < batch; i++) {
             sp.momentum[i] = a.momentum[i];
-        for (int i = 0; i < batch * a.R; i++)
+            low |= reinterpret_cast<uintptr_t>(a.momentum[i]);
+        }
+        for (int i = 0; i < batch * a.R; i++) {
             sp.grads[i] = a.grads[i];
-        start_kernel<true><<<grid, kStartThreads, 0, s>>>(sp);
+            low |= reinterpret_cast<uintptr_t>(a.grads[i]);
+        }
+        sp.vec = (low & 15u) == 0;
+        st = launch("muon (start)", start_kernel<true>, grid, kStartThreads, 0, s, 1, sp);
     } else {
         sp.g = a.g;
         sp.ldg = a.ldg;
         sp.g_stride = a.g_stride;
-        start_kernel<false><<<grid, kStartThreads, 0, s>>>(sp);
+        st = launch("newton_schulz (start)", start_kernel<false>, grid, kStartThreads, 0, s, 1, sp);
     }
-    if ((st = launched("newton_schulz (start)")) != FSDP_OK)
+    if (st != FSDP_OK)
         return st;
-    scale_kernel<<<grid, kStartThreads, 0, s>>>(q.x32, q.x16[0], q.partial, sp.parts, a.eps, a.m * q.ldx);
-    if ((st = launched("newton_schulz (scale)")) != FSDP_OK)
+    if ((st = launch("newton_schulz (scale)", scale_kernel, grid, kStartThreads, 0, s, 1, q.x32, q.x16[0], q.partial,
+                     parts, a.eps, a.m * q.ldx, q.inv)) != FSDP_OK)
         return st;
 
     if (a.steps == 0) {
         FinishParams fp{};
         fp.x32 = q.x32;
+        fp.inv = q.inv;
         fp.m = m;
         fp.n = n;
         fp.ld = q.ldx;
@@ -432,28 +463,26 @@ fsdp_status launch_newton_schulz(const SchulzArgs &a, void *workspace, int dev, 
             fp.master[i] = a.master[i];
             fp.param[i] = a.param_out ? static_cast<uint16_t *>(a.param_out[i]) : nullptr;
         }
-        if (muon)
-            finish_kernel<true><<<grid, kStartThreads, 0, s>>>(fp);
-        else
-            finish_kernel<false><<<grid, kStartThreads, 0, s>>>(fp);
-        return launched("newton_schulz (result)");
+        return launch("newton_schulz (result)", muon ? finish_kernel<true> : finish_kernel<false>, grid, kStartThreads,
+                      0, s, 1, fp);
     }
 
     const bool wide = a.m <= a.n;
     const int64_t xs = a.m * q.ldx, ks = q.k * q.ldk;
-    MasterEpi::Params mp{};
-    if (muon) {
-        mp.x32 = q.x32;
-        mp.ld = q.ldx;
-        mp.stride = xs;
-        mp.a = a.a;
-        mp.decay = a.decay;
-        mp.lr = a.lr;
-        mp.n = a.n;
-        for (int i = 0; i < batch; i++) {
-            mp.master[i] = a.master[i];
-            mp.param[i] = a.param_out ? static_cast<uint16_t *>(a.param_out[i]) : nullptr;
-        }
+    StepEpi::Params ep{};
+    ep.x32 = q.x32;
+    ep.ld = q.ldx;
+    ep.stride = xs;
+    ep.a = a.a;
+    ep.out = static_cast<uint16_t *>(a.out);
+    ep.ldo = a.ldo;
+    ep.out_stride = a.out_stride;
+    ep.n = a.n;
+    ep.decay = a.decay;
+    ep.lr = a.lr;
+    for (int i = 0; muon && i < batch; i++) {
+        ep.master[i] = a.master[i];
+        ep.param[i] = a.param_out ? static_cast<uint16_t *>(a.param_out[i]) : nullptr;
     }
     for (int step = 0; step < a.steps; step++) {
         const Operand x{q.x16[step % 2], a.n, a.m, q.ldx, xs};
@@ -465,38 +494,30 @@ fsdp_status launch_newton_schulz(const SchulzArgs &a, void *workspace, int dev, 
         sq.sym = 1;
         const SquareEpi::Params e1{q.s, nullptr, q.ldk, ks, 0.0f, 0.0f};
         const SquareEpi::Params e2{q.p, q.s, q.ldk, ks, a.b, a.c};
-        st = wide ? product<1, kTileN, false, false, SquareEpi>(sq, x, x, false, e1, dev, s, "newton_schulz (S)")
-                  : product<1, kTileN, true, true, SquareEpi>(sq, x, x, false, e1, dev, s, "newton_schulz (S)");
+        st = wide ? product<false, false, SquareEpi>(sq, x, x, false, e1, dev, s, "newton_schulz (S)")
+                  : product<true, true, SquareEpi>(sq, x, x, false, e1, dev, s, "newton_schulz (S)");
         if (st != FSDP_OK)
             return st;
         sq.K = (int)q.k;
-        if ((st = product<1, kTileN, false, false, SquareEpi>(sq, gram, gram, false, e2, dev, s,
-                                                              "newton_schulz (P)")) != FSDP_OK)
+        if ((st = product<false, false, SquareEpi>(sq, gram, gram, false, e2, dev, s, "newton_schulz (P)")) != FSDP_OK)
             return st;
         Shape up{};
         up.M = m;
         up.N = n;
         up.K = (int)q.k;
         up.batch = batch;
-        auto update = [&](auto epi, const auto &ep) {
-            using E = decltype(epi);
-            // wide: P x, x with its columns adjacent; tall: x P, P symmetric
-            return wide ? product<1, kTileN, false, true, E>(up, poly, x, false, ep, dev, s, "newton_schulz (x)")
-                        : product<1, kTileN, false, false, E>(up, x, poly, false, ep, dev, s, "newton_schulz (x)");
-        };
-        if (step + 1 < a.steps)
-            st = update(StepEpi{}, StepEpi::Params{q.x32, q.x16[(step + 1) % 2], q.ldx, xs, a.a});
-        else if (muon)
-            st = update(MasterEpi{}, mp);
-        else
-            st = update(OutEpi{}, OutEpi::Params{q.x32, q.ldx, xs, a.a, static_cast<uint16_t *>(a.out), a.ldo,
-                                                 a.out_stride});
+        ep.inv = step == 0 ? q.inv : nullptr;
+        ep.x16 = q.x16[(step + 1) % 2];
+        ep.then = step + 1 < a.steps ? Then::kKeep : muon ? Then::kMaster : Then::kOut;
+        // wide: P x, x with its columns adjacent; tall: x P, P symmetric
+        st = wide ? product<false, true, StepEpi>(up, poly, x, false, ep, dev, s, "newton_schulz (x)")
+                  : product<false, false, StepEpi>(up, x, poly, false, ep, dev, s, "newton_schulz (x)");
         if (st != FSDP_OK)
             return st;
     }
     return FSDP_OK;
 }
 
-cudaError_t muon_wait_timeouts(unsigned long long *n) { return tc::wait_timeouts(n); }
+cudaError_t muon_wait_timeouts(unsigned long long *n) { return wait::wait_timeouts(n); }
 
 }  // namespace fsdp

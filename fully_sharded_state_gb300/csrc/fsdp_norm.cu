@@ -2,177 +2,149 @@
 //
 // Both passes are bound by HBM: 8 (forward) or 14 (backward) flops per
 // element that is read or written once. TPR threads hold one row in
-// registers, 16 elements each, so x (and dy) is read once whatever the
-// statistics need; rows wider than 16,384 are walked again instead, from L2.
-// A row's mean and its sum of squares about the mean are joined from the
-// threads' own (count, mean, M2) in one exchange, which keeps fp32 precision
-// under a large mean where sum(x^2) - mean^2 would lose it.
+// registers, as the 16-byte chunks it was loaded in, so x (and dy) is read
+// once whatever the statistics need; rows past the widest such shape are
+// walked again instead, from L2. A row's mean and its sum of squares about
+// the mean are formed per warp, in two steps over the registers, and the
+// warps' joined by their counts: fp32 precision under a large mean, where
+// sum(x^2) - mean^2 would lose it.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
-#include "fsdp_ops_internal.h"
+#include "fsdp_launch.cuh"
+#include "fsdp_wait.cuh"
 
 namespace fsdp {
 namespace {
 
-constexpr int kElems = 16;        // of a row, per thread
-constexpr int kMaxTpr = 1024;
-constexpr int kMinThreads = 256;  // narrow rows share a block
+using namespace wait;
+
+constexpr int kWide = 1024;      // threads of the kernels for the widest rows
+constexpr int kMinThreads = 128;  // forward: narrow rows share a block of this size
+constexpr int kBackThreads = 256; // backward: likewise
 
 __device__ __forceinline__ float to_f32(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
 __device__ __forceinline__ float to_f32(float f) { return f; }
 __device__ __forceinline__ void from_f32(uint16_t &d, float f) { d = __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
 __device__ __forceinline__ void from_f32(float &d, float f) { d = f; }
 
-// Element i of a thread's 16 is column col(i): pieces of V adjacent ones, the
-// pieces of one row's threads side by side.
-template <typename T, bool kVec>
-struct Cols {
-    static constexpr int V = kVec ? 16 / (int)sizeof(T) : 1;
-    static constexpr int kPieces = kElems / V;
-    template <int TPR>
-    static __device__ __forceinline__ int at(int i, int t)
+// A chunk: 16 bytes of a row, V elements. Chunk q of thread t of a row's TPR
+// is number q * TPR + t.
+template <typename T>
+struct Chunk {
+    static constexpr int V = 16 / (int)sizeof(T);
+    uint4 raw;
+    __device__ __forceinline__ void values(float (&v)[V]) const
     {
-        return ((i / V) * TPR + t) * V + i % V;
+        const T *e = reinterpret_cast<const T *>(&raw);
+#pragma unroll
+        for (int i = 0; i < V; i++)
+            v[i] = to_f32(e[i]);
+    }
+    // Between two uses: keeps the compiler from holding the widened values,
+    // twice the registers, from one to the other.
+    __device__ __forceinline__ void keep_packed()
+    {
+        asm volatile("" : "+r"(raw.x), "+r"(raw.y), "+r"(raw.z), "+r"(raw.w));
     }
 };
 
-template <typename T, bool kVec, int TPR>
-__device__ __forceinline__ void load_row(const T *p, int cols, int t, float (&v)[kElems])
+// Streamed rows stay out of L1, where gamma and beta are kept.
+__device__ __forceinline__ uint4 load_stream(const void *p)
 {
-    using C = Cols<T, kVec>;
+    uint4 u;
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                 : "l"(p));
+    return u;
+}
+
+// kFull: rows are whole chunks, and every row, gamma and beta start on 16
+// bytes; nothing but vector accesses is compiled then (with the others beside
+// them, unrolled, the kernels outgrow the instruction cache).
+template <typename T, bool kFull>
+__device__ __forceinline__ void load_chunk(Chunk<T> &c, const T *row, int col, int cols)
+{
+    constexpr int V = Chunk<T>::V;
+    if (kFull) {
+        c.raw = col < cols ? load_stream(row + col) : make_uint4(0, 0, 0, 0);
+    } else {
+        c.raw = make_uint4(0, 0, 0, 0);
+        T *e = reinterpret_cast<T *>(&c.raw);
 #pragma unroll
-    for (int q = 0; q < C::kPieces; q++) {
-        const int c = (q * TPR + t) * C::V;
-        if (kVec && c + C::V <= cols) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(p + c);
-            const T *e = reinterpret_cast<const T *>(&u);
+        for (int i = 0; i < V; i++)
+            if (col + i < cols)
+                e[i] = row[col + i];
+    }
+}
+
+template <typename T, bool kFull>
+__device__ __forceinline__ void store_chunk(T *row, int col, int cols, const float (&v)[Chunk<T>::V])
+{
+    constexpr int V = Chunk<T>::V;
+    if (kFull) {
+        uint4 u;
+        T *e = reinterpret_cast<T *>(&u);
 #pragma unroll
-            for (int i = 0; i < C::V; i++)
-                v[q * C::V + i] = to_f32(e[i]);
+        for (int i = 0; i < V; i++)
+            from_f32(e[i], v[i]);
+        __stcs(reinterpret_cast<uint4 *>(row + col), u);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i++)
+            if (col + i < cols)
+                from_f32(row[col + i], v[i]);
+    }
+}
+
+// gamma or beta of a chunk's columns, of either type; zeros past the row.
+template <int V, bool kFull>
+__device__ __forceinline__ void load_param(const void *p, bool bf16, int col, int cols, float (&v)[V])
+{
+    if (kFull) {
+        // volatile, "memory": neither hoisted out of the rows' loop into
+        // registers nor gathered ahead of the stores before it
+        if (bf16) {
+            const uint16_t *q = static_cast<const uint16_t *>(p) + col;
+            uint32_t u[V / 2];
+            if (V == 8)
+                asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(u[0]), "=r"(u[1]), "=r"(u[V / 2 - 2]), "=r"(u[V / 2 - 1])
+                             : "l"(q)
+                             : "memory");
+            else
+                asm volatile("ld.global.nc.v2.b32 {%0,%1}, [%2];" : "=r"(u[0]), "=r"(u[1]) : "l"(q) : "memory");
+#pragma unroll
+            for (int i = 0; i < V / 2; i++) {
+                v[2 * i] = __uint_as_float(u[i] << 16);
+                v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+            }
         } else {
+            const float *q = static_cast<const float *>(p) + col;
 #pragma unroll
-            for (int i = 0; i < C::V; i++)
-                v[q * C::V + i] = c + i < cols ? to_f32(p[c + i]) : 0.0f;
+            for (int i = 0; i < V; i += 4)
+                asm volatile("ld.global.nc.v4.f32 {%0,%1,%2,%3}, [%4];"
+                             : "=f"(v[i]), "=f"(v[i + 1]), "=f"(v[i + 2]), "=f"(v[i + 3])
+                             : "l"(q + i)
+                             : "memory");
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i++)
+            v[i] = col + i >= cols ? 0.0f
+                   : bf16          ? to_f32(static_cast<const uint16_t *>(p)[col + i])
+                                   : static_cast<const float *>(p)[col + i];
     }
 }
 
-template <typename T, bool kVec, int TPR>
-__device__ __forceinline__ void store_row(T *p, int cols, int t, const float (&v)[kElems], bool vec)
+__device__ __forceinline__ float warp_sum(float v)
 {
-    using C = Cols<T, kVec>;
 #pragma unroll
-    for (int q = 0; q < C::kPieces; q++) {
-        const int c = (q * TPR + t) * C::V;
-        if (kVec && vec && c + C::V <= cols) {
-            uint4 u;
-            T *e = reinterpret_cast<T *>(&u);
-#pragma unroll
-            for (int i = 0; i < C::V; i++)
-                from_f32(e[i], v[q * C::V + i]);
-            *reinterpret_cast<uint4 *>(p + c) = u;
-        } else {
-#pragma unroll
-            for (int i = 0; i < C::V; i++)
-                if (c + i < cols)
-                    from_f32(p[c + i], v[q * C::V + i]);
-        }
-    }
-}
-
-// gamma or beta of the thread's columns, of either type.
-template <typename T, bool kVec, int TPR>
-__device__ __forceinline__ void load_param(const void *p, bool bf16, int cols, int t, float (&v)[kElems])
-{
-    using C = Cols<T, kVec>;
-#pragma unroll
-    for (int i = 0; i < kElems; i++) {
-        const int c = C::template at<TPR>(i, t);
-        v[i] = c >= cols ? 0.0f
-               : bf16    ? to_f32(static_cast<const uint16_t *>(p)[c])
-                         : static_cast<const float *>(p)[c];
-    }
-}
-
-// Count, mean and sum of squares about the mean of a part of a row.
-struct Moments {
-    float n, mean, m2;
-};
-__device__ __forceinline__ Moments join(const Moments &a, const Moments &b)
-{
-    const float n = a.n + b.n;
-    if (n == 0.0f)
-        return a;
-    const float d = b.mean - a.mean, r = b.n / n;
-    return {n, a.mean + d * r, a.m2 + b.m2 + d * d * a.n * r};
-}
-
-// Joins over the TPR threads of a row; every one gets the same bits.
-template <int TPR>
-__device__ __forceinline__ Moments join_row(Moments m, float (*sh)[3])
-{
-    constexpr int kWarps = TPR / 32;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        Moments b;
-        b.n = __shfl_xor_sync(0xffffffffu, m.n, o);
-        b.mean = __shfl_xor_sync(0xffffffffu, m.mean, o);
-        b.m2 = __shfl_xor_sync(0xffffffffu, m.m2, o);
-        // the lower lane's part first, on both sides
-        m = (threadIdx.x & o) ? join(b, m) : join(m, b);
-    }
-    if (kWarps > 1) {
-        const int w = threadIdx.x / 32;
-        if (threadIdx.x % 32 == 0) {
-            sh[w][0] = m.n;
-            sh[w][1] = m.mean;
-            sh[w][2] = m.m2;
-        }
-        __syncthreads();
-        const int w0 = w / kWarps * kWarps;
-        m = {sh[w0][0], sh[w0][1], sh[w0][2]};
-        for (int i = 1; i < kWarps; i++)
-            m = join(m, {sh[w0 + i][0], sh[w0 + i][1], sh[w0 + i][2]});
-        __syncthreads();
-    }
-    return m;
-}
-
-// Two sums over the TPR threads of a row.
-template <int TPR>
-__device__ __forceinline__ void sum_row(float &a, float &b, float (*sh)[3])
-{
-    constexpr int kWarps = TPR / 32;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        b += __shfl_xor_sync(0xffffffffu, b, o);
-    }
-    if (kWarps > 1) {
-        const int w = threadIdx.x / 32;
-        if (threadIdx.x % 32 == 0) {
-            sh[w][0] = a;
-            sh[w][1] = b;
-        }
-        __syncthreads();
-        const int w0 = w / kWarps * kWarps;
-        a = sh[w0][0];
-        b = sh[w0][1];
-        for (int i = 1; i < kWarps; i++) {
-            a += sh[w0 + i][0];
-            b += sh[w0 + i][1];
-        }
-        __syncthreads();
-    }
-}
-
-template <int TPR>
-constexpr int block_of()
-{
-    return TPR < kMinThreads ? kMinThreads : TPR;
+    for (int o = 16; o > 0; o >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
 }
 
 struct ForwardParams {
@@ -182,62 +154,122 @@ struct ForwardParams {
     void *y;
     float *mean, *rstd;
     float eps;
-    int param_bf16, vec_out;
+    int param_bf16;
 };
 
-template <typename T, bool kVec, int TPR>
-__global__ void __launch_bounds__(block_of<TPR>()) norm_forward_kernel(const ForwardParams p)
+template <int TPR>
+constexpr int forward_block()
 {
-    constexpr int kRowsPerBlock = block_of<TPR>() / TPR;
-    __shared__ float sh[32][3];
+    return TPR < kMinThreads ? kMinThreads : TPR;
+}
+
+// NV chunks per thread, at most 4: a row of 4096 bf16 is 128 threads', and a
+// multiprocessor has about ten such rows under way. (One warp per row with
+// 16 chunks a thread needs no barrier, but its unrolled code missed the
+// instruction cache: 16384 x 4096 bf16 took 132 us.)
+template <typename T, bool kFull, int TPR, int NV>
+__global__ void __launch_bounds__(forward_block<TPR>()) norm_forward_kernel(const ForwardParams p)
+{
+    constexpr int kRowsPerBlock = forward_block<TPR>() / TPR, kWarps = TPR / 32, V = Chunk<T>::V;
+    __shared__ float4 sh[2][32];
+    launch_wait();
+    launch_next();
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
-    using C = Cols<T, kVec>;
-    float gamma[kElems], beta[kElems];
-    load_param<T, kVec, TPR>(p.gamma, p.param_bf16, p.cols, t, gamma);
-    if (p.beta) {
-        load_param<T, kVec, TPR>(p.beta, p.param_bf16, p.cols, t, beta);
-    } else {
+    const int warp = threadIdx.x / 32, warp0 = warp / kWarps * kWarps;
+    // this warp's number of elements, the same in every row
+    float mine = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kElems; i++)
-            beta[i] = 0.0f;
+    for (int q = 0; q < NV; q++) {
+        const int left = p.cols - (q * TPR + t) * V;
+        mine += (float)(left < 0 ? 0 : left < V ? left : V);
     }
-    for (int64_t r0 = (int64_t)blockIdx.x * kRowsPerBlock; r0 < p.rows; r0 += (int64_t)gridDim.x * kRowsPerBlock) {
+    const float count = warp_sum(mine);
+    const float inv_count = count > 0.0f ? 1.0f / count : 0.0f, inv_cols = 1.0f / (float)p.cols;
+    int phase = 0;
+    for (int64_t r0 = (int64_t)blockIdx.x * kRowsPerBlock; r0 < p.rows;
+         r0 += (int64_t)gridDim.x * kRowsPerBlock, phase ^= 1) {
         const int64_t r = r0 + sub;
+        // rows of one block meet no barrier of each other's unless a row is
+        // several warps', and then the last rows' places are worked on as row
+        // rows - 1, and not stored
         const bool live = r < p.rows;
-        float v[kElems];
-        if (live) {
-            load_row<T, kVec, TPR>(static_cast<const T *>(p.x) + r * p.ldx, p.cols, t, v);
-        } else {
+        if (kWarps == 1 && !live)
+            break;
+        const T *x = static_cast<const T *>(p.x) + (live ? r : p.rows - 1) * p.ldx;
+        Chunk<T> c[NV];
 #pragma unroll
-            for (int i = 0; i < kElems; i++)
-                v[i] = 0.0f;
-        }
-        float n = 0.0f, s = 0.0f, m2 = 0.0f;
+        for (int q = 0; q < NV; q++)
+            load_chunk<T, kFull>(c[q], x, (q * TPR + t) * V, p.cols);
+        float s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kElems; i++)
-            if (C::template at<TPR>(i, t) < p.cols) {
-                n += 1.0f;
+        for (int q = 0; q < NV; q++) {
+            float v[V];
+            c[q].values(v);
+#pragma unroll
+            for (int i = 0; i < V; i++)
                 s += v[i];
-            }
-        const float mu = n > 0.0f ? s / n : 0.0f;
+        }
+        float mean = warp_sum(s) * inv_count, m2 = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kElems; i++)
-            if (C::template at<TPR>(i, t) < p.cols) {
-                const float d = v[i] - mu;
-                m2 += d * d;
+        for (int q = 0; q < NV; q++) {
+            c[q].keep_packed();
+            const int left = p.cols - (q * TPR + t) * V;
+            float v[V];
+            c[q].values(v);
+            if (kFull ? left > 0 : left >= V) {
+#pragma unroll
+                for (int i = 0; i < V; i++)
+                    m2 += (v[i] - mean) * (v[i] - mean);
+            } else if (!kFull) {
+#pragma unroll
+                for (int i = 0; i < V; i++)
+                    if (i < left)
+                        m2 += (v[i] - mean) * (v[i] - mean);
             }
-        const Moments m = join_row<TPR>({n, mu, m2}, sh);
-        const float rstd = 1.0f / sqrtf(m.m2 / (float)p.cols + p.eps);
+        }
+        m2 = warp_sum(m2);
+        if (kWarps > 1) {
+            if (threadIdx.x % 32 == 0)
+                sh[phase][warp] = make_float4(mean, m2, count, 0.0f);
+            __syncthreads();
+            mean = m2 = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; w++)
+                mean += sh[phase][warp0 + w].x * sh[phase][warp0 + w].z;
+            mean *= inv_cols;
+#pragma unroll
+            for (int w = 0; w < kWarps; w++) {
+                const float4 f = sh[phase][warp0 + w];
+                m2 += f.y + f.z * (f.x - mean) * (f.x - mean);
+            }
+        }
+        const float rstd = 1.0f / sqrtf(m2 * inv_cols + p.eps);
         if (!live)
             continue;
         if (t == 0 && p.mean) {
-            p.mean[r] = m.mean;
+            p.mean[r] = mean;
             p.rstd[r] = rstd;
         }
+        T *y = static_cast<T *>(p.y) + r * p.ldy;
 #pragma unroll
-        for (int i = 0; i < kElems; i++)
-            v[i] = (v[i] - m.mean) * rstd * gamma[i] + beta[i];
-        store_row<T, kVec, TPR>(static_cast<T *>(p.y) + r * p.ldy, p.cols, t, v, p.vec_out);
+        for (int q = 0; q < NV; q++) {
+            const int col = (q * TPR + t) * V;
+            if (col >= p.cols)
+                break;
+            float v[V], g[V], b[V];
+            c[q].keep_packed();
+            c[q].values(v);
+            load_param<V, kFull>(p.gamma, p.param_bf16, col, p.cols, g);
+#pragma unroll
+            for (int i = 0; i < V; i++)
+                b[i] = 0.0f;
+            if (p.beta)
+                load_param<V, kFull>(p.beta, p.param_bf16, col, p.cols, b);
+#pragma unroll
+            for (int i = 0; i < V; i++)
+                v[i] = fmaf((v[i] - mean) * rstd, g[i], b[i]);
+            store_chunk<T, kFull>(y, col, p.cols, v);
+        }
     }
 }
 
@@ -248,110 +280,250 @@ struct BackwardParams {
     const float *mean, *rstd;
     void *dx;
     float *partial;  // [2][gridDim.x][cols]: sums of dy*xhat and of dy
-    int param_bf16, vec_out;
+    int param_bf16;
+    int stages;      // of the staged form
 };
 
-// dgamma and dbeta: every thread sums its 16 columns over the block's rows in
-// registers; a block's rows then join in shared memory, and its sums go to
-// its own line of `partial`, which norm_columns_kernel adds up in order.
-template <typename T, bool kVec, int TPR>
-__global__ void __launch_bounds__(block_of<TPR>()) norm_backward_kernel(const BackwardParams p)
+template <int TPR>
+constexpr int backward_block()
 {
-    constexpr int kRowsPerBlock = block_of<TPR>() / TPR;
-    __shared__ float sh[32][3];
-    __shared__ float col[kRowsPerBlock > 1 ? kRowsPerBlock : 1][kRowsPerBlock > 1 ? TPR * kElems : 1];
+    return TPR < kBackThreads ? kBackThreads : TPR;
+}
+
+// 1-D bulk copy of one row into shared memory, completing on `bar`.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(saddr(dst)),
+        "l"(src), "r"(bytes), "r"(saddr(bar))
+        : "memory");
+}
+
+// dgamma and dbeta: every thread sums its columns over the block's rows in
+// registers; the rows that share a block then join in shared memory, and the
+// block's sums go to its own line of `partial`, which norm_columns_kernel
+// adds up in order.
+//
+// Staged (kStaged, for rows of whole chunks): a block's rows of x and dy come
+// into a ring of `stages` shared-memory stages by bulk copies, so that loads
+// are under way while a row waits for its sums. The one barrier per row, that
+// of the sums, comes after every thread has its chunks in registers: behind
+// it the stage is free and is filled again. Registers alone held too little:
+// 16384 x 4096 bf16 took 107 us.
+template <typename T, bool kFull, bool kStaged, int TPR, int NV>
+__global__ void __launch_bounds__(backward_block<TPR>(), backward_block<TPR>() == 256 ? 2 : 1)
+    norm_backward_kernel(const BackwardParams p)
+{
+    constexpr int kSub = backward_block<TPR>() / TPR, kWarps = TPR / 32, V = Chunk<T>::V;
+    __shared__ float2 sh[2][32];
+    __shared__ uint64_t bars[8];
+    extern __shared__ __align__(128) unsigned char dyn[];  // the ring, then the joining of the rows' sums
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
-    using C = Cols<T, kVec>;
-    float gamma[kElems], dg[kElems], db[kElems];
-    load_param<T, kVec, TPR>(p.gamma, p.param_bf16, p.cols, t, gamma);
+    const int warp = threadIdx.x / 32, warp0 = warp / kWarps * kWarps;
+    const uint32_t row_bytes = (uint32_t)p.cols * sizeof(T);
+    const int64_t step = (int64_t)gridDim.x * kSub;
+    const int64_t first = (int64_t)blockIdx.x * kSub;
+
+    auto fill = [&](int stage, int64_t r0) {
+        // thread 0: the rows r0 .. r0 + kSub of x, then of dy
+        const int64_t left = p.rows - r0;
+        const int n = left < kSub ? (int)left : kSub;
+        bar_expect(bars + stage, 2 * n * row_bytes);
+        unsigned char *d = dyn + (size_t)stage * 2 * kSub * row_bytes;
+        for (int i = 0; i < n; i++) {
+            bulk_load(d + i * row_bytes, static_cast<const T *>(p.x) + (r0 + i) * p.ldx, row_bytes, bars + stage);
+            bulk_load(d + (kSub + i) * row_bytes, static_cast<const T *>(p.dy) + (r0 + i) * p.lddy, row_bytes,
+                      bars + stage);
+        }
+    };
+    launch_wait();
+    launch_next();
+    if (kStaged) {
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < p.stages; i++)
+                bar_init(bars + i, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            for (int i = 0; i < p.stages && first + i * step < p.rows; i++)
+                fill(i, first + i * step);
+        }
+        __syncthreads();
+    }
+    float gamma[NV][V], dg[NV][V], db[NV][V];
 #pragma unroll
-    for (int i = 0; i < kElems; i++)
-        dg[i] = db[i] = 0.0f;
+    for (int q = 0; q < NV; q++) {
+        const int col = (q * TPR + t) * V;
+#pragma unroll
+        for (int i = 0; i < V; i++)
+            gamma[q][i] = dg[q][i] = db[q][i] = 0.0f;
+        if (col < p.cols)
+            load_param<V, kFull>(p.gamma, p.param_bf16, col, p.cols, gamma[q]);
+    }
     const float inv = 1.0f / (float)p.cols;
-    for (int64_t r0 = (int64_t)blockIdx.x * kRowsPerBlock; r0 < p.rows; r0 += (int64_t)gridDim.x * kRowsPerBlock) {
+    int phase = 0, stage = 0;
+    uint32_t parity = 0;
+    for (int64_t r0 = first; r0 < p.rows; r0 += step, phase ^= 1) {
         const int64_t r = r0 + sub;
         const bool live = r < p.rows;
-        float x[kElems], g[kElems], mean = 0.0f, rstd = 0.0f;
+        Chunk<T> cx[NV], cy[NV];
+        float mean = 0.0f, rstd = 0.0f;
         if (live) {
             mean = p.mean[r];
             rstd = p.rstd[r];
-            load_row<T, kVec, TPR>(static_cast<const T *>(p.x) + r * p.ldx, p.cols, t, x);
-            load_row<T, kVec, TPR>(static_cast<const T *>(p.dy) + r * p.lddy, p.cols, t, g);
+        }
+        bool ok = true;
+        if (kStaged) {
+            ok = bar_wait(bars + stage, parity);
+            const unsigned char *d = dyn + (size_t)stage * 2 * kSub * row_bytes + sub * row_bytes;
+#pragma unroll
+            for (int q = 0; q < NV; q++) {
+                const uint32_t at = (uint32_t)(q * TPR + t) * 16;
+                const bool in = live && at < row_bytes;
+                cx[q].raw = in ? *reinterpret_cast<const uint4 *>(d + at) : make_uint4(0, 0, 0, 0);
+                cy[q].raw = in ? *reinterpret_cast<const uint4 *>(d + kSub * row_bytes + at) : make_uint4(0, 0, 0, 0);
+            }
         } else {
 #pragma unroll
-            for (int i = 0; i < kElems; i++)
-                x[i] = g[i] = 0.0f;
+            for (int q = 0; q < NV; q++) {
+                cx[q].raw = cy[q].raw = make_uint4(0, 0, 0, 0);
+                if (live) {
+                    load_chunk<T, kFull>(cx[q], static_cast<const T *>(p.x) + r * p.ldx, (q * TPR + t) * V, p.cols);
+                    load_chunk<T, kFull>(cy[q], static_cast<const T *>(p.dy) + r * p.lddy, (q * TPR + t) * V, p.cols);
+                }
+            }
         }
         float a = 0.0f, b = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kElems; i++) {
-            x[i] = C::template at<TPR>(i, t) < p.cols ? (x[i] - mean) * rstd : 0.0f;
-            dg[i] += g[i] * x[i];
-            db[i] += g[i];
-            g[i] *= gamma[i];
-            a += g[i];
-            b += g[i] * x[i];
+        for (int q = 0; q < NV; q++) {
+            float x[V], g[V];
+            cx[q].values(x);
+            cy[q].values(g);
+#pragma unroll
+            for (int i = 0; i < V; i++) {
+                // past the row's end dy and gamma are 0, and so is all that xhat enters
+                const float xh = (x[i] - mean) * rstd, gg = g[i] * gamma[q][i];
+                dg[q][i] = fmaf(g[i], xh, dg[q][i]);
+                db[q][i] += g[i];
+                a += gg;
+                b = fmaf(gg, xh, b);
+            }
         }
-        sum_row<TPR>(a, b, sh);
+        a = warp_sum(a);
+        b = warp_sum(b);
+        if (kWarps > 1 && threadIdx.x % 32 == 0)
+            sh[phase][warp] = make_float2(a, b);
+        if (kStaged) {
+            if (!__syncthreads_and(ok)) {
+                if (threadIdx.x == 0) {
+                    atomicAdd(&g_wait_timeouts, 1ull);
+                    let_copies_land();
+                }
+                __syncthreads();
+                return;
+            }
+            if (threadIdx.x == 0 && r0 + p.stages * step < p.rows)
+                fill(stage, r0 + p.stages * step);
+            if (++stage == p.stages) {
+                stage = 0;
+                parity ^= 1;
+            }
+        } else if (kWarps > 1) {
+            __syncthreads();
+        }
+        if (kWarps > 1) {
+            a = b = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; w++) {
+                const float2 f = sh[phase][warp0 + w];
+                a += f.x;
+                b += f.y;
+            }
+        }
         if (!live)
             continue;
         a *= inv;
         b *= inv;
+        T *dx = static_cast<T *>(p.dx) + r * p.lddx;
 #pragma unroll
-        for (int i = 0; i < kElems; i++)
-            g[i] = rstd * (g[i] - a - x[i] * b);
-        store_row<T, kVec, TPR>(static_cast<T *>(p.dx) + r * p.lddx, p.cols, t, g, p.vec_out);
+        for (int q = 0; q < NV; q++) {
+            const int c = (q * TPR + t) * V;
+            if (c >= p.cols)
+                break;
+            float x[V], g[V];
+            cx[q].keep_packed();
+            cy[q].keep_packed();
+            cx[q].values(x);
+            cy[q].values(g);
+#pragma unroll
+            for (int i = 0; i < V; i++)
+                g[i] = rstd * (g[i] * gamma[q][i] - a - (x[i] - mean) * rstd * b);
+            store_chunk<T, kFull>(dx, c, p.cols, g);
+        }
     }
     float *pg = p.partial + (int64_t)blockIdx.x * p.cols;
     float *pb = pg + (int64_t)gridDim.x * p.cols;
-    if (kRowsPerBlock == 1) {
+    if (kSub == 1) {
 #pragma unroll
-        for (int i = 0; i < kElems; i++) {
-            const int c = C::template at<TPR>(i, t);
-            if (c < p.cols) {
-                pg[c] = dg[i];
-                pb[c] = db[i];
+        for (int q = 0; q < NV; q++)
+#pragma unroll
+            for (int i = 0; i < V; i++) {
+                const int c = (q * TPR + t) * V + i;
+                if (c < p.cols) {
+                    pg[c] = dg[q][i];
+                    pb[c] = db[q][i];
+                }
             }
-        }
     } else {
+        // every copy has landed and been read; [kSub][TPR * NV * V] fp32
+        float *col = reinterpret_cast<float *>(dyn);
+        constexpr int kLine = TPR * NV * V;
         for (int which = 0; which < 2; which++) {
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < kElems; i++)
-                col[sub][C::template at<TPR>(i, t)] = which ? db[i] : dg[i];
+            for (int q = 0; q < NV; q++)
+#pragma unroll
+                for (int i = 0; i < V; i++)
+                    col[sub * kLine + (q * TPR + t) * V + i] = which ? db[q][i] : dg[q][i];
             __syncthreads();
-            for (int c = threadIdx.x; c < p.cols; c += block_of<TPR>()) {
+            for (int c = threadIdx.x; c < p.cols; c += backward_block<TPR>()) {
                 float s = 0.0f;
-                for (int q = 0; q < kRowsPerBlock; q++)
-                    s += col[q][c];
+                for (int q = 0; q < kSub; q++)
+                    s += col[q * kLine + c];
                 (which ? pb : pg)[c] = s;
             }
         }
     }
 }
 
-// Rows wider than 16 x 1024 elements: one block per row, which walks it once
-// for the sum, once for the squares and once for the result.
-__device__ __forceinline__ float block_sum(float a, float (*sh)[3])
+// The widest rows: one block per row, which walks it once for the sum, once
+// for the squares and once for the result.
+__device__ __forceinline__ float block_sum(float v, float *sh)
 {
-    float b = 0.0f;
-    sum_row<kMaxTpr>(a, b, sh);
-    return a;
+    v = warp_sum(v);
+    if (threadIdx.x % 32 == 0)
+        sh[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = 0.0f;
+    for (int i = 0; i < kWide / 32; i++)
+        v += sh[i];
+    __syncthreads();
+    return v;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kMaxTpr) norm_forward_wide_kernel(const ForwardParams p)
+__global__ void __launch_bounds__(kWide, 1) norm_forward_wide_kernel(const ForwardParams p)
 {
-    __shared__ float sh[32][3];
+    __shared__ float sh[kWide / 32];
+    launch_wait();
+    launch_next();
     for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
         const T *x = static_cast<const T *>(p.x) + r * p.ldx;
         T *y = static_cast<T *>(p.y) + r * p.ldy;
         float s = 0.0f;
-        for (int c = threadIdx.x; c < p.cols; c += kMaxTpr)
+        for (int c = threadIdx.x; c < p.cols; c += kWide)
             s += to_f32(x[c]);
         const float mean = block_sum(s, sh) / (float)p.cols;
         s = 0.0f;
-        for (int c = threadIdx.x; c < p.cols; c += kMaxTpr) {
+        for (int c = threadIdx.x; c < p.cols; c += kWide) {
             const float d = to_f32(x[c]) - mean;
             s += d * d;
         }
@@ -360,7 +532,7 @@ __global__ void __launch_bounds__(kMaxTpr) norm_forward_wide_kernel(const Forwar
             p.mean[r] = mean;
             p.rstd[r] = rstd;
         }
-        for (int c = threadIdx.x; c < p.cols; c += kMaxTpr) {
+        for (int c = threadIdx.x; c < p.cols; c += kWide) {
             const float ga = p.param_bf16 ? to_f32(static_cast<const uint16_t *>(p.gamma)[c])
                                           : static_cast<const float *>(p.gamma)[c];
             const float be = !p.beta        ? 0.0f
@@ -372,12 +544,14 @@ __global__ void __launch_bounds__(kMaxTpr) norm_forward_wide_kernel(const Forwar
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kMaxTpr) norm_backward_wide_kernel(const BackwardParams p)
+__global__ void __launch_bounds__(kWide, 1) norm_backward_wide_kernel(const BackwardParams p)
 {
-    __shared__ float sh[32][3];
+    __shared__ float sh[kWide / 32];
+    launch_wait();
+    launch_next();
     float *pg = p.partial + (int64_t)blockIdx.x * p.cols;
     float *pb = pg + (int64_t)gridDim.x * p.cols;
-    for (int c = threadIdx.x; c < p.cols; c += kMaxTpr)
+    for (int c = threadIdx.x; c < p.cols; c += kWide)
         pg[c] = pb[c] = 0.0f;  // each column is one thread's throughout
     for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
         const T *x = static_cast<const T *>(p.x) + r * p.ldx;
@@ -385,7 +559,7 @@ __global__ void __launch_bounds__(kMaxTpr) norm_backward_wide_kernel(const Backw
         T *dx = static_cast<T *>(p.dx) + r * p.lddx;
         const float mean = p.mean[r], rstd = p.rstd[r];
         float a = 0.0f, b = 0.0f;
-        for (int c = threadIdx.x; c < p.cols; c += kMaxTpr) {
+        for (int c = threadIdx.x; c < p.cols; c += kWide) {
             const float xh = (to_f32(x[c]) - mean) * rstd, d = to_f32(dy[c]);
             const float ga = p.param_bf16 ? to_f32(static_cast<const uint16_t *>(p.gamma)[c])
                                           : static_cast<const float *>(p.gamma)[c];
@@ -394,10 +568,9 @@ __global__ void __launch_bounds__(kMaxTpr) norm_backward_wide_kernel(const Backw
             a += d * ga;
             b += d * ga * xh;
         }
-        sum_row<kMaxTpr>(a, b, sh);
-        a /= (float)p.cols;
-        b /= (float)p.cols;
-        for (int c = threadIdx.x; c < p.cols; c += kMaxTpr) {
+        a = block_sum(a, sh) / (float)p.cols;
+        b = block_sum(b, sh) / (float)p.cols;
+        for (int c = threadIdx.x; c < p.cols; c += kWide) {
             const float xh = (to_f32(x[c]) - mean) * rstd, d = to_f32(dy[c]);
             const float ga = p.param_bf16 ? to_f32(static_cast<const uint16_t *>(p.gamma)[c])
                                           : static_cast<const float *>(p.gamma)[c];
@@ -406,29 +579,34 @@ __global__ void __launch_bounds__(kMaxTpr) norm_backward_wide_kernel(const Backw
     }
 }
 
-// dgamma, dbeta: the parts' sums, added in the parts' order. 32 columns and
-// 8 slices of the parts per block.
-__global__ void __launch_bounds__(256) norm_columns_kernel(const float *partial, int parts, int cols, void *dgamma,
-                                                           void *dbeta, int param_bf16)
+// dgamma, dbeta: the parts' sums, added in a fixed order. A block has 32
+// columns and 32 slices of the parts.
+__global__ void __launch_bounds__(1024) norm_columns_kernel(const float *partial, int parts, int cols, void *dgamma,
+                                                            void *dbeta, int param_bf16)
 {
-    __shared__ float sh[8][33];
+    __shared__ float sh[32][33];
+    launch_wait();
+    launch_next();
     const int lane = threadIdx.x % 32, slice = threadIdx.x / 32;
     const int c = blockIdx.x * 32 + lane;
     void *out = blockIdx.y ? dbeta : dgamma;
-    const float *src = partial + (int64_t)blockIdx.y * parts * cols;
+    const float *src = partial + (int64_t)blockIdx.y * parts * cols + c;
     float s = 0.0f;
-    if (c < cols)
-        for (int q = slice; q < parts; q += 8)
-            s += src[(int64_t)q * cols + c];
+    if (c < cols) {
+#pragma unroll 8
+        for (int q = slice; q < parts; q += 32)
+            s += src[(int64_t)q * cols];
+    }
     sh[slice][lane] = s;
     __syncthreads();
-    if (slice == 0 && c < cols) {
-        for (int q = 1; q < 8; q++)
-            s += sh[q][lane];
+    // warp w sums column w's slices
+    s = warp_sum(sh[lane][slice]);
+    const int w = blockIdx.x * 32 + slice;
+    if (lane == 0 && w < cols) {
         if (param_bf16)
-            from_f32(static_cast<uint16_t *>(out)[c], s);
+            from_f32(static_cast<uint16_t *>(out)[w], s);
         else
-            static_cast<float *>(out)[c] = s;
+            static_cast<float *>(out)[w] = s;
     }
 }
 
@@ -437,72 +615,121 @@ bool vec_ok(const void *p, int64_t ld, int64_t size)
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * size) % 16 == 0;
 }
 
-int tpr_for(int64_t cols)
+// The shape of a kernel: threads per row and chunks per thread. Calls
+// f.template run<T, kFull, TPR, NV>(); false if no shape holds the row.
+template <typename T, bool kFull, class F>
+bool forward_shape(int64_t rows, int64_t cols, int sms, F f)
 {
-    int t = 32;
-    while ((int64_t)t * kElems < cols && t < kMaxTpr)
-        t *= 2;
-    return t;
-}
-
-fsdp_status launched(const char *what)
-{
-    const cudaError_t err = cudaGetLastError();
-    return err == cudaSuccess ? FSDP_OK
-                              : set_error(FSDP_ECUDA, "%s launch failed: %s", what, cudaGetErrorString(err));
-}
-
-// Calls f.template run<T, kVec, TPR>() for the types and widths given.
-template <class F>
-void with_shape(fsdp_dtype dt, bool vec, int tpr, F f)
-{
-    auto width = [&](auto type, auto v) {
-        using T = decltype(type);
-        constexpr bool kVec = decltype(v)::value;
-        switch (tpr) {
-        case 32: f.template run<T, kVec, 32>(); break;
-        case 64: f.template run<T, kVec, 64>(); break;
-        case 128: f.template run<T, kVec, 128>(); break;
-        case 256: f.template run<T, kVec, 256>(); break;
-        case 512: f.template run<T, kVec, 512>(); break;
-        default: f.template run<T, kVec, 1024>(); break;
-        }
-    };
-    if (dt == FSDP_BF16)
-        vec ? width(uint16_t{}, std::true_type{}) : width(uint16_t{}, std::false_type{});
+    const int64_t chunks = (cols + Chunk<T>::V - 1) / Chunk<T>::V;
+    // 4 chunks a thread where the rows fill the multiprocessors; with few rows
+    // their latency counts, and a thread has one chunk.
+    if (chunks <= 32)
+        f.template run<T, kFull, 32, 1>();
+    else if (chunks <= 32 * 4 && rows >= 4 * sms)
+        f.template run<T, kFull, 32, 4>();
+    else if (chunks <= 128)
+        f.template run<T, kFull, 128, 1>();
+    else if (chunks <= 128 * 4 && rows >= 4 * sms)
+        f.template run<T, kFull, 128, 4>();
+    else if (chunks <= 512)
+        f.template run<T, kFull, 512, 1>();
+    else if (chunks <= 512 * 2)
+        f.template run<T, kFull, 512, 2>();
+    else if (chunks <= 512 * 4)
+        f.template run<T, kFull, 512, 4>();
+    else if (chunks <= 512 * 8)
+        f.template run<T, kFull, 512, 8>();
     else
-        vec ? width(float{}, std::true_type{}) : width(float{}, std::false_type{});
+        return false;
+    return true;
+}
+
+// The backward pass keeps 3 fp32 numbers per column and thread: 16 columns a
+// thread, 32 where the block would be larger than 512 threads. Returns the
+// rows that a block takes at a time, 0 if no shape holds the row.
+template <typename T, bool kFull, class F>
+int backward_shape(int64_t cols, F f)
+{
+    constexpr int NV = sizeof(T) == 2 ? 2 : 4;
+    if (cols <= 32 * 16)
+        return f.template run<T, kFull, 32, NV>(), 8;
+    if (cols <= 64 * 16)
+        return f.template run<T, kFull, 64, NV>(), 4;
+    if (cols <= 128 * 16)
+        return f.template run<T, kFull, 128, NV>(), 2;
+    if (cols <= 256 * 16)
+        return f.template run<T, kFull, 256, NV>(), 1;
+    if (cols <= 512 * 16)
+        return f.template run<T, kFull, 512, NV>(), 1;
+    if (cols <= 512 * 32)
+        return f.template run<T, kFull, 512, 2 * NV>(), 1;
+    return 0;
 }
 
 struct Forward {
     const ForwardParams &p;
     int sms;
     cudaStream_t s;
-    template <typename T, bool kVec, int TPR>
+    fsdp_status *st;
+    template <typename T, bool kFull, int TPR, int NV>
     void run()
     {
-        const int64_t blocks = (p.rows + block_of<TPR>() / TPR - 1) / (block_of<TPR>() / TPR);
-        const int64_t most = (int64_t)sms * (2048 / block_of<TPR>());
-        norm_forward_kernel<T, kVec, TPR>
-            <<<(unsigned)(blocks < most ? blocks : most), block_of<TPR>(), 0, s>>>(p);
-    }
-};
-struct Backward {
-    const BackwardParams &p;
-    int parts;
-    cudaStream_t s;
-    template <typename T, bool kVec, int TPR>
-    void run()
-    {
-        norm_backward_kernel<T, kVec, TPR><<<parts, block_of<TPR>(), 0, s>>>(p);
+        constexpr int kBlock = forward_block<TPR>(), kRows = kBlock / TPR;
+        const int64_t blocks = (p.rows + kRows - 1) / kRows, most = (int64_t)sms * (2048 / kBlock);
+        *st = launch("layer_norm", norm_forward_kernel<T, kFull, TPR, NV>, (unsigned)(blocks < most ? blocks : most),
+                     kBlock, 0, s, 1, p);
     }
 };
 
+// Shared memory of a block's stages: two blocks of 256 threads share a
+// multiprocessor, one of 512 has it alone.
+constexpr int kStageBudget = 96 * 1024;
+constexpr int kMaxStages = 6;
+
+struct Backward {
+    BackwardParams &p;
+    int parts;
+    cudaStream_t s;
+    fsdp_status *st;
+    template <typename T, bool kFull, int TPR, int NV>
+    void run()
+    {
+        constexpr int kBlock = backward_block<TPR>(), kSub = kBlock / TPR;
+        constexpr int kJoin = kSub > 1 ? kSub * TPR * NV * Chunk<T>::V * 4 : 0;
+        constexpr int kBudget = kStageBudget * (kBlock / kBackThreads);
+        const int stage = 2 * kSub * p.cols * (int)sizeof(T);
+        p.stages = kBudget / stage < kMaxStages ? kBudget / stage : kMaxStages;
+        if (kFull && p.stages >= 2) {
+            auto kernel = norm_backward_kernel<T, kFull, kFull, TPR, NV>;
+            const int smem = p.stages * stage > kJoin ? p.stages * stage : kJoin;
+            if (smem > 48 * 1024) {
+                const cudaError_t err =
+                    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBudget);
+                if (err != cudaSuccess) {
+                    *st = set_error(FSDP_ECUDA, "layer_norm_backward: cudaFuncSetAttribute: %s", cudaGetErrorString(err));
+                    return;
+                }
+            }
+            *st = launch("layer_norm_backward", kernel, parts, kBlock, smem, s, 1, p);
+        } else {
+            *st = launch("layer_norm_backward", norm_backward_kernel<T, kFull, false, TPR, NV>, parts, kBlock, kJoin, s,
+                         1, p);
+        }
+    }
+};
+struct Nothing {
+    template <typename T, bool kFull, int TPR, int NV>
+    void run()
+    {
+    }
+};
+
+// Blocks of the backward pass, each with a line of partial sums: two per
+// multiprocessor of a GB300, fewer where there are not so many rows.
 int64_t backward_parts(int64_t rows, int64_t cols)
 {
-    const int tpr = tpr_for(cols);
-    const int per = tpr < kMinThreads ? kMinThreads / tpr : 1;
-    const int64_t blocks = (rows + per - 1) / per;
+    const int per = backward_shape<float, true>(cols, Nothing{});
+    const int64_t blocks = per ? (rows + per - 1) / per : rows;
     const int64_t most = 152 * 2;
     return blocks < 1 ? 1 : blocks < most ? blocks : most;
 }
@@ -516,49 +743,52 @@ int64_t norm_backward_workspace(int64_t rows, int64_t cols)
 
 fsdp_status launch_layer_norm(const NormArgs &a, int dev, void *stream)
 {
-    if (a.rows == 0)
-        return FSDP_OK;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int64_t size = a.dtype == FSDP_BF16 ? 2 : 4;
-    ForwardParams p{a.rows, a.ldx, a.ldy, (int)a.cols, a.x, a.gamma, a.beta, a.y, a.mean, a.rstd, a.eps,
-                    a.param_dtype == FSDP_BF16, vec_ok(a.y, a.ldy, size)};
+    const bool bf16 = a.dtype == FSDP_BF16;
+    const int64_t size = bf16 ? 2 : 4;
+    ForwardParams p{a.rows, a.ldx,  a.ldy,  (int)a.cols, a.x, a.gamma, a.beta, a.y, a.mean, a.rstd, a.eps,
+                    a.param_dtype == FSDP_BF16};
     const int sms = device_sms(dev);
-    if (a.cols > kElems * kMaxTpr) {
+    fsdp_status st = FSDP_OK;
+    const Forward f{p, sms, s, &st};
+    const bool full = vec_ok(a.x, a.ldx, size) && vec_ok(a.y, a.ldy, size) && vec_ok(a.gamma, a.cols, size) &&
+                      vec_ok(a.beta, 0, 1);
+    const bool held = bf16 ? (full ? forward_shape<uint16_t, true>(a.rows, a.cols, sms, f)
+                                   : forward_shape<uint16_t, false>(a.rows, a.cols, sms, f))
+                           : (full ? forward_shape<float, true>(a.rows, a.cols, sms, f)
+                                   : forward_shape<float, false>(a.rows, a.cols, sms, f));
+    if (!held) {
         const unsigned grid = (unsigned)(a.rows < 2 * sms ? a.rows : 2 * sms);
-        if (a.dtype == FSDP_BF16)
-            norm_forward_wide_kernel<uint16_t><<<grid, kMaxTpr, 0, s>>>(p);
-        else
-            norm_forward_wide_kernel<float><<<grid, kMaxTpr, 0, s>>>(p);
-    } else {
-        with_shape(a.dtype, vec_ok(a.x, a.ldx, size), tpr_for(a.cols), Forward{p, sms, s});
+        st = launch("layer_norm", bf16 ? norm_forward_wide_kernel<uint16_t> : norm_forward_wide_kernel<float>, grid, kWide,
+                    0, s, 1, p);
     }
-    return launched("layer_norm");
+    return st;
 }
 
 fsdp_status launch_layer_norm_backward(const NormArgs &a, int dev, void *stream)
 {
     (void)dev;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int64_t size = a.dtype == FSDP_BF16 ? 2 : 4;
+    const bool bf16 = a.dtype == FSDP_BF16;
+    const int64_t size = bf16 ? 2 : 4;
     const int parts = (int)backward_parts(a.rows, a.cols);
     BackwardParams p{a.rows,  a.lddy,    a.ldx,  a.lddx, (int)a.cols, a.dy, a.x, a.gamma, a.mean_in, a.rstd_in,
-                     a.dx, a.partial, a.param_dtype == FSDP_BF16, vec_ok(a.dx, a.lddx, size)};
-    if (a.cols > kElems * kMaxTpr) {
-        if (a.dtype == FSDP_BF16)
-            norm_backward_wide_kernel<uint16_t><<<parts, kMaxTpr, 0, s>>>(p);
-        else
-            norm_backward_wide_kernel<float><<<parts, kMaxTpr, 0, s>>>(p);
-    } else {
-        with_shape(a.dtype, vec_ok(a.x, a.ldx, size) && vec_ok(a.dy, a.lddy, size), tpr_for(a.cols),
-                   Backward{p, parts, s});
-    }
-    fsdp_status st = launched("layer_norm_backward");
+                     a.dx, a.partial, a.param_dtype == FSDP_BF16, 0};
+    fsdp_status st = FSDP_OK;
+    const Backward f{p, parts, s, &st};
+    const bool full = vec_ok(a.x, a.ldx, size) && vec_ok(a.dy, a.lddy, size) && vec_ok(a.dx, a.lddx, size) &&
+                      vec_ok(a.gamma, a.cols, size);
+    const int held = bf16 ? (full ? backward_shape<uint16_t, true>(a.cols, f) : backward_shape<uint16_t, false>(a.cols, f))
+                          : (full ? backward_shape<float, true>(a.cols, f) : backward_shape<float, false>(a.cols, f));
+    if (!held)
+        st = launch("layer_norm_backward", bf16 ? norm_backward_wide_kernel<uint16_t> : norm_backward_wide_kernel<float>,
+                    parts, kWide, 0, s, 1, p);
     if (st != FSDP_OK)
         return st;
-    const dim3 grid((unsigned)((a.cols + 31) / 32), a.dbeta ? 2 : 1);
-    norm_columns_kernel<<<grid, 256, 0, s>>>(a.partial, parts, (int)a.cols, a.dgamma, a.dbeta,
-                                             a.param_dtype == FSDP_BF16);
-    return launched("layer_norm_backward (columns)");
+    return launch("layer_norm_backward (columns)", norm_columns_kernel, dim3((unsigned)((a.cols + 31) / 32), a.dbeta ? 2 : 1),
+                  1024, 0, s, 1, a.partial, parts, a.cols, a.dgamma, a.dbeta, a.param_dtype == FSDP_BF16);
 }
+
+cudaError_t norm_wait_timeouts(unsigned long long *n) { return wait::wait_timeouts(n); }
 
 }  // namespace fsdp

@@ -13,6 +13,7 @@
 
 namespace fsdp {
 
+cudaError_t norm_wait_timeouts(unsigned long long *n);
 cudaError_t loss_wait_timeouts(unsigned long long *n);
 cudaError_t muon_wait_timeouts(unsigned long long *n);
 
@@ -473,17 +474,19 @@ fsdp_status fsdp_ops_wait_timeouts(int device, uint64_t *count)
         return set_error(FSDP_ECUDA, "%s: cudaGetDevice: %s", fn, cudaGetErrorString(err));
     if (prev != device && (err = cudaSetDevice(device)) != cudaSuccess)
         return set_error(FSDP_ECUDA, "%s: cudaSetDevice(%d): %s", fn, device, cudaGetErrorString(err));
-    unsigned long long a = 0, b = 0;
+    unsigned long long n[3] = {0, 0, 0};
     err = cudaDeviceSynchronize();
     if (err == cudaSuccess)
-        err = loss_wait_timeouts(&a);
+        err = norm_wait_timeouts(&n[0]);
     if (err == cudaSuccess)
-        err = muon_wait_timeouts(&b);
+        err = loss_wait_timeouts(&n[1]);
+    if (err == cudaSuccess)
+        err = muon_wait_timeouts(&n[2]);
     if (prev != device)
         cudaSetDevice(prev);
     if (err != cudaSuccess)
         return set_error(FSDP_ECUDA, "%s: %s", fn, cudaGetErrorString(err));
-    *count = a + b;
+    *count = n[0] + n[1] + n[2];
     return FSDP_OK;
 }
 

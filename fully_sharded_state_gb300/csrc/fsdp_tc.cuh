@@ -11,7 +11,10 @@
 //             tensor memory, double-buffered
 //   warps 4.. eight epilogue warps read the finished accumulator (a thread
 //             holds one row of the tile, TN / 2 columns of it) while the next
-//             tile is being multiplied
+//             tile is being multiplied. What they read and write in memory
+//             goes through 4 KB of shared memory per warp, so that lanes
+//             touch whole lines of a row; with each lane on a row of its own,
+//             a 512 x 512 update spent 17 us per tile on its accesses
 // The grid is persistent. An operand may be stored with K adjacent
 // (row-major [rows, K]) or with its rows adjacent ([K, rows], "MN-major"),
 // which the descriptors express; nothing is transposed in memory.
@@ -29,68 +32,20 @@
 #include <cstdint>
 
 #include "fsdp_ops_internal.h"
+#include "fsdp_launch.cuh"
+#include "fsdp_wait.cuh"
 
 namespace fsdp {
 namespace tc {
 namespace {
 
+using namespace wait;
+
 constexpr int kBK = 64;        // K elements of a stage: 128 bytes, one swizzle row
 constexpr int kTM = 128;       // rows of a CTA's tile: the lanes of tensor memory
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
-constexpr uint64_t kWaitNs = 2000000000ull;
 
-__device__ unsigned long long g_wait_timeouts;
-
-// ------------------------------------------------------------- barriers ----
-
-__device__ __forceinline__ uint32_t saddr(const void *p)
-{
-    return (uint32_t)__cvta_generic_to_shared(p);
-}
-__device__ __forceinline__ void bar_init(uint64_t *bar, uint32_t count)
-{
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(saddr(bar)), "r"(count) : "memory");
-}
-__device__ __forceinline__ bool bar_try(uint64_t *bar, uint32_t parity)
-{
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(saddr(bar)), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-__device__ __forceinline__ uint64_t now_ns()
-{
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-// Waits for the phase of `parity` at most kWaitNs (and 2^27 polls, should the
-// timer stand still); false if it gave up.
-__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity)
-{
-    if (bar_try(bar, parity))
-        return true;
-    const uint64_t t0 = now_ns();
-    for (uint32_t round = 0; round < (1u << 22); round++) {
-        for (int k = 0; k < 32; k++)
-            if (bar_try(bar, parity))
-                return true;
-        if (now_ns() - t0 > kWaitNs)
-            return false;
-    }
-    return false;
-}
-__device__ __forceinline__ void bar_expect(uint64_t *bar, uint32_t bytes)
-{
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(saddr(bar)), "r"(bytes)
-                 : "memory");
-}
 // One arrival on the barrier at the same place in CTA `rank` of the cluster.
 __device__ __forceinline__ void bar_arrive_at(uint64_t *bar, uint32_t rank)
 {
@@ -240,7 +195,7 @@ struct Shape {
     int batch;        // matrices, on the maps' third axis
     int splits;       // parts of K, each its own tile (its results are partial sums)
     int split_blocks; // K blocks of a part
-    int sym;          // only the 256-squares on and above the diagonal (M = N)
+    int sym;          // only the squares on and above the diagonal (M = N)
     int group;        // row tiles that are walked together, for reuse in L2
     uint32_t idesc;
     const int *dyn;   // NULL, or a device count that limits M or K:
@@ -257,7 +212,7 @@ struct Work {
 template <int kCtas, int TN>
 struct Tiles {
     static constexpr int kRows = kTM * kCtas;
-    static constexpr int kSquare = 256;  // of sym
+    static constexpr int kSquare = kRows > TN ? kRows : TN;  // of sym
     int m_tiles, n_tiles, M, K;
     int64_t per_z, total;
 
@@ -322,6 +277,8 @@ struct Tiles {
 struct Slot {
     int z, split, row, col, M, N;
     uint32_t tmem;
+    unsigned char *stage;  // the warp's 4 KB: 32 rows of 128 bytes
+    int lane;
     bool mirror;  // sym: also store the transposed element
     bool empty;   // K was empty: the accumulator holds nothing, the sum is 0
 
@@ -335,6 +292,52 @@ struct Slot {
                 v[i] = 0.0f;
         }
     }
+
+    // 16-byte piece c (0..7) of line r (0..31) of the stage. Pieces of a line
+    // are permuted by its number: eight lanes on one piece of eight lines, and
+    // eight lanes on the pieces of one line, both touch every bank once.
+    __device__ __forceinline__ uint4 *piece(int r, int c) const
+    {
+        return reinterpret_cast<uint4 *>(stage + r * 128 + ((c ^ (r & 7)) << 4));
+    }
+
+    // Calls f(r, c, v) for the 32 x 32 values of a chunk, 4 at a time, a row's
+    // 8 groups on 8 adjacent lanes: row `row - lane + r`, columns from
+    // col + 32 * chunk + c on. Rows and columns past the matrix are included.
+    // What f leaves in v is back in `mine` (the thread's own row) after it,
+    // where kBack is set.
+    template <bool kBack, class F>
+    __device__ __forceinline__ void across(int chunk, float (&mine)[32], F f) const
+    {
+        load(chunk, mine);
+#pragma unroll
+        for (int c = 0; c < 8; c++)
+            *piece(lane, c) = make_uint4(__float_as_uint(mine[4 * c]), __float_as_uint(mine[4 * c + 1]),
+                                         __float_as_uint(mine[4 * c + 2]), __float_as_uint(mine[4 * c + 3]));
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const int r = i * 4 + lane / 8;
+            const uint4 u = *piece(r, lane % 8);
+            float v[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
+            f(r, lane % 8 * 4, v);
+            if (kBack)
+                *piece(r, lane % 8) = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                                 __float_as_uint(v[3]));
+        }
+        __syncwarp();
+        if (kBack) {
+#pragma unroll
+            for (int c = 0; c < 8; c++) {
+                const uint4 u = *piece(lane, c);
+                mine[4 * c] = __uint_as_float(u.x);
+                mine[4 * c + 1] = __uint_as_float(u.y);
+                mine[4 * c + 2] = __uint_as_float(u.z);
+                mine[4 * c + 3] = __uint_as_float(u.w);
+            }
+            __syncwarp();
+        }
+    }
 };
 
 template <int kCtas, int TN>
@@ -343,11 +346,14 @@ struct Ring {
     static constexpr int kBytesA = kTM * kBK * 2;
     static constexpr int kBytesB = kRowsB * kBK * 2;
     static constexpr int kStageBytes = kBytesA + kBytesB;
-    static constexpr int kFit = 196 * 1024 / kStageBytes;
+    static constexpr int kFit = 192 * 1024 / kStageBytes;
     static constexpr int kStages = kFit < 8 ? kFit : 8;
     static constexpr int kBarriers = 2 * kStages + 4;
-    // 1024 bytes for the swizzle's alignment, the barriers, the TMEM address
-    static constexpr int kSmem = 1024 + kStages * kStageBytes + kBarriers * 8 + 16;
+    static constexpr int kEpiBytes = kEpiWarps * 4096;
+    // 1024 bytes for the swizzle's alignment, the epilogue's stages, the
+    // barriers and the TMEM address
+    static constexpr int kSmem = 1024 + kStages * kStageBytes + kEpiBytes + kBarriers * 8 + 16;
+    static_assert(kSmem <= 227 * 1024, "shared memory of a block");
 };
 
 template <int kCtas, int TN, bool kAMN, bool kBMN, class Epi>
@@ -360,7 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the same offset in both CTAs of a pair: dynamic shared memory starts at
     // one address in every CTA
     unsigned char *ring = raw + ((1024 - (saddr(raw) & 1023)) & 1023);
-    uint64_t *full = reinterpret_cast<uint64_t *>(ring + R::kStages * R::kStageBytes);
+    unsigned char *epi = ring + R::kStages * R::kStageBytes;
+    uint64_t *full = reinterpret_cast<uint64_t *>(epi + R::kEpiBytes);
     uint64_t *empty = full + R::kStages;
     uint64_t *acc_full = empty + R::kStages;
     uint64_t *acc_empty = acc_full + 2;
@@ -368,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = kCtas == 2 ? cluster_rank() : 0;
-    const Tiles<kCtas, TN> tiles(s);
+    using T = Tiles<kCtas, TN>;
     const int64_t first = blockIdx.x / kCtas, step = gridDim.x / kCtas;
 
     if (warp == 2)
@@ -392,6 +399,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_after();
     const uint32_t tmem = *tmem_at;
     bool ok = true;
+    // what follows reads the launches before this one's results
+    launch_wait();
+    launch_next();
+    const T tiles(s);
 
     if (warp == 0) {
         if (lane == 0) {
@@ -425,12 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (!ok) {
-                // copies may be in flight: give them time before the block ends
-                const uint64_t t0 = now_ns();
-                for (int i = 0; i < (1 << 20) && now_ns() - t0 < 10000000ull; i++)
-                    __nanosleep(1000);
-            }
+            if (!ok)
+                let_copies_land();
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
@@ -483,8 +490,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             x.col = w.col + half * (TN / 2);
             x.M = tiles.M;
             x.N = s.N;
+            x.lane = lane;
+            x.stage = epi + (warp - 4) * 4096;
             x.tmem = tmem + acc * TN + half * (TN / 2) + ((uint32_t)(quarter * 32) << 16);
-            x.mirror = s.sym && w.row / 256 != w.col / 256;
+            x.mirror = s.sym && w.row / T::kSquare != w.col / T::kSquare;
             x.empty = w.nkb == 0;
             Epi::template run<TN / 2>(ep, x);
             fence_before();
@@ -559,11 +568,9 @@ inline fsdp_status make_map(CUtensorMap *map, const Operand &o, int batch, int b
     return FSDP_OK;
 }
 
-// Launches D = A B^T. `s` needs M, N, K, batch, sym, dyn* and, for split
-// sums, splits and split_blocks; the rest is filled in here.
 template <int kCtas, int TN, bool kAMN, bool kBMN, class Epi>
-fsdp_status product(Shape s, const Operand &a, const Operand &b, bool bf16, const typename Epi::Params &ep,
-                    int dev, cudaStream_t stream, const char *what)
+fsdp_status product_as(Shape s, const Operand &a, const Operand &b, bool bf16, const typename Epi::Params &ep,
+                       int64_t tiles, int dev, cudaStream_t stream, const char *what)
 {
     using R = Ring<kCtas, TN>;
     auto kernel = product_kernel<kCtas, TN, kAMN, kBMN, Epi>;
@@ -582,44 +589,72 @@ fsdp_status product(Shape s, const Operand &a, const Operand &b, bool bf16, cons
         st = make_map(&mb, b, s.batch, kBMN ? kBK : R::kRowsB, bf16);
     if (st != FSDP_OK)
         return st;
-    if (s.splits < 1)
-        s.splits = 1;
-    if (s.splits == 1)
-        s.split_blocks = (s.K + kBK - 1) / kBK;
-    s.group = s.group > 0 ? s.group : 8;
     // D fp32; A, B bf16 (1) or fp16 (0); majors; N / 8; M / 16
     s.idesc = (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((kAMN ? 1u : 0u) << 15) |
               ((kBMN ? 1u : 0u) << 16) | ((uint32_t)(TN / 8) << 17) | ((uint32_t)(kTM * kCtas / 16) << 24);
-    const int64_t mt = (s.M + kTM * kCtas - 1) / (kTM * kCtas), nt = (s.N + TN - 1) / TN;
-    int64_t total = mt * nt;
-    if (s.sym) {
-        const int64_t q = (s.M + 255) / 256;
-        total = q * (q + 1) / 2 * (256 / (kTM * kCtas)) * (256 / TN);
-    }
-    total *= (int64_t)s.batch * s.splits;
     const int64_t most = device_sms(dev) / kCtas;
-    if (total < 1)
-        return FSDP_OK;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((total < most ? total : most) * kCtas));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = R::kSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = kCtas;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = kCtas == 2 ? 1 : 0;
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, ma, mb, s, ep);
-    if (err != cudaSuccess)
-        return set_error(FSDP_ECUDA, "%s launch failed: %s", what, cudaGetErrorString(err));
-    return FSDP_OK;
+    return launch(what, kernel, dim3((unsigned)((tiles < most ? tiles : most) * kCtas)), kThreads, R::kSmem, stream,
+                  kCtas, ma, mb, s, ep);
 }
 
-inline cudaError_t wait_timeouts(unsigned long long *n)
+// Output tiles of rows x cols, over the batch and the parts of K.
+inline int64_t count_tiles(const Shape &s, int64_t rows, int64_t cols)
 {
-    return cudaMemcpyFromSymbol(n, g_wait_timeouts, sizeof *n);
+    int64_t n = ((s.M + rows - 1) / rows) * ((s.N + cols - 1) / cols);
+    if (s.sym) {
+        const int64_t square = rows > cols ? rows : cols, q = (s.M + square - 1) / square;
+        n = q * (q + 1) / 2 * (square / rows) * (square / cols);
+    }
+    return n * s.batch * s.splits;
+}
+
+// Launches D = A B^T. `s` needs M, N, K, batch, sym, dyn* and, for split
+// sums, splits and split_blocks; the rest is filled in here.
+//
+// The tile: the largest output tile makes the fewest trips to L2 per product,
+// a smaller one spreads a small product over more multiprocessors. Taken is
+// the one with the least estimate of waves * (K blocks * clocks of one + those
+// of a tile's start and end), where a block's clocks are those of its MMAs
+// (2 per column of the tile) or of its loads at 90 bytes per clock.
+template <bool kAMN, bool kBMN, class Epi>
+fsdp_status product(Shape s, const Operand &a, const Operand &b, bool bf16, const typename Epi::Params &ep,
+                    int dev, cudaStream_t stream, const char *what)
+{
+    const int64_t blocks = (s.K + kBK - 1) / kBK;
+    if (s.splits < 1)
+        s.splits = 1;
+    if (s.splits == 1)
+        s.split_blocks = (int)blocks;
+    s.group = s.group > 0 ? s.group : 8;
+    const int64_t sms = device_sms(dev);
+    const int64_t nk = s.split_blocks < blocks ? s.split_blocks : blocks;
+    struct Form {
+        int ctas, tn;
+        int64_t tiles, cost;
+    } forms[4] = {{2, 256, 0, 0}, {1, 256, 0, 0}, {1, 128, 0, 0}, {1, 64, 0, 0}};
+    const Form *best = nullptr;
+    for (Form &f : forms) {
+        if (f.tn < Epi::kLeastTN)
+            continue;
+        f.tiles = count_tiles(s, kTM * f.ctas, f.tn);
+        const int64_t slots = sms / f.ctas, waves = (f.tiles + slots - 1) / slots;
+        const int64_t loads = (kTM + f.tn / f.ctas) * 128 / 90, mmas = 2 * f.tn;
+        f.cost = waves * (nk * (loads > mmas ? loads : mmas) + 1500 + 8 * f.tn);
+        if (!best || f.cost < best->cost)
+            best = &f;
+    }
+    if (best->tiles < 1)
+        return FSDP_OK;
+    if (best->ctas == 2)
+        return product_as<2, 256, kAMN, kBMN, Epi>(s, a, b, bf16, ep, best->tiles, dev, stream, what);
+    if (best->tn == 256)
+        return product_as<1, 256, kAMN, kBMN, Epi>(s, a, b, bf16, ep, best->tiles, dev, stream, what);
+    if constexpr (Epi::kLeastTN <= 64) {
+        if (best->tn == 128)
+            return product_as<1, 128, kAMN, kBMN, Epi>(s, a, b, bf16, ep, best->tiles, dev, stream, what);
+        return product_as<1, 64, kAMN, kBMN, Epi>(s, a, b, bf16, ep, best->tiles, dev, stream, what);
+    }
+    return FSDP_OK;
 }
 
 // ------------------------------------------------- rows of an epilogue ----
@@ -642,67 +677,46 @@ __device__ __forceinline__ bool aligned(const void *p, unsigned bytes)
     return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
 }
 
-// Stores `n` (of 32) values as 16-bit ones at p, in 16-byte pieces where p
-// is aligned.
+// 4 adjacent elements of a row, of which the first n exist; one access where
+// all do and p is aligned.
 template <bool kBf16>
-__device__ __forceinline__ void store16(uint16_t *p, const float (&v)[32], int n)
+__device__ __forceinline__ void put4_16(uint16_t *p, const float (&v)[4], int n)
 {
-    if (n <= 0)
-        return;
-    if (aligned(p, 16)) {
-#pragma unroll
-        for (int g = 0; g < 4; g++) {
-            if (g * 8 + 8 <= n) {
-                uint4 u;
-                uint32_t *w = reinterpret_cast<uint32_t *>(&u);
-#pragma unroll
-                for (int i = 0; i < 4; i++)
-                    w[i] = kBf16 ? pack_bf16(v[g * 8 + 2 * i], v[g * 8 + 2 * i + 1])
-                                 : pack_f16(v[g * 8 + 2 * i], v[g * 8 + 2 * i + 1]);
-                *reinterpret_cast<uint4 *>(p + g * 8) = u;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; i++)
-                    if (g * 8 + i < n)
-                        p[g * 8 + i] = kBf16 ? to_bf16(v[g * 8 + i])
-                                             : __half_as_ushort(__float2half_rn(v[g * 8 + i]));
-            }
-        }
+    if (n >= 4 && aligned(p, 8)) {
+        *reinterpret_cast<uint2 *>(p) = kBf16 ? make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]))
+                                              : make_uint2(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]));
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; i++)
+        for (int i = 0; i < 4; i++)
             if (i < n)
                 p[i] = kBf16 ? to_bf16(v[i]) : __half_as_ushort(__float2half_rn(v[i]));
     }
 }
-
-// fp32 rows, in 16-byte pieces where p is aligned.
-__device__ __forceinline__ void load_f32(const float *p, float (&v)[32], int n)
+__device__ __forceinline__ void get4_f16(const uint16_t *p, float (&v)[4])  // 8-byte aligned
 {
-    if (aligned(p, 16) && n >= 32) {
-#pragma unroll
-        for (int g = 0; g < 8; g++) {
-            const float4 f = reinterpret_cast<const float4 *>(p)[g];
-            v[4 * g] = f.x;
-            v[4 * g + 1] = f.y;
-            v[4 * g + 2] = f.z;
-            v[4 * g + 3] = f.w;
-        }
+    const uint2 u = *reinterpret_cast<const uint2 *>(p);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&u.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&u.y));
+    v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+}
+__device__ __forceinline__ void get4_f32(const float *p, float (&v)[4], int n)
+{
+    if (n >= 4 && aligned(p, 16)) {
+        const float4 f = *reinterpret_cast<const float4 *>(p);
+        v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; i++)
+        for (int i = 0; i < 4; i++)
             v[i] = i < n ? p[i] : 0.0f;
     }
 }
-__device__ __forceinline__ void store_f32(float *p, const float (&v)[32], int n)
+__device__ __forceinline__ void put4_f32(float *p, const float (&v)[4], int n)
 {
-    if (aligned(p, 16) && n >= 32) {
-#pragma unroll
-        for (int g = 0; g < 8; g++)
-            reinterpret_cast<float4 *>(p)[g] = make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
+    if (n >= 4 && aligned(p, 16)) {
+        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; i++)
+        for (int i = 0; i < 4; i++)
             if (i < n)
                 p[i] = v[i];
     }

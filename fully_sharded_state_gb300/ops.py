@@ -25,45 +25,60 @@ from .capi import FsdpArgumentError
 
 _vp, _i64 = ctypes.c_void_p, ctypes.c_int64
 _DT = {torch.bfloat16: capi.FSDP_BF16, torch.float32: capi.FSDP_F32}
+_SAME = nullcontext()
 NEWTON_SCHULZ_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
 
 
-def _need(ok, message):
-    if not ok:
-        raise FsdpArgumentError(message)
+def _refuse(message):
+    raise FsdpArgumentError(message)
 
 
 def _matrix(t, name, rows=None, cols=None, dtype=None, device=None):
     """Checks a 2-D tensor; returns its row stride."""
-    _need(isinstance(t, torch.Tensor) and t.is_cuda, f"{name} is not a CUDA tensor")
-    _need(t.dim() == 2, f"{name} has {t.dim()} dimensions, needs 2")
-    _need(device is None or t.device == device, f"{name} is on {t.device}, other tensors on {device}")
-    _need(dtype is None or t.dtype == dtype, f"{name} has dtype {t.dtype}, needs {dtype}")
-    r, c = t.shape
-    _need((rows is None or r == rows) and (cols is None or c == cols),
-          f"{name} has shape {tuple(t.shape)}, needs ({'any' if rows is None else rows}, "
-          f"{'any' if cols is None else cols})")
-    s0, s1 = t.stride()
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        _refuse(f"{name} is not a CUDA tensor")
+    shape = t.shape
+    if len(shape) != 2:
+        _refuse(f"{name} has {len(shape)} dimensions, needs 2")
+    if device is not None and t.device != device:
+        _refuse(f"{name} is on {t.device}, other tensors on {device}")
+    if dtype is not None and t.dtype != dtype:
+        _refuse(f"{name} has dtype {t.dtype}, needs {dtype}")
+    r, c = shape
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        _refuse(f"{name} has shape {tuple(shape)}, needs ({'any' if rows is None else rows}, "
+                f"{'any' if cols is None else cols})")
     if r == 0 or c == 0:
         return c
-    _need(s1 == 1 or c == 1, f"{name}: the elements of a row are not adjacent")
-    _need(r == 1 or s0 >= c, f"{name}: its rows overlap")
-    return s0 if r > 1 else c
+    s0, s1 = t.stride()
+    if s1 != 1 and c != 1:
+        _refuse(f"{name}: the elements of a row are not adjacent")
+    if r == 1:
+        return c
+    if s0 < c:
+        _refuse(f"{name}: its rows overlap")
+    return s0
 
 
 def _vector(t, name, n, dtype, device):
-    _need(isinstance(t, torch.Tensor) and t.is_cuda, f"{name} is not a CUDA tensor")
-    _need(t.device == device, f"{name} is on {t.device}, other tensors on {device}")
-    _need(t.dim() == 1 and t.shape[0] == n, f"{name} has shape {tuple(t.shape)}, needs ({n},)")
-    _need(t.dtype == dtype, f"{name} has dtype {t.dtype}, needs {dtype}")
-    _need(n <= 1 or t.stride(0) == 1, f"{name} is not contiguous")
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        _refuse(f"{name} is not a CUDA tensor")
+    if t.device != device:
+        _refuse(f"{name} is on {t.device}, other tensors on {device}")
+    shape = t.shape
+    if len(shape) != 1 or shape[0] != n:
+        _refuse(f"{name} has shape {tuple(shape)}, needs ({n},)")
+    if t.dtype != dtype:
+        _refuse(f"{name} has dtype {t.dtype}, needs {dtype}")
+    if n > 1 and t.stride(0) != 1:
+        _refuse(f"{name} is not contiguous")
     return t.data_ptr()
 
 
 def _on(stream, device):
     """The stream's handle, and the context in which memory is allocated for it."""
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream, nullcontext()
+        return torch.cuda.current_stream(device).cuda_stream, _SAME
     return stream.cuda_stream, torch.cuda.stream(stream)
 
 
@@ -81,9 +96,12 @@ def _ptr(t):
 
 def _norm_inputs(x, gamma):
     ldx = _matrix(x, "x")
-    _need(x.dtype in _DT, f"x has dtype {x.dtype}, needs bfloat16 or float32")
-    _need(x.shape[1] > 0, "x has no columns")
-    _need(isinstance(gamma, torch.Tensor) and gamma.dtype in _DT, "gamma needs dtype bfloat16 or float32")
+    if not (x.dtype in _DT):
+        _refuse(f"x has dtype {x.dtype}, needs bfloat16 or float32")
+    if not (x.shape[1] > 0):
+        _refuse("x has no columns")
+    if not (isinstance(gamma, torch.Tensor) and gamma.dtype in _DT):
+        _refuse("gamma needs dtype bfloat16 or float32")
     _vector(gamma, "gamma", x.shape[1], gamma.dtype, x.device)
     return ldx
 
@@ -100,12 +118,11 @@ def layer_norm(x, gamma, beta=None, eps: float = 1e-5, out=None, stream=None):
     handle, ctx = _on(stream, x.device)
     with ctx:
         y = torch.empty_like(x, memory_format=torch.contiguous_format) if out is None else out
-        stats = torch.empty((2, rows), dtype=torch.float32, device=x.device)
+        mean, rstd = torch.empty((2, rows), dtype=torch.float32, device=x.device).unbind(0)
     ldy = _matrix(y, "out", rows, cols, x.dtype, x.device)
-    mean, rstd = stats[0], stats[1]
     capi._check(lib.fsdp_layer_norm(rows, cols, x.data_ptr(), ldx, _DT[x.dtype], gamma.data_ptr(), _ptr(beta),
-                                    _DT[gamma.dtype], eps, y.data_ptr(), ldy, stats.data_ptr(),
-                                    stats.data_ptr() + 4 * rows, handle))
+                                    _DT[gamma.dtype], eps, y.data_ptr(), ldy, mean.data_ptr(),
+                                    rstd.data_ptr(), handle))
     return y, mean, rstd
 
 
@@ -130,7 +147,8 @@ def layer_norm_backward(dy, x, gamma, mean, rstd, with_beta: bool = True, dx=Non
         if with_beta and dbeta is None:
             dbeta = torch.empty(cols, dtype=gamma.dtype, device=dev)
         ws, nws = _workspace(lib.fsdp_layer_norm_backward_workspace, rows, cols, device=dev)
-    _need(with_beta or dbeta is None, "dbeta is given, but with_beta is false")
+    if not (with_beta or dbeta is None):
+        _refuse("dbeta is given, but with_beta is false")
     lddx = _matrix(dx, "dx", rows, cols, x.dtype, dev)
     _vector(dgamma, "dgamma", cols, gamma.dtype, dev)
     if dbeta is not None:
@@ -151,8 +169,10 @@ def _loss_call(hidden, weight, targets, ignore_index, reduction, grad, grad_scal
     dev = hidden.device
     ldw = _matrix(weight, "weight", None, cols, torch.bfloat16, dev)
     vocab = weight.shape[0]
-    _need(cols > 0 and vocab > 0, "hidden and weight need at least one column and one row")
-    _need(reduction in ("mean", "sum"), f"reduction {reduction!r} is not 'mean' or 'sum'")
+    if not (cols > 0 and vocab > 0):
+        _refuse("hidden and weight need at least one column and one row")
+    if not (reduction in ("mean", "sum")):
+        _refuse(f"reduction {reduction!r} is not 'mean' or 'sum'")
     pt = _vector(targets, "targets", rows, torch.int64, dev)
     handle, ctx = _on(stream, dev)
     with ctx:
@@ -201,19 +221,23 @@ def newton_schulz(g, steps: int = 5, eps: float = 1e-7, coefficients=NEWTON_SCHU
     Newton-Schulz iteration; returns bf16 of the same shape. With the default
     coefficients and steps the singular values end between about 0.7 and 1.2."""
     lib = capi.load()
-    _need(isinstance(g, torch.Tensor) and g.is_cuda, "g is not a CUDA tensor")
-    _need(g.dtype in _DT, f"g has dtype {g.dtype}, needs bfloat16 or float32")
-    _need(g.dim() in (2, 3), f"g has {g.dim()} dimensions, needs 2 or 3")
+    if not (isinstance(g, torch.Tensor) and g.is_cuda):
+        _refuse("g is not a CUDA tensor")
+    if not (g.dtype in _DT):
+        _refuse(f"g has dtype {g.dtype}, needs bfloat16 or float32")
+    if not (g.dim() in (2, 3)):
+        _refuse(f"g has {g.dim()} dimensions, needs 2 or 3")
     handle, ctx = _on(stream, g.device)
     with ctx:
         if out is None:
             out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
         g3 = g if g.dim() == 3 else g.unsqueeze(0)
         batch, m, n = g3.shape
-        _need(m > 0 and n > 0, "g has no rows or no columns")
+        if not (m > 0 and n > 0):
+            _refuse("g has no rows or no columns")
         ws, nws = _workspace(lib.fsdp_newton_schulz_workspace, batch, m, n, device=g.device)
-    _need(isinstance(out, torch.Tensor) and out.shape == g.shape and out.dtype == torch.bfloat16 and
-          out.device == g.device, f"out needs shape {tuple(g.shape)}, bfloat16, on {g.device}")
+    if not (isinstance(out, torch.Tensor) and out.shape == g.shape and out.dtype == torch.bfloat16 and out.device == g.device):
+        _refuse(f"out needs shape {tuple(g.shape)}, bfloat16, on {g.device}")
     o3 = out if out.dim() == 3 else out.unsqueeze(0)
     if batch == 0:
         return out
@@ -252,35 +276,43 @@ def muon_step(grads, master, momentum, params, hp: MuonHP, stream=None) -> None:
     the kernels together."""
     lib = capi.load()
     count = len(master)
-    _need(len(grads) == count and len(momentum) == count and (params is None or len(params) == count),
-          f"grads, master, momentum and params need one entry per matrix ({count})")
+    if not (len(grads) == count and len(momentum) == count and (params is None or len(params) == count)):
+        _refuse(f"grads, master, momentum and params need one entry per matrix ({count})")
     groups = {}
     for i, w in enumerate(master):
-        _need(isinstance(w, torch.Tensor) and w.is_cuda and w.dim() == 2, f"master[{i}] is not a 2-D CUDA tensor")
-        _need(len(grads[i]) > 0, f"grads[{i}] is empty")
+        if not (isinstance(w, torch.Tensor) and w.is_cuda and w.dim() == 2):
+            _refuse(f"master[{i}] is not a 2-D CUDA tensor")
+        if not (len(grads[i]) > 0):
+            _refuse(f"grads[{i}] is empty")
         groups.setdefault((w.shape[0], w.shape[1], len(grads[i]), grads[i][0].dtype), []).append(i)
     if not groups:
         return
     dev = master[0].device
 
-    def ptr(t, name, m, n, dtype):
-        ld = _matrix(t, name, m, n, dtype, dev)
-        _need(m <= 1 or ld == n, f"{name} is not contiguous")
-        return t.data_ptr()
+    def ptr(t, m, n, dtype, name, *index):
+        if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.shape == (m, n) and
+                t.device == dev and t.is_contiguous()):
+            return t.data_ptr()
+        name += "".join(f"[{i}]" for i in index)
+        _matrix(t, name, m, n, dtype, dev)
+        _refuse(f"{name} is not contiguous")
 
     calls = []
     for (m, n, R, dt), ids in groups.items():
-        _need(m > 0 and n > 0, "a matrix has no rows or no columns")
-        _need(dt in _DT, f"grads have dtype {dt}, need bfloat16 or float32")
-        _need(R <= capi.FSDP_MAX_RANKS, f"{R} ranks, at most {capi.FSDP_MAX_RANKS}")
+        if not (m > 0 and n > 0):
+            _refuse("a matrix has no rows or no columns")
+        if not (dt in _DT):
+            _refuse(f"grads have dtype {dt}, need bfloat16 or float32")
+        if not (R <= capi.FSDP_MAX_RANKS):
+            _refuse(f"{R} ranks, at most {capi.FSDP_MAX_RANKS}")
         per = min(capi.FSDP_MUON_MAX_MATRICES, 1024 // R)
         for lo in range(0, len(ids), per):
             part = ids[lo:lo + per]
             k = len(part)
-            g = (_vp * (k * R))(*[ptr(t, f"grads[{i}][{q}]", m, n, dt) for i in part for q, t in enumerate(grads[i])])
-            mo = (_vp * k)(*[ptr(momentum[i], f"momentum[{i}]", m, n, torch.float32) for i in part])
-            ma = (_vp * k)(*[ptr(master[i], f"master[{i}]", m, n, torch.float32) for i in part])
-            po = None if params is None else (_vp * k)(*[ptr(params[i], f"params[{i}]", m, n, torch.bfloat16)
+            g = (_vp * (k * R))(*[ptr(t, m, n, dt, "grads", i, q) for i in part for q, t in enumerate(grads[i])])
+            mo = (_vp * k)(*[ptr(momentum[i], m, n, torch.float32, "momentum", i) for i in part])
+            ma = (_vp * k)(*[ptr(master[i], m, n, torch.float32, "master", i) for i in part])
+            po = None if params is None else (_vp * k)(*[ptr(params[i], m, n, torch.bfloat16, "params", i)
                                                          for i in part])
             calls.append((k, m, n, R, g, _DT[dt], mo, ma, po))
     handle, ctx = _on(stream, dev)
