@@ -56,18 +56,30 @@ __device__ __forceinline__ bool kept(int64_t t, const PrepParams &p)
     return t != p.ignore && t >= 0 && t < p.vocab;
 }
 
-// A warp copies one row (or zeros it, src NULL).
+// A warp copies one row (or zeros it, src NULL), 8 elements a lane.
 __device__ __forceinline__ void copy_row(uint16_t *dst, const uint16_t *src, int n, int lane)
 {
-    if (aligned(dst, 16) && (!src || aligned(src, 16))) {
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        for (int c = lane * 8; c + 8 <= n; c += 256)
-            *reinterpret_cast<uint4 *>(dst + c) = src ? *reinterpret_cast<const uint4 *>(src + c) : zero;
-        for (int c = n / 8 * 8 + lane; c < n; c += 32)
-            dst[c] = src ? src[c] : 0;
-    } else {
-        for (int c = lane; c < n; c += 32)
-            dst[c] = src ? src[c] : 0;
+    const bool whole = src && aligned(src, 16), wide = aligned(dst, 16);
+#pragma unroll 2
+    for (int c = lane * 8; c < n; c += 256) {
+        uint4 u = make_uint4(0, 0, 0, 0);
+        uint16_t *e = reinterpret_cast<uint16_t *>(&u);
+        if (whole && c + 8 <= n) {
+            u = *reinterpret_cast<const uint4 *>(src + c);
+        } else if (src) {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                if (c + i < n)
+                    e[i] = src[c + i];
+        }
+        if (wide && c + 8 <= n) {
+            *reinterpret_cast<uint4 *>(dst + c) = u;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                if (c + i < n)
+                    dst[c + i] = e[i];
+        }
     }
 }
 
@@ -173,8 +185,10 @@ struct LogitsEpi {
         const int *target;
         float *tlogit;
     };
+    using Pre = NoPre;
+    static __device__ __forceinline__ void fetch(const Params &, const Slot &, int, Pre &) {}
     template <int COLS>
-    static __device__ __forceinline__ void run(const Params &p, const Slot &x)
+    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &)
     {
         static_assert(COLS == kPieceCols, "one thread's columns are one piece");
         // the columns past the vocabulary are compared only where there are some
@@ -385,45 +399,63 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowsParams p)
 // dhidden rows back at their own places, bf16.
 struct HiddenEpi {
     static constexpr int kLeastTN = 64;
+    static constexpr bool kAhead = false;
     struct Params {
         uint16_t *out;
         int64_t ld;
         const int *source;
     };
-    template <int COLS>
-    static __device__ __forceinline__ void run(const Params &p, const Slot &x)
+    struct Pre {
+        int row[8];
+    };
+    static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int chunk, Pre &pre)
     {
-#pragma unroll 1
-        for (int c = 0; c < COLS / 32; c++) {
-            float mine[32];
-            x.across<false>(c, mine, [&](int r, int i, float(&v)[4]) {
-                const int row = x.row - x.lane + r, col = x.col + c * 32 + i;
-                if (row < x.M && col < x.N)
-                    put4_16<true>(p.out + (int64_t)p.source[row] * p.ld + col, v, x.N - col);
-            });
+        if (chunk == 0) {  // the same rows in every chunk
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                pre.row[i] = x.group_row(i) < x.M ? p.source[x.group_row(i)] : -1;
         }
+    }
+    static __device__ __forceinline__ void chunk(const Params &p, const Slot &x, int c, Pre &pre)
+    {
+        float mine[32];
+        const int col = x.group_col(c);
+        x.across<false>(c, mine, [&](int i, float(&v)[4]) {
+            if (pre.row[i] >= 0 && col < x.N)
+                put4_16<true>(p.out + (int64_t)pre.row[i] * p.ld + col, v, x.N - col);
+        });
+    }
+    template <int COLS>
+    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre)
+    {
+        finish_tile<COLS, HiddenEpi>(p, x, pre);
     }
 };
 
 // Partial sums of split products, fp32.
 struct PartEpi {
     static constexpr int kLeastTN = 64;
+    static constexpr bool kAhead = false;
     struct Params {
         float *out;  // [splits][rows][ld], ld a multiple of 8
         int64_t ld, split_stride;
     };
-    template <int COLS>
-    static __device__ __forceinline__ void run(const Params &p, const Slot &x)
+    using Pre = NoPre;
+    static __device__ __forceinline__ void fetch(const Params &, const Slot &, int, Pre &) {}
+    static __device__ __forceinline__ void chunk(const Params &p, const Slot &x, int c, Pre &)
     {
-#pragma unroll 1
-        for (int c = 0; c < COLS / 32; c++) {
-            float mine[32];
-            x.across<false>(c, mine, [&](int r, int i, float(&v)[4]) {
-                const int row = x.row - x.lane + r, col = x.col + c * 32 + i;
-                if (row < x.M && col < x.N)
-                    put4_f32(p.out + x.split * p.split_stride + (int64_t)row * p.ld + col, v, 4);
-            });
-        }
+        float mine[32];
+        const int col = x.group_col(c);
+        x.across<false>(c, mine, [&](int i, float(&v)[4]) {
+            const int row = x.group_row(i);
+            if (row < x.M && col < x.N)
+                put4_f32(p.out + x.split * p.split_stride + (int64_t)row * p.ld + col, v, 4);
+        });
+    }
+    template <int COLS>
+    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre)
+    {
+        finish_tile<COLS, PartEpi>(p, x, pre);
     }
 };
 
@@ -452,6 +484,7 @@ __global__ void __launch_bounds__(128) join_hidden_kernel(const float *parts, in
 // dweight, over the pieces of the rows in fp32 where there are several.
 struct WeightEpi {
     static constexpr int kLeastTN = 64;
+    static constexpr bool kAhead = true;
     struct Params {
         uint16_t *out;
         int64_t ld;
@@ -459,32 +492,46 @@ struct WeightEpi {
         int64_t lds; // a multiple of 8
         int first, last;
     };
-    template <int COLS>
-    static __device__ __forceinline__ void run(const Params &p, const Slot &x)
+    struct Pre {
+        float o[8][4];
+    };
+    static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int chunk, Pre &pre)
     {
-#pragma unroll 1
-        for (int c = 0; c < COLS / 32; c++) {
-            float mine[32];
-            x.across<false>(c, mine, [&](int r, int i, float(&v)[4]) {
-                const int row = x.row - x.lane + r, col = x.col + c * 32 + i;
-                if (row >= x.M || col >= x.N)
-                    return;
-                if (p.sum) {
-                    float *s = p.sum + (int64_t)row * p.lds + col;
-                    if (!p.first) {
-                        float o[4];
-                        get4_f32(s, o, 4);
+        const int col = x.group_col(chunk);
+        const bool more = p.sum && !p.first;
 #pragma unroll
-                        for (int k = 0; k < 4; k++)
-                            v[k] += o[k];
-                    }
-                    if (!p.last)
-                        put4_f32(s, v, 4);
-                }
-                if (p.last)
-                    put4_16<true>(p.out + (int64_t)row * p.ld + col, v, x.N - col);
-            });
+        for (int i = 0; i < 8; i++) {
+            const int row = x.group_row(i);
+            if (more && row < x.M && col < x.N) {
+                get4_f32(p.sum + (int64_t)row * p.lds + col, pre.o[i], 4);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; k++)
+                    pre.o[i][k] = 0.0f;
+            }
         }
+    }
+    static __device__ __forceinline__ void chunk(const Params &p, const Slot &x, int c, Pre &pre)
+    {
+        float mine[32];
+        const int col = x.group_col(c);
+        x.across<false>(c, mine, [&](int i, float(&v)[4]) {
+            const int row = x.group_row(i);
+            if (row >= x.M || col >= x.N)
+                return;
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+                v[k] += pre.o[i][k];
+            if (p.last)
+                put4_16<true>(p.out + (int64_t)row * p.ld + col, v, x.N - col);
+            else
+                put4_f32(p.sum + (int64_t)row * p.lds + col, v, 4);
+        });
+    }
+    template <int COLS>
+    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre)
+    {
+        finish_tile<COLS, WeightEpi>(p, x, pre);
     }
 };
 
@@ -502,7 +549,7 @@ struct Plan {
 
 bool map_ok(const void *p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0; }
 
-constexpr int kPairs = 76;  // tiles that keep the multiprocessors busy
+constexpr int kTargetTiles = 152;  // one for each multiprocessor of a GB300
 
 Plan plan_of(const LossArgs &a, bool grad, void *base, bool with_weight)
 {
@@ -520,11 +567,12 @@ Plan plan_of(const LossArgs &a, bool grad, void *base, bool with_weight)
     q.pieces = a.rows ? (a.rows + q.piece - 1) / q.piece : 0;
     q.ldx = ceil_to(a.cols, 16);
     q.stat_pieces = (int)((a.vocab + kPieceCols - 1) / kPieceCols);
-    // dhidden sums over the vocabulary: where its tiles are few, the sum is
-    // cut so that about all multiprocessors have a part of it
-    const int64_t tiles = (q.piece + 127) / 128 * ((a.cols + kTileN - 1) / kTileN);
+    // dhidden sums over the vocabulary: where its tiles (of 128 x 128, the
+    // smallest worth it) are few, the sum is cut so that about all
+    // multiprocessors have a part of it
+    const int64_t tiles = (q.piece + 127) / 128 * ((a.cols + 127) / 128);
     const int64_t blocks = (a.vocab + kBK - 1) / kBK;
-    int64_t splits = tiles ? 2 * kPairs / tiles : 1;
+    int64_t splits = tiles ? kTargetTiles / tiles : 1;
     if (splits > blocks / 8)
         splits = blocks / 8;
     if (splits < 1)

@@ -224,53 +224,67 @@ __global__ void __launch_bounds__(kStartThreads) scale_kernel(const float *x32, 
 // multiples of 16, so groups of 4 and pairs of rows stay inside a padded row.
 struct SquareEpi {
     static constexpr int kLeastTN = 64;
+    static constexpr bool kAhead = true;
     struct Params {
         uint16_t *out;
         const uint16_t *from;
         int64_t ld, stride;
         float b, c;
     };
-    template <int COLS>
-    static __device__ __forceinline__ void run(const Params &p, const Slot &x)
+    struct Pre {
+        uint2 s[8];
+    };
+    static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int chunk, Pre &pre)
+    {
+        const int col = x.group_col(chunk);
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const int row = x.group_row(i);
+            pre.s[i] = make_uint2(0, 0);
+            if (p.from && row < x.M && col < x.N)
+                pre.s[i] = *reinterpret_cast<const uint2 *>(p.from + x.z * p.stride + row * p.ld + col);
+        }
+    }
+    static __device__ __forceinline__ void chunk(const Params &p, const Slot &x, int c, Pre &pre)
     {
         uint16_t *out = p.out + x.z * p.stride;
-        const uint16_t *from = p.from ? p.from + x.z * p.stride : nullptr;
-        const int row0 = x.row - x.lane;
-#pragma unroll 1
-        for (int c = 0; c < COLS / 32; c++) {
-            const int col0 = x.col + c * 32;
-            float mine[32];
-            auto direct = [&](int r, int i, float(&v)[4]) {
-                const int row = row0 + r, col = col0 + i;
-                if (row >= x.M || col >= x.N)
-                    return;
-                const int64_t at = row * p.ld + col;
-                if (from) {
-                    float f[4];
-                    get4_f16(from + at, f);
-#pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        v[k] = fmaf(p.c, v[k], p.b * f[k]);
-                }
-                put4_16<false>(out + at, v, 4);
-            };
-            if (!x.mirror) {
-                x.across<false>(c, mine, direct);
-                continue;
+        const int col = x.group_col(c);
+        float mine[32];
+        auto direct = [&](int i, float(&v)[4]) {
+            const int row = x.group_row(i);
+            if (row >= x.M || col >= x.N)
+                return;
+            if (p.from) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&pre.s[i].x));
+                const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&pre.s[i].y));
+                v[0] = fmaf(p.c, v[0], p.b * f.x);
+                v[1] = fmaf(p.c, v[1], p.b * f.y);
+                v[2] = fmaf(p.c, v[2], p.b * g.x);
+                v[3] = fmaf(p.c, v[3], p.b * g.y);
             }
-            x.across<true>(c, mine, direct);
-            // the transposed elements: two rows' on a pair of lanes make one
-            // 32-bit store, of column j on the even and j + 1 on the odd lane
-            const int odd = x.lane & 1, row = x.row & ~1;
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-                const float other = __shfl_xor_sync(0xffffffffu, odd ? mine[j] : mine[j + 1], 1);
-                const int col = col0 + j + odd;
-                const uint32_t pair = odd ? pack_f16(other, mine[j + 1]) : pack_f16(mine[j], other);
-                if (row < x.M && col < x.N)
-                    *reinterpret_cast<uint32_t *>(out + col * p.ld + row) = pair;
-            }
+            put4_16<false>(out + row * p.ld + col, v, 4);
+        };
+        if (!x.mirror) {
+            x.across<false>(c, mine, direct);
+            return;
         }
+        x.across<true>(c, mine, direct);
+        // the transposed elements: two rows' on a pair of lanes make one
+        // 32-bit store, of column j on the even and j + 1 on the odd lane
+        const int odd = x.lane & 1, row = x.row & ~1;
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? mine[j] : mine[j + 1], 1);
+            const int to = x.col + c * 32 + j + odd;
+            const uint32_t pair = odd ? pack_f16(other, mine[j + 1]) : pack_f16(mine[j], other);
+            if (row < x.M && to < x.N)
+                *reinterpret_cast<uint32_t *>(out + to * p.ld + row) = pair;
+        }
+    }
+    template <int COLS>
+    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre)
+    {
+        finish_tile<COLS, SquareEpi>(p, x, pre);
     }
 };
 
@@ -280,58 +294,79 @@ struct SquareEpi {
 //   kMaster  w = w decay - lr x, and the bf16 parameter
 enum class Then { kKeep, kOut, kMaster };
 
+struct StepParams {
+    float *x32;
+    const float *inv;  // the first step's factor of x32, per matrix; NULL: 1
+    int64_t ld, stride;
+    float a;
+    uint16_t *x16;
+    uint16_t *out;
+    int64_t ldo, out_stride, n;
+    float decay, lr;
+    float *master[kMuonMaxMats];
+    uint16_t *param[kMuonMaxMats];
+};
+
+template <Then kThen>
 struct StepEpi {
     static constexpr int kLeastTN = 64;
-    struct Params {
-        float *x32;
-        const float *inv;  // the first step's factor of x32, per matrix; NULL: 1
-        int64_t ld, stride;
+    static constexpr bool kAhead = kThen != Then::kMaster;  // registers
+    using Params = StepParams;
+    struct Pre {
         float a;
-        Then then;
-        uint16_t *x16;
-        uint16_t *out;
-        int64_t ldo, out_stride, n;
-        float decay, lr;
-        float *master[kMuonMaxMats];
-        uint16_t *param[kMuonMaxMats];
+        float x[8][4];
+        float w[kThen == Then::kMaster ? 8 : 1][4];
     };
-    template <int COLS>
-    static __device__ __forceinline__ void run(const Params &p, const Slot &x)
+    static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int chunk, Pre &pre)
     {
-        const float a = p.inv ? p.a * p.inv[x.z] : p.a;
-        float *x32 = p.x32 + x.z * p.stride;
-        float *master = p.then == Then::kMaster ? p.master[x.z] : nullptr;
-        uint16_t *param = p.then == Then::kMaster ? p.param[x.z] : nullptr;
-#pragma unroll 1
-        for (int c = 0; c < COLS / 32; c++) {
-            float mine[32];
-            x.across<false>(c, mine, [&](int r, int i, float(&v)[4]) {
-                const int row = x.row - x.lane + r, col = x.col + c * 32 + i, left = x.N - col;
-                if (row >= x.M || left <= 0)
-                    return;
-                const int64_t at = row * p.ld + col;
-                float o[4];
-                get4_f32(x32 + at, o, 4);
+        const int col = x.group_col(chunk);
+        pre.a = p.inv ? p.a * p.inv[x.z] : p.a;
+        const float *x32 = p.x32 + x.z * p.stride;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const int row = x.group_row(i);
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+                pre.x[i][k] = 0.0f;
+            if (row < x.M && col < x.N) {
+                get4_f32(x32 + row * p.ld + col, pre.x[i], 4);
+                if (kThen == Then::kMaster)
+                    get4_f32(p.master[x.z] + row * p.n + col, pre.w[kThen == Then::kMaster ? i : 0], x.N - col);
+            }
+        }
+    }
+    static __device__ __forceinline__ void chunk(const Params &p, const Slot &x, int c, Pre &pre)
+    {
+        const int col = x.group_col(c), left = x.N - col;
+        float mine[32];
+        x.across<false>(c, mine, [&](int i, float(&v)[4]) {
+            const int row = x.group_row(i);
+            if (row >= x.M || left <= 0)
+                return;
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+                v[k] = fmaf(pre.a, pre.x[i][k], v[k]);
+            if (kThen == Then::kKeep) {
+                const int64_t at = x.z * p.stride + row * p.ld + col;
+                put4_f32(p.x32 + at, v, 4);
+                put4_16<false>(p.x16 + at, v, 4);
+            } else if (kThen == Then::kOut) {
+                put4_16<true>(p.out + x.z * p.out_stride + row * p.ldo + col, v, left);
+            } else {
+                const int64_t to = row * p.n + col;
 #pragma unroll
                 for (int k = 0; k < 4; k++)
-                    v[k] = fmaf(a, o[k], v[k]);
-                if (p.then == Then::kKeep) {
-                    put4_f32(x32 + at, v, 4);
-                    put4_16<false>(p.x16 + x.z * p.stride + at, v, 4);
-                } else if (p.then == Then::kOut) {
-                    put4_16<true>(p.out + x.z * p.out_stride + row * p.ldo + col, v, left);
-                } else {
-                    const int64_t to = row * p.n + col;
-                    get4_f32(master + to, o, left);
-#pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        v[k] = fmaf(-p.lr, v[k], o[k] * p.decay);
-                    put4_f32(master + to, v, left);
-                    if (param)
-                        put4_16<true>(param + to, v, left);
-                }
-            });
-        }
+                    v[k] = fmaf(-p.lr, v[k], pre.w[kThen == Then::kMaster ? i : 0][k] * p.decay);
+                put4_f32(p.master[x.z] + to, v, left);
+                if (p.param[x.z])
+                    put4_16<true>(p.param[x.z] + to, v, left);
+            }
+        });
+    }
+    template <int COLS>
+    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre)
+    {
+        finish_tile<COLS, StepEpi>(p, x, pre);
     }
 };
 
@@ -469,7 +504,7 @@ fsdp_status launch_newton_schulz(const SchulzArgs &a, void *workspace, int dev, 
 
     const bool wide = a.m <= a.n;
     const int64_t xs = a.m * q.ldx, ks = q.k * q.ldk;
-    StepEpi::Params ep{};
+    StepParams ep{};
     ep.x32 = q.x32;
     ep.ld = q.ldx;
     ep.stride = xs;
@@ -508,10 +543,15 @@ fsdp_status launch_newton_schulz(const SchulzArgs &a, void *workspace, int dev, 
         up.batch = batch;
         ep.inv = step == 0 ? q.inv : nullptr;
         ep.x16 = q.x16[(step + 1) % 2];
-        ep.then = step + 1 < a.steps ? Then::kKeep : muon ? Then::kMaster : Then::kOut;
-        // wide: P x, x with its columns adjacent; tall: x P, P symmetric
-        st = wide ? product<false, true, StepEpi>(up, poly, x, false, ep, dev, s, "newton_schulz (x)")
-                  : product<false, false, StepEpi>(up, x, poly, false, ep, dev, s, "newton_schulz (x)");
+        auto update = [&](auto epi) {
+            using E = decltype(epi);
+            // wide: P x, x with its columns adjacent; tall: x P, P symmetric
+            return wide ? product<false, true, E>(up, poly, x, false, ep, dev, s, "newton_schulz (x)")
+                        : product<false, false, E>(up, x, poly, false, ep, dev, s, "newton_schulz (x)");
+        };
+        st = step + 1 < a.steps ? update(StepEpi<Then::kKeep>{})
+             : muon             ? update(StepEpi<Then::kMaster>{})
+                                : update(StepEpi<Then::kOut>{});
         if (st != FSDP_OK)
             return st;
     }

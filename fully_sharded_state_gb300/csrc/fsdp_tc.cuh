@@ -214,7 +214,7 @@ struct Tiles {
     static constexpr int kRows = kTM * kCtas;
     static constexpr int kSquare = kRows > TN ? kRows : TN;  // of sym
     int m_tiles, n_tiles, M, K;
-    int64_t per_z, total;
+    uint32_t per_z, total;  // below 2^31
 
     __device__ __forceinline__ Tiles(const Shape &s)
     {
@@ -228,21 +228,21 @@ struct Tiles {
         m_tiles = (M + kRows - 1) / kRows;
         n_tiles = (s.N + TN - 1) / TN;
         if (s.sym) {
-            const int64_t q = (M + kSquare - 1) / kSquare;
+            const uint32_t q = (M + kSquare - 1) / kSquare;
             per_z = q * (q + 1) / 2 * (kSquare / kRows) * (kSquare / TN);
         } else {
-            per_z = (int64_t)m_tiles * n_tiles;
+            per_z = (uint32_t)m_tiles * n_tiles;
         }
         total = per_z * s.batch * s.splits;
     }
 
-    __device__ __forceinline__ Work at(const Shape &s, int64_t t) const
+    __device__ __forceinline__ Work at(const Shape &s, uint32_t t) const
     {
         Work w;
-        const int64_t zs = t / per_z;
+        const uint32_t zs = t / per_z;
         int i = (int)(t - zs * per_z);
-        w.split = (int)(zs % s.splits);
-        w.z = (int)(zs / s.splits);
+        w.split = (int)(zs % (uint32_t)s.splits);
+        w.z = (int)(zs / (uint32_t)s.splits);
         if (s.sym) {
             constexpr int kSubM = kSquare / kRows, kSubN = kSquare / TN;
             const int sub = i % (kSubM * kSubN);
@@ -301,11 +301,14 @@ struct Slot {
         return reinterpret_cast<uint4 *>(stage + r * 128 + ((c ^ (r & 7)) << 4));
     }
 
-    // Calls f(r, c, v) for the 32 x 32 values of a chunk, 4 at a time, a row's
-    // 8 groups on 8 adjacent lanes: row `row - lane + r`, columns from
-    // col + 32 * chunk + c on. Rows and columns past the matrix are included.
-    // What f leaves in v is back in `mine` (the thread's own row) after it,
-    // where kBack is set.
+    // Group i (0..7) of this lane in a chunk: 4 adjacent columns of a row, the
+    // 8 groups of a row on 8 adjacent lanes.
+    __device__ __forceinline__ int group_row(int i) const { return row - lane + i * 4 + lane / 8; }
+    __device__ __forceinline__ int group_col(int chunk) const { return col + chunk * 32 + lane % 8 * 4; }
+
+    // Takes a chunk of the accumulator to the lanes by groups and calls
+    // f(i, v) for each of this lane's 8. What f leaves in v is back in `mine`
+    // (the thread's own row of the chunk) after it, where kBack is set.
     template <bool kBack, class F>
     __device__ __forceinline__ void across(int chunk, float (&mine)[32], F f) const
     {
@@ -317,13 +320,13 @@ struct Slot {
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-            const int r = i * 4 + lane / 8;
-            const uint4 u = *piece(r, lane % 8);
+            uint4 *at = piece(i * 4 + lane / 8, lane % 8);
+            const uint4 u = *at;
             float v[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
-            f(r, lane % 8 * 4, v);
+            f(i, v);
             if (kBack)
-                *piece(r, lane % 8) = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                                                 __float_as_uint(v[3]));
+                *at = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                 __float_as_uint(v[3]));
         }
         __syncwarp();
         if (kBack) {
@@ -338,6 +341,40 @@ struct Slot {
             __syncwarp();
         }
     }
+};
+
+// An epilogue E has
+//   Params, kLeastTN   its arguments; the narrowest tile it takes
+//   Pre                what it reads from memory for one chunk, in registers
+//   fetch(p, x, chunk, pre)   starts those reads
+//   chunk(p, x, chunk, pre)   finishes a chunk with them
+// The first chunk's reads are started before the accumulator is waited for,
+// and with kAhead each chunk's before the one before it is finished: with
+// reads and stores in turn, their latency made up most of a short product.
+template <int COLS, class E>
+__device__ __forceinline__ void finish_tile(const typename E::Params &p, const Slot &x, typename E::Pre &a)
+{
+    constexpr int n = COLS / 32;
+    if (E::kAhead && n > 1) {
+        typename E::Pre b;
+#pragma unroll 1
+        for (int c = 0; c < n; c += 2) {
+            E::fetch(p, x, c + 1, b);
+            E::chunk(p, x, c, a);
+            if (c + 2 < n)
+                E::fetch(p, x, c + 2, a);
+            E::chunk(p, x, c + 1, b);
+        }
+    } else {
+#pragma unroll 1
+        for (int c = 0; c < n; c++) {
+            if (c > 0)
+                E::fetch(p, x, c, a);
+            E::chunk(p, x, c, a);
+        }
+    }
+}
+struct NoPre {
 };
 
 template <int kCtas, int TN>
@@ -376,11 +413,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = kCtas == 2 ? cluster_rank() : 0;
     using T = Tiles<kCtas, TN>;
-    const int64_t first = blockIdx.x / kCtas, step = gridDim.x / kCtas;
+    const uint32_t first = blockIdx.x / kCtas, step = gridDim.x / kCtas;
 
     if (warp == 2)
         tmem_alloc<kCtas>(tmem_at, 2 * TN);
     if (threadIdx.x == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_a) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_b) : "memory");
         for (int i = 0; i < R::kStages; i++) {
             bar_init(full + i, 1);
             bar_init(empty + i, 1);
@@ -408,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             int stage = 0;
             uint32_t phase = 0;
-            for (int64_t t = first; ok && t < tiles.total; t += step) {
+            for (uint32_t t = first; ok && t < tiles.total; t += step) {
                 const Work w = tiles.at(s, t);
                 const int row = w.row + (int)rank * kTM, col = w.col + (int)rank * R::kRowsB;
                 for (int kb = 0; kb < w.nkb; kb++) {
@@ -443,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0 && rank == 0) {
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
-            for (int64_t t = first; ok && t < tiles.total; t += step) {
+            for (uint32_t t = first; ok && t < tiles.total; t += step) {
                 const Work w = tiles.at(s, t);
                 if (!(ok = bar_wait(acc_empty + acc, acc_phase ^ 1)))
                     break;
@@ -476,13 +515,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int acc = 0;
         uint32_t acc_phase = 0;
         const int quarter = warp % 4, half = (warp - 4) / 4;
-        for (int64_t t = first; t < tiles.total; t += step) {
+        for (uint32_t t = first; t < tiles.total; t += step) {
             const Work w = tiles.at(s, t);
-            ok = bar_wait(acc_full + acc, acc_phase);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok)
-                break;
-            fence_after();
             Slot x;
             x.z = w.z;
             x.split = w.split;
@@ -495,7 +529,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             x.tmem = tmem + acc * TN + half * (TN / 2) + ((uint32_t)(quarter * 32) << 16);
             x.mirror = s.sym && w.row / T::kSquare != w.col / T::kSquare;
             x.empty = w.nkb == 0;
-            Epi::template run<TN / 2>(ep, x);
+            typename Epi::Pre pre;
+            Epi::fetch(ep, x, 0, pre);
+            ok = bar_wait(acc_full + acc, acc_phase);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok)
+                break;
+            fence_after();
+            Epi::template run<TN / 2>(ep, x, pre);
             fence_before();
             __syncwarp();
             if (lane == 0)
@@ -645,6 +686,8 @@ fsdp_status product(Shape s, const Operand &a, const Operand &b, bool bf16, cons
     }
     if (best->tiles < 1)
         return FSDP_OK;
+    if (best->tiles >= (int64_t)1 << 31)
+        return set_error(FSDP_ERANGE, "%s: %lld tiles", what, (long long)best->tiles);
     if (best->ctas == 2)
         return product_as<2, 256, kAMN, kBMN, Epi>(s, a, b, bf16, ep, best->tiles, dev, stream, what);
     if (best->tn == 256)

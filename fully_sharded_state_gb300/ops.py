@@ -78,7 +78,8 @@ def _vector(t, name, n, dtype, device):
 def _on(stream, device):
     """The stream's handle, and the context in which memory is allocated for it."""
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream, _SAME
+        # the handle alone: torch.cuda.current_stream() builds a Stream object, 2 us of a 25 us call
+        return torch._C._cuda_getCurrentRawStream(device.index), _SAME
     return stream.cuda_stream, torch.cuda.stream(stream)
 
 
