@@ -418,12 +418,21 @@ struct HiddenEpi {
     }
     static __device__ __forceinline__ void chunk(const Params &p, const Slot &x, int c, Pre &pre)
     {
-        float mine[32];
-        const int col = x.group_col(c);
-        x.across<false>(c, mine, [&](int i, float(&v)[4]) {
-            if (pre.row[i] >= 0 && col < x.N)
-                put4_16<true>(p.out + (int64_t)pre.row[i] * p.ld + col, v, x.N - col);
-        });
+        if (groups_of_4(p.out, p.ld)) {
+            float mine[32];
+            const int col = x.group_col(c);
+            x.across<false>(c, mine, [&](int i, float(&v)[4]) {
+                if (pre.row[i] >= 0 && col < x.N)
+                    put4_16<true>(p.out + (int64_t)pre.row[i] * p.ld + col, v, x.N - col);
+            });
+        } else {
+            const int col = x.col + c * 32 + x.lane;
+            x.by_rows(c, [&](int r, float v) {
+                const int row = x.row - x.lane + r;
+                if (row < x.M && col < x.N)
+                    p.out[(int64_t)p.source[row] * p.ld + col] = to_bf16(v);
+            });
+        }
     }
     template <int COLS>
     static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre)
@@ -445,11 +454,12 @@ struct PartEpi {
     static __device__ __forceinline__ void chunk(const Params &p, const Slot &x, int c, Pre &)
     {
         float mine[32];
-        const int col = x.group_col(c);
+        const int rows = x.M - x.group_row(0);
+        const bool in = x.group_col(c) < x.N;
+        float *to = p.out + x.split * p.split_stride + x.group_row(0) * p.ld + x.group_col(c);
         x.across<false>(c, mine, [&](int i, float(&v)[4]) {
-            const int row = x.group_row(i);
-            if (row < x.M && col < x.N)
-                put4_f32(p.out + x.split * p.split_stride + (int64_t)row * p.ld + col, v, 4);
+            if (i * 4 < rows && in)
+                *reinterpret_cast<float4 *>(to + i * 4 * p.ld) = make_float4(v[0], v[1], v[2], v[3]);
         });
     }
     template <int COLS>
@@ -493,40 +503,59 @@ struct WeightEpi {
         int first, last;
     };
     struct Pre {
-        float o[8][4];
+        float4 o[8];
     };
     static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int chunk, Pre &pre)
     {
-        const int col = x.group_col(chunk);
-        const bool more = p.sum && !p.first;
+        if (!p.sum || p.first)
+            return;
+        const int rows = x.M - x.group_row(0);
+        const float *from = p.sum + x.group_row(0) * p.lds + x.group_col(chunk);
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const int row = x.group_row(i);
-            if (more && row < x.M && col < x.N) {
-                get4_f32(p.sum + (int64_t)row * p.lds + col, pre.o[i], 4);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 4; k++)
-                    pre.o[i][k] = 0.0f;
-            }
-        }
+        for (int i = 0; i < 8; i++)
+            if (i * 4 < rows && x.group_col(chunk) < x.N)
+                pre.o[i] = *reinterpret_cast<const float4 *>(from + i * 4 * p.lds);
     }
     static __device__ __forceinline__ void chunk(const Params &p, const Slot &x, int c, Pre &pre)
     {
+        const int col = x.group_col(c), left = x.N - col, rows = x.M - x.group_row(0);
+        uint16_t *to = p.out + x.group_row(0) * p.ld + col;
         float mine[32];
-        const int col = x.group_col(c);
-        x.across<false>(c, mine, [&](int i, float(&v)[4]) {
-            const int row = x.group_row(i);
-            if (row >= x.M || col >= x.N)
-                return;
-#pragma unroll
-            for (int k = 0; k < 4; k++)
-                v[k] += pre.o[i][k];
-            if (p.last)
-                put4_16<true>(p.out + (int64_t)row * p.ld + col, v, x.N - col);
-            else
-                put4_f32(p.sum + (int64_t)row * p.lds + col, v, 4);
-        });
+        if (p.sum) {
+            float *sum = p.sum + x.group_row(0) * p.lds + col;
+            x.across<false>(c, mine, [&](int i, float(&v)[4]) {
+                if (i * 4 >= rows || left <= 0)
+                    return;
+                if (!p.first) {
+                    v[0] += pre.o[i].x;
+                    v[1] += pre.o[i].y;
+                    v[2] += pre.o[i].z;
+                    v[3] += pre.o[i].w;
+                }
+                if (p.last)
+                    put4_16<true>(to + i * 4 * p.ld, v, left);
+                else
+                    *reinterpret_cast<float4 *>(sum + i * 4 * p.lds) = make_float4(v[0], v[1], v[2], v[3]);
+            });
+        } else if (groups_of_4(p.out, p.ld)) {
+            x.across<false>(c, mine, [&](int i, float(&v)[4]) {
+                if (i * 4 >= rows || left <= 0)
+                    return;
+                if (left >= 4)
+                    *reinterpret_cast<uint2 *>(to + i * 4 * p.ld) = four_16<true>(v);
+                else
+                    put4_16<true>(to + i * 4 * p.ld, v, left);
+            });
+        } else {
+            // a lane per column: every 32-byte sector is written in one go
+            uint16_t *row = p.out + (x.row - x.lane) * p.ld + x.col + c * 32 + x.lane;
+            const int n = x.M - (x.row - x.lane);
+            const bool in = x.col + c * 32 + x.lane < x.N;
+            x.by_rows(c, [&](int r, float v) {
+                if (r < n && in)
+                    row[r * p.ld] = to_bf16(v);
+            });
+        }
     }
     template <int COLS>
     static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre)

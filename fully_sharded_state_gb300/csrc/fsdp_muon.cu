@@ -236,23 +236,24 @@ struct SquareEpi {
     };
     static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int chunk, Pre &pre)
     {
-        const int col = x.group_col(chunk);
+        if (!p.from)
+            return;
+        const int rows = x.M - x.group_row(0);
+        const uint16_t *from = p.from + x.z * p.stride + x.group_row(0) * p.ld + x.group_col(chunk);
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const int row = x.group_row(i);
-            pre.s[i] = make_uint2(0, 0);
-            if (p.from && row < x.M && col < x.N)
-                pre.s[i] = *reinterpret_cast<const uint2 *>(p.from + x.z * p.stride + row * p.ld + col);
-        }
+        for (int i = 0; i < 8; i++)
+            if (i * 4 < rows && x.group_col(chunk) < x.N)
+                pre.s[i] = *reinterpret_cast<const uint2 *>(from + i * 4 * p.ld);
     }
     static __device__ __forceinline__ void chunk(const Params &p, const Slot &x, int c, Pre &pre)
     {
         uint16_t *out = p.out + x.z * p.stride;
-        const int col = x.group_col(c);
+        const int rows = x.M - x.group_row(0);
+        const bool in = x.group_col(c) < x.N;
+        uint16_t *to = out + x.group_row(0) * p.ld + x.group_col(c);
         float mine[32];
         auto direct = [&](int i, float(&v)[4]) {
-            const int row = x.group_row(i);
-            if (row >= x.M || col >= x.N)
+            if (i * 4 >= rows || !in)
                 return;
             if (p.from) {
                 const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&pre.s[i].x));
@@ -262,7 +263,7 @@ struct SquareEpi {
                 v[2] = fmaf(p.c, v[2], p.b * g.x);
                 v[3] = fmaf(p.c, v[3], p.b * g.y);
             }
-            put4_16<false>(out + row * p.ld + col, v, 4);
+            *reinterpret_cast<uint2 *>(to + i * 4 * p.ld) = four_16<false>(v);
         };
         if (!x.mirror) {
             x.across<false>(c, mine, direct);
@@ -272,13 +273,14 @@ struct SquareEpi {
         // the transposed elements: two rows' on a pair of lanes make one
         // 32-bit store, of column j on the even and j + 1 on the odd lane
         const int odd = x.lane & 1, row = x.row & ~1;
+        const int cols = row < x.M ? x.N - (x.col + c * 32 + odd) : 0;
+        uint16_t *across = out + (x.col + c * 32 + odd) * p.ld + row;
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
             const float other = __shfl_xor_sync(0xffffffffu, odd ? mine[j] : mine[j + 1], 1);
-            const int to = x.col + c * 32 + j + odd;
             const uint32_t pair = odd ? pack_f16(other, mine[j + 1]) : pack_f16(mine[j], other);
-            if (row < x.M && to < x.N)
-                *reinterpret_cast<uint32_t *>(out + to * p.ld + row) = pair;
+            if (j < cols)
+                *reinterpret_cast<uint32_t *>(across + j * p.ld) = pair;
         }
     }
     template <int COLS>
@@ -310,56 +312,53 @@ struct StepParams {
 template <Then kThen>
 struct StepEpi {
     static constexpr int kLeastTN = 64;
-    static constexpr bool kAhead = kThen != Then::kMaster;  // registers
+    static constexpr bool kAhead = kThen != Then::kMaster;  // it has twice the reads: registers
     using Params = StepParams;
+    static constexpr bool kMaster = kThen == Then::kMaster;
     struct Pre {
         float a;
-        float x[8][4];
-        float w[kThen == Then::kMaster ? 8 : 1][4];
+        float4 x[8];
+        float w[kMaster ? 8 : 1][4];
     };
     static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int chunk, Pre &pre)
     {
-        const int col = x.group_col(chunk);
+        const int rows = x.M - x.group_row(0), left = x.N - x.group_col(chunk);
         pre.a = p.inv ? p.a * p.inv[x.z] : p.a;
-        const float *x32 = p.x32 + x.z * p.stride;
+        const float *from = p.x32 + x.z * p.stride + x.group_row(0) * p.ld + x.group_col(chunk);
+        const float *w = kMaster ? p.master[x.z] + x.group_row(0) * p.n + x.group_col(chunk) : nullptr;
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const int row = x.group_row(i);
-#pragma unroll
-            for (int k = 0; k < 4; k++)
-                pre.x[i][k] = 0.0f;
-            if (row < x.M && col < x.N) {
-                get4_f32(x32 + row * p.ld + col, pre.x[i], 4);
-                if (kThen == Then::kMaster)
-                    get4_f32(p.master[x.z] + row * p.n + col, pre.w[kThen == Then::kMaster ? i : 0], x.N - col);
+        for (int i = 0; i < 8; i++)
+            if (i * 4 < rows && left > 0) {
+                pre.x[i] = *reinterpret_cast<const float4 *>(from + i * 4 * p.ld);
+                if (kMaster)
+                    get4_f32(w + i * 4 * p.n, pre.w[kMaster ? i : 0], left);
             }
-        }
     }
     static __device__ __forceinline__ void chunk(const Params &p, const Slot &x, int c, Pre &pre)
     {
-        const int col = x.group_col(c), left = x.N - col;
+        const int rows = x.M - x.group_row(0), col = x.group_col(c), left = x.N - col;
+        const int64_t at = x.z * p.stride + x.group_row(0) * p.ld + col;
+        const int64_t to = x.group_row(0) * (kThen == Then::kOut ? p.ldo : p.n) + col;
         float mine[32];
         x.across<false>(c, mine, [&](int i, float(&v)[4]) {
-            const int row = x.group_row(i);
-            if (row >= x.M || left <= 0)
+            if (i * 4 >= rows || left <= 0)
                 return;
-#pragma unroll
-            for (int k = 0; k < 4; k++)
-                v[k] = fmaf(pre.a, pre.x[i][k], v[k]);
+            v[0] = fmaf(pre.a, pre.x[i].x, v[0]);
+            v[1] = fmaf(pre.a, pre.x[i].y, v[1]);
+            v[2] = fmaf(pre.a, pre.x[i].z, v[2]);
+            v[3] = fmaf(pre.a, pre.x[i].w, v[3]);
             if (kThen == Then::kKeep) {
-                const int64_t at = x.z * p.stride + row * p.ld + col;
-                put4_f32(p.x32 + at, v, 4);
-                put4_16<false>(p.x16 + at, v, 4);
+                *reinterpret_cast<float4 *>(p.x32 + at + i * 4 * p.ld) = make_float4(v[0], v[1], v[2], v[3]);
+                *reinterpret_cast<uint2 *>(p.x16 + at + i * 4 * p.ld) = four_16<false>(v);
             } else if (kThen == Then::kOut) {
-                put4_16<true>(p.out + x.z * p.out_stride + row * p.ldo + col, v, left);
+                put4_16<true>(p.out + x.z * p.out_stride + to + i * 4 * p.ldo, v, left);
             } else {
-                const int64_t to = row * p.n + col;
 #pragma unroll
                 for (int k = 0; k < 4; k++)
-                    v[k] = fmaf(-p.lr, v[k], pre.w[kThen == Then::kMaster ? i : 0][k] * p.decay);
-                put4_f32(p.master[x.z] + to, v, left);
+                    v[k] = fmaf(-p.lr, v[k], pre.w[kMaster ? i : 0][k] * p.decay);
+                put4_f32(p.master[x.z] + to + i * 4 * p.n, v, left);
                 if (p.param[x.z])
-                    put4_16<true>(p.param[x.z] + to, v, left);
+                    put4_16<true>(p.param[x.z] + to + i * 4 * p.n, v, left);
             }
         });
     }

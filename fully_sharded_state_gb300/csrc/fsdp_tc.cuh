@@ -47,11 +47,14 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 
 // One arrival on the barrier at the same place in CTA `rank` of the cluster.
+// Of CTA scope: what it orders is the reads of tensor memory before it, by the
+// tcgen05 fence. A release at cluster scope would also wait until the
+// epilogue's stores to memory are done, some microseconds for every tile.
 __device__ __forceinline__ void bar_arrive_at(uint64_t *bar, uint32_t rank)
 {
     uint32_t a;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr(bar)), "r"(rank));
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(a) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(a) : "memory");
 }
 __device__ __forceinline__ uint32_t cluster_rank()
 {
@@ -280,17 +283,13 @@ struct Slot {
     unsigned char *stage;  // the warp's 4 KB: 32 rows of 128 bytes
     int lane;
     bool mirror;  // sym: also store the transposed element
-    bool empty;   // K was empty: the accumulator holds nothing, the sum is 0
+    bool empty;   // K was empty (only a dynamic one can be): the accumulator
+                  // holds nothing, the sum is 0
 
     __device__ __forceinline__ void load(int chunk, float (&v)[32]) const
     {
         __syncwarp();  // the load is the whole warp's
         tmem_load32(tmem + chunk * 32, v);
-        if (empty) {
-#pragma unroll
-            for (int i = 0; i < 32; i++)
-                v[i] = 0.0f;
-        }
     }
 
     // 16-byte piece c (0..7) of line r (0..31) of the stage. Pieces of a line
@@ -306,18 +305,43 @@ struct Slot {
     __device__ __forceinline__ int group_row(int i) const { return row - lane + i * 4 + lane / 8; }
     __device__ __forceinline__ int group_col(int chunk) const { return col + chunk * 32 + lane % 8 * 4; }
 
+    // A chunk of the accumulator into the warp's stage.
+    __device__ __forceinline__ void put_stage(int chunk, float (&mine)[32]) const
+    {
+        load(chunk, mine);
+        if (empty) {
+#pragma unroll
+            for (int c = 0; c < 8; c++)
+                *piece(lane, c) = make_uint4(0, 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int c = 0; c < 8; c++)
+                *piece(lane, c) = make_uint4(__float_as_uint(mine[4 * c]), __float_as_uint(mine[4 * c + 1]),
+                                             __float_as_uint(mine[4 * c + 2]), __float_as_uint(mine[4 * c + 3]));
+        }
+        __syncwarp();
+    }
+
+    // Calls f(r, v) for every row of a chunk, v the value of this lane's
+    // column: for rows that do not start on whole groups.
+    template <class F>
+    __device__ __forceinline__ void by_rows(int chunk, F f) const
+    {
+        float mine[32];
+        put_stage(chunk, mine);
+#pragma unroll 8
+        for (int r = 0; r < 32; r++)
+            f(r, reinterpret_cast<const float *>(piece(r, lane / 4))[lane % 4]);
+        __syncwarp();
+    }
+
     // Takes a chunk of the accumulator to the lanes by groups and calls
     // f(i, v) for each of this lane's 8. What f leaves in v is back in `mine`
     // (the thread's own row of the chunk) after it, where kBack is set.
     template <bool kBack, class F>
     __device__ __forceinline__ void across(int chunk, float (&mine)[32], F f) const
     {
-        load(chunk, mine);
-#pragma unroll
-        for (int c = 0; c < 8; c++)
-            *piece(lane, c) = make_uint4(__float_as_uint(mine[4 * c]), __float_as_uint(mine[4 * c + 1]),
-                                         __float_as_uint(mine[4 * c + 2]), __float_as_uint(mine[4 * c + 3]));
-        __syncwarp();
+        put_stage(chunk, mine);
 #pragma unroll
         for (int i = 0; i < 8; i++) {
             uint4 *at = piece(i * 4 + lane / 8, lane % 8);
@@ -720,27 +744,30 @@ __device__ __forceinline__ bool aligned(const void *p, unsigned bytes)
     return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
 }
 
+// Whether all rows from p on, ld 16-bit elements apart, hold whole groups of 4.
+__device__ __forceinline__ bool groups_of_4(const uint16_t *p, int64_t ld)
+{
+    return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * 2)) & 7) == 0;
+}
+template <bool kBf16>
+__device__ __forceinline__ uint2 four_16(const float (&v)[4])
+{
+    return kBf16 ? make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]))
+                 : make_uint2(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]));
+}
 // 4 adjacent elements of a row, of which the first n exist; one access where
 // all do and p is aligned.
 template <bool kBf16>
 __device__ __forceinline__ void put4_16(uint16_t *p, const float (&v)[4], int n)
 {
     if (n >= 4 && aligned(p, 8)) {
-        *reinterpret_cast<uint2 *>(p) = kBf16 ? make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]))
-                                              : make_uint2(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]));
+        *reinterpret_cast<uint2 *>(p) = four_16<kBf16>(v);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; i++)
             if (i < n)
                 p[i] = kBf16 ? to_bf16(v[i]) : __half_as_ushort(__float2half_rn(v[i]));
     }
-}
-__device__ __forceinline__ void get4_f16(const uint16_t *p, float (&v)[4])  // 8-byte aligned
-{
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
-    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&u.x));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&u.y));
-    v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
 }
 __device__ __forceinline__ void get4_f32(const float *p, float (&v)[4], int n)
 {
