@@ -17,73 +17,12 @@
 // of rank 16 under 1 % noise comes out 4e-2 off (its small directions grow by
 // a per step, and the rounding with them); so it is 4e-4 off. Full-rank
 // gradients: 1.5e-3 either way.
-#include "fsdp_tc.cuh"
+#include "fsdp_muon.cuh"
 
 namespace fsdp {
 namespace {
 
 using namespace tc;
-
-constexpr int kStartThreads = 256;
-constexpr int kMaxParts = 1024;  // partial sums of one matrix's norm
-
-__device__ __forceinline__ float block_sum(float v, float *sh)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (threadIdx.x % 32 == 0)
-        sh[threadIdx.x / 32] = v;
-    __syncthreads();
-    v = sh[0];
-    for (int i = 1; i < kStartThreads / 32; i++)
-        v += sh[i];
-    __syncthreads();
-    return v;
-}
-
-// 8 elements of a row, from column c on; zeros past the end.
-__device__ __forceinline__ void load8(const void *base, int64_t at, int left, bool bf16, float (&v)[8])
-{
-    if (bf16) {
-        const uint16_t *p = static_cast<const uint16_t *>(base) + at;
-        if (left >= 8 && aligned(p, 16)) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(p);
-            const uint32_t *w = reinterpret_cast<const uint32_t *>(&u);
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                v[2 * i] = __uint_as_float(w[i] << 16);
-                v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; i++)
-                v[i] = i < left ? bf16_at(p + i) : 0.0f;
-        }
-    } else {
-        const float *p = static_cast<const float *>(base) + at;
-        if (left >= 8 && aligned(p, 16)) {
-            const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; i++)
-                v[i] = i < left ? p[i] : 0.0f;
-        }
-    }
-}
-__device__ __forceinline__ void store8(float *p, int left, const float (&v)[8])
-{
-    if (left >= 8 && aligned(p, 16)) {
-        reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; i++)
-            if (i < left)
-                p[i] = v[i];
-    }
-}
 
 struct StartParams {
     int m, n, groups;       // groups of 8 columns per row
@@ -402,41 +341,19 @@ __global__ void __launch_bounds__(kStartThreads) finish_kernel(const __grid_cons
     }
 }
 
-struct Plan {
-    int64_t ldx, ldk, k;
-    float *x32, *partial, *inv;
-    uint16_t *x16[2], *s, *p;
-    int64_t bytes;
-};
-
-Plan plan_of(int64_t batch, int64_t m, int64_t n, void *base)
-{
-    Plan q{};
-    q.k = m < n ? m : n;
-    q.ldx = ceil_to(n, 16);
-    q.ldk = ceil_to(q.k, 16);
-    Carver c(base);
-    q.partial = c.take<float>(batch * kMaxParts);
-    q.inv = c.take<float>(batch);
-    q.x32 = c.take<float>(batch * m * q.ldx);
-    q.x16[0] = c.take<uint16_t>(batch * m * q.ldx);
-    q.x16[1] = c.take<uint16_t>(batch * m * q.ldx);
-    q.s = c.take<uint16_t>(batch * q.k * q.ldk);
-    q.p = c.take<uint16_t>(batch * q.k * q.ldk);
-    q.bytes = c.used();
-    return q;
-}
-
 }  // namespace
 
-int64_t schulz_workspace(int64_t batch, int64_t m, int64_t n) { return plan_of(batch, m, n, nullptr).bytes; }
+int64_t schulz_workspace(int64_t batch, int64_t m, int64_t n) { return schulz_plan(batch, m, n, nullptr).bytes; }
 
 fsdp_status launch_newton_schulz(const SchulzArgs &a, void *workspace, int dev, void *stream)
 {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool muon = a.grads != nullptr;
     const int sms = device_sms(dev);
-    const Plan q = plan_of(a.batch, a.m, a.n, workspace);
+    const int64_t team = team_clocks(a, dev);
+    if (team >= 0 && team < product_clocks(a, sms))
+        return launch_team(a, workspace, dev, stream);
+    const SchulzPlan q = schulz_plan(a.batch, a.m, a.n, workspace);
     const int batch = (int)a.batch, m = (int)a.m, n = (int)a.n;
     fsdp_status st;
 

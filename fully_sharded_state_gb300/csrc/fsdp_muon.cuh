@@ -1,0 +1,132 @@
+// fsdp_muon.cuh -- what the two forms of the Newton-Schulz iteration share
+// (fsdp_muon.cu, fsdp_team.cu): the workspace and the reading of gradients.
+#pragma once
+
+#include "fsdp_tc.cuh"
+
+namespace fsdp {
+
+// One kernel for all products of small matrices (fsdp_team.cu). Estimated
+// clocks, or -1 where the matrices do not fit it.
+int64_t team_clocks(const SchulzArgs &a, int dev);
+fsdp_status launch_team(const SchulzArgs &a, void *workspace, int dev, void *stream);
+
+namespace {
+
+using namespace tc;
+
+constexpr int kStartThreads = 256;
+constexpr int kMaxParts = 1024;  // partial sums of one matrix's norm
+
+__device__ __forceinline__ float block_sum(float v, float *sh)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (threadIdx.x % 32 == 0)
+        sh[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = sh[0];
+    for (int i = 1; i < kStartThreads / 32; i++)
+        v += sh[i];
+    __syncthreads();
+    return v;
+}
+
+// 8 elements of a row, from column c on; zeros past the end.
+__device__ __forceinline__ void load8(const void *base, int64_t at, int left, bool bf16, float (&v)[8])
+{
+    if (bf16) {
+        const uint16_t *p = static_cast<const uint16_t *>(base) + at;
+        if (left >= 8 && aligned(p, 16)) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(p);
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(&u);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                v[2 * i] = __uint_as_float(w[i] << 16);
+                v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                v[i] = i < left ? bf16_at(p + i) : 0.0f;
+        }
+    } else {
+        const float *p = static_cast<const float *>(base) + at;
+        if (left >= 8 && aligned(p, 16)) {
+            const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                v[i] = i < left ? p[i] : 0.0f;
+        }
+    }
+}
+__device__ __forceinline__ void store8(float *p, int left, const float (&v)[8])
+{
+    if (left >= 8 && aligned(p, 16)) {
+        reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (i < left)
+                p[i] = v[i];
+    }
+}
+
+// The workspace of one call.
+struct SchulzPlan {
+    int64_t ldx, ldk, k;
+    float *x32, *partial, *inv;
+    unsigned *arrived;  // of each team
+    uint16_t *x16[2], *s, *p;
+    int64_t bytes;
+};
+
+inline SchulzPlan schulz_plan(int64_t batch, int64_t m, int64_t n, void *base)
+{
+    SchulzPlan q{};
+    q.k = m < n ? m : n;
+    q.ldx = ceil_to(n, 16);
+    q.ldk = ceil_to(q.k, 16);
+    Carver c(base);
+    q.partial = c.take<float>(batch * kMaxParts);
+    q.inv = c.take<float>(batch);
+    q.arrived = c.take<unsigned>(kMaxParts);
+    q.x32 = c.take<float>(batch * m * q.ldx);
+    q.x16[0] = c.take<uint16_t>(batch * m * q.ldx);
+    q.x16[1] = c.take<uint16_t>(batch * m * q.ldx);
+    q.s = c.take<uint16_t>(batch * q.k * q.ldk);
+    q.p = c.take<uint16_t>(batch * q.k * q.ldk);
+    q.bytes = c.used();
+    return q;
+}
+
+// Clocks of `steps` steps as one kernel per product: the products' own and,
+// for each, a kernel's start and end.
+constexpr int64_t kLaunchClocks = 6000;
+inline int64_t product_clocks(const SchulzArgs &a, int sms)
+{
+    const int64_t k = a.m < a.n ? a.m : a.n, l = a.m < a.n ? a.n : a.m;
+    Shape s{};
+    s.batch = (int)a.batch;
+    s.splits = 1;
+    s.sym = 1;
+    s.M = s.N = (int)k;
+    s.K = (int)l;
+    s.split_blocks = (int)((l + kBK - 1) / kBK);
+    int64_t t = best_form(s, sms, 64).cost;
+    s.K = (int)k;
+    s.split_blocks = (int)((k + kBK - 1) / kBK);
+    t += best_form(s, sms, 64).cost;
+    s.sym = 0;
+    s.M = (int)a.m;
+    s.N = (int)a.n;
+    t += best_form(s, sms, 64).cost;
+    return a.steps * (t + 3 * kLaunchClocks);
+}
+
+}  // namespace
+}  // namespace fsdp

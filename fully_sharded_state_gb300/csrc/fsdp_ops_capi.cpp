@@ -16,6 +16,7 @@ namespace fsdp {
 cudaError_t norm_wait_timeouts(unsigned long long *n);
 cudaError_t loss_wait_timeouts(unsigned long long *n);
 cudaError_t muon_wait_timeouts(unsigned long long *n);
+cudaError_t team_wait_timeouts(unsigned long long *n);
 
 int device_sms(int dev)
 {
@@ -474,7 +475,7 @@ fsdp_status fsdp_ops_wait_timeouts(int device, uint64_t *count)
         return set_error(FSDP_ECUDA, "%s: cudaGetDevice: %s", fn, cudaGetErrorString(err));
     if (prev != device && (err = cudaSetDevice(device)) != cudaSuccess)
         return set_error(FSDP_ECUDA, "%s: cudaSetDevice(%d): %s", fn, device, cudaGetErrorString(err));
-    unsigned long long n[3] = {0, 0, 0};
+    unsigned long long n[4] = {0, 0, 0, 0};
     err = cudaDeviceSynchronize();
     if (err == cudaSuccess)
         err = norm_wait_timeouts(&n[0]);
@@ -482,11 +483,13 @@ fsdp_status fsdp_ops_wait_timeouts(int device, uint64_t *count)
         err = loss_wait_timeouts(&n[1]);
     if (err == cudaSuccess)
         err = muon_wait_timeouts(&n[2]);
+    if (err == cudaSuccess)
+        err = team_wait_timeouts(&n[3]);
     if (prev != device)
         cudaSetDevice(prev);
     if (err != cudaSuccess)
         return set_error(FSDP_ECUDA, "%s: %s", fn, cudaGetErrorString(err));
-    *count = n[0] + n[1] + n[2];
+    *count = n[0] + n[1] + n[2] + n[3];
     return FSDP_OK;
 }
 

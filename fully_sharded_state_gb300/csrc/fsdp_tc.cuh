@@ -172,23 +172,44 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32])
         v[i] = __uint_as_float(r[i]);
 }
 
+// The reverse: thread t's values become row t's.
+__device__ __forceinline__ void tmem_store32(uint32_t addr, const float (&v)[32])
+{
+    uint32_t r[32];
+#pragma unroll
+    for (int i = 0; i < 32; i++)
+        r[i] = __float_as_uint(v[i]);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+        "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+        "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
 // Shared-memory matrix descriptor of a 128-byte swizzled operand tile.
 //   K adjacent: rows of 128 bytes (64 of K); 8-row groups 1024 bytes apart.
 //     The next 16 of K start 32 bytes on.
 //   rows adjacent: blocks of [64 of K][64 rows] (8192 bytes, one after the
 //     other along the rows); 8-K groups 1024 bytes apart. The next 16 of K
 //     start 2048 bytes on.
-template <bool kMN>
-__device__ __forceinline__ uint64_t operand_desc(uint32_t addr)
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool mn)
 {
-    const uint64_t lead = kMN ? (kBK * 128) >> 4 : 1;
+    const uint64_t lead = mn ? (kBK * 128) >> 4 : 1;
     return (uint64_t)((addr >> 4) & 0x3FFF) | (lead << 16) | ((uint64_t)(1024 >> 4) << 32) |
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
-template <bool kMN>
-__host__ __device__ constexpr uint32_t k_step()
+__host__ __device__ constexpr uint32_t k_step(bool mn) { return (mn ? 2048 : 32) >> 4; }
+
+// Instruction descriptor: D fp32; A, B bf16 (1) or fp16 (0); majors; N / 8; M / 16.
+__host__ __device__ constexpr uint32_t instruction(int rows, int cols, bool bf16, bool a_mn, bool b_mn)
 {
-    return (kMN ? 2048 : 32) >> 4;
+    return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) |
+           ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(cols / 8) << 17) | ((uint32_t)(rows / 16) << 24);
 }
 
 // ---------------------------------------------------------------- shapes ----
@@ -305,22 +326,28 @@ struct Slot {
     __device__ __forceinline__ int group_row(int i) const { return row - lane + i * 4 + lane / 8; }
     __device__ __forceinline__ int group_col(int chunk) const { return col + chunk * 32 + lane % 8 * 4; }
 
-    // A chunk of the accumulator into the warp's stage.
-    __device__ __forceinline__ void put_stage(int chunk, float (&mine)[32]) const
+    // The threads' own rows of 32 values into the warp's stage.
+    __device__ __forceinline__ void put_stage(const float (&mine)[32]) const
     {
-        load(chunk, mine);
-        if (empty) {
 #pragma unroll
-            for (int c = 0; c < 8; c++)
-                *piece(lane, c) = make_uint4(0, 0, 0, 0);
-        } else {
+        for (int c = 0; c < 8; c++)
+            *piece(lane, c) = make_uint4(__float_as_uint(mine[4 * c]), __float_as_uint(mine[4 * c + 1]),
+                                         __float_as_uint(mine[4 * c + 2]), __float_as_uint(mine[4 * c + 3]));
+        __syncwarp();
+    }
+    __device__ __forceinline__ void get_stage(float (&mine)[32]) const
+    {
 #pragma unroll
-            for (int c = 0; c < 8; c++)
-                *piece(lane, c) = make_uint4(__float_as_uint(mine[4 * c]), __float_as_uint(mine[4 * c + 1]),
-                                             __float_as_uint(mine[4 * c + 2]), __float_as_uint(mine[4 * c + 3]));
+        for (int c = 0; c < 8; c++) {
+            const uint4 u = *piece(lane, c);
+            mine[4 * c] = __uint_as_float(u.x);
+            mine[4 * c + 1] = __uint_as_float(u.y);
+            mine[4 * c + 2] = __uint_as_float(u.z);
+            mine[4 * c + 3] = __uint_as_float(u.w);
         }
         __syncwarp();
     }
+    __device__ __forceinline__ uint4 *group(int i) const { return piece(i * 4 + lane / 8, lane % 8); }
 
     // Calls f(r, v) for every row of a chunk, v the value of this lane's
     // column: for rows that do not start on whole groups.
@@ -328,42 +355,64 @@ struct Slot {
     __device__ __forceinline__ void by_rows(int chunk, F f) const
     {
         float mine[32];
-        put_stage(chunk, mine);
+        load_sum(chunk, mine);
+        put_stage(mine);
 #pragma unroll 8
         for (int r = 0; r < 32; r++)
             f(r, reinterpret_cast<const float *>(piece(r, lane / 4))[lane % 4]);
         __syncwarp();
     }
 
-    // Takes a chunk of the accumulator to the lanes by groups and calls
-    // f(i, v) for each of this lane's 8. What f leaves in v is back in `mine`
-    // (the thread's own row of the chunk) after it, where kBack is set.
-    template <bool kBack, class F>
-    __device__ __forceinline__ void across(int chunk, float (&mine)[32], F f) const
+    __device__ __forceinline__ void load_sum(int chunk, float (&mine)[32]) const
     {
-        put_stage(chunk, mine);
+        load(chunk, mine);
+        if (empty) {
+#pragma unroll
+            for (int i = 0; i < 32; i++)
+                mine[i] = 0.0f;
+        }
+    }
+
+    // Takes the threads' own rows of a chunk to the lanes by groups and calls
+    // f(i, v) for each of this lane's 8. What f leaves in v is back in `mine`
+    // after it, where kBack is set.
+    template <bool kBack, class F>
+    __device__ __forceinline__ void spread(float (&mine)[32], F f) const
+    {
+        put_stage(mine);
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-            uint4 *at = piece(i * 4 + lane / 8, lane % 8);
-            const uint4 u = *at;
+            const uint4 u = *group(i);
             float v[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
             f(i, v);
             if (kBack)
-                *at = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                                 __float_as_uint(v[3]));
+                *group(i) = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                       __float_as_uint(v[3]));
         }
         __syncwarp();
-        if (kBack) {
+        if (kBack)
+            get_stage(mine);
+    }
+    template <bool kBack, class F>
+    __device__ __forceinline__ void across(int chunk, float (&mine)[32], F f) const
+    {
+        load_sum(chunk, mine);
+        spread<kBack>(mine, f);
+    }
+    // The reverse: f(i, v) makes this lane's 8 groups, `mine` becomes the
+    // thread's own row of them.
+    template <class F>
+    __device__ __forceinline__ void collect(float (&mine)[32], F f) const
+    {
 #pragma unroll
-            for (int c = 0; c < 8; c++) {
-                const uint4 u = *piece(lane, c);
-                mine[4 * c] = __uint_as_float(u.x);
-                mine[4 * c + 1] = __uint_as_float(u.y);
-                mine[4 * c + 2] = __uint_as_float(u.z);
-                mine[4 * c + 3] = __uint_as_float(u.w);
-            }
-            __syncwarp();
+        for (int i = 0; i < 8; i++) {
+            float v[4];
+            f(i, v);
+            *group(i) = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                   __float_as_uint(v[3]));
         }
+        __syncwarp();
+        get_stage(mine);
     }
 };
 
@@ -517,10 +566,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     fence_after();
                     const uint32_t a = saddr(ring + stage * R::kStageBytes);
-                    uint64_t da = operand_desc<kAMN>(a), db = operand_desc<kBMN>(a + R::kBytesA);
+                    const uint64_t da = operand_desc(a, kAMN), db = operand_desc(a + R::kBytesA, kBMN);
 #pragma unroll
                     for (int k = 0; k < kBK / 16; k++)
-                        mma_f16<kCtas>(d, da + k * k_step<kAMN>(), db + k * k_step<kBMN>(), s.idesc,
+                        mma_f16<kCtas>(d, da + k * k_step(kAMN), db + k * k_step(kBMN), s.idesc,
                                        kb > 0 || k > 0);
                     mma_commit<kCtas>(empty + stage);
                     if (++stage == R::kStages) {
@@ -654,9 +703,7 @@ fsdp_status product_as(Shape s, const Operand &a, const Operand &b, bool bf16, c
         st = make_map(&mb, b, s.batch, kBMN ? kBK : R::kRowsB, bf16);
     if (st != FSDP_OK)
         return st;
-    // D fp32; A, B bf16 (1) or fp16 (0); majors; N / 8; M / 16
-    s.idesc = (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((kAMN ? 1u : 0u) << 15) |
-              ((kBMN ? 1u : 0u) << 16) | ((uint32_t)(TN / 8) << 17) | ((uint32_t)(kTM * kCtas / 16) << 24);
+    s.idesc = instruction(kTM * kCtas, TN, bf16, kAMN, kBMN);
     const int64_t most = device_sms(dev) / kCtas;
     return launch(what, kernel, dim3((unsigned)((tiles < most ? tiles : most) * kCtas)), kThreads, R::kSmem, stream,
                   kCtas, ma, mb, s, ep);
@@ -673,53 +720,62 @@ inline int64_t count_tiles(const Shape &s, int64_t rows, int64_t cols)
     return n * s.batch * s.splits;
 }
 
-// Launches D = A B^T. `s` needs M, N, K, batch, sym, dyn* and, for split
-// sums, splits and split_blocks; the rest is filled in here.
-//
-// The tile: the largest output tile makes the fewest trips to L2 per product,
+// The tile of a product. The largest output tile makes the fewest trips to L2,
 // a smaller one spreads a small product over more multiprocessors. Taken is
 // the one with the least estimate of waves * (K blocks * clocks of one + those
 // of a tile's start and end), where a block's clocks are those of its MMAs
 // (2 per column of the tile) or of its loads at 90 bytes per clock.
+struct Form {
+    int ctas, tn;
+    int64_t tiles, cost;  // clocks
+};
+inline int64_t block_clocks(int ctas, int tn)
+{
+    const int64_t loads = (kTM + tn / ctas) * 128 / 90, mmas = 2 * tn;
+    return loads > mmas ? loads : mmas;
+}
+inline Form best_form(const Shape &s, int64_t sms, int least_tn)
+{
+    const int64_t blocks = (s.K + kBK - 1) / kBK;
+    const int64_t nk = s.split_blocks < blocks ? s.split_blocks : blocks;
+    Form best{0, 0, 0, 0};
+    static const int kForms[4][2] = {{2, 256}, {1, 256}, {1, 128}, {1, 64}};
+    for (const int *f : kForms) {
+        if (f[1] < least_tn)
+            continue;
+        Form g{f[0], f[1], count_tiles(s, kTM * f[0], f[1]), 0};
+        const int64_t slots = sms / g.ctas < 1 ? 1 : sms / g.ctas, waves = (g.tiles + slots - 1) / slots;
+        g.cost = waves * (nk * block_clocks(g.ctas, g.tn) + 1500 + 8 * g.tn);
+        if (best.tn == 0 || g.cost < best.cost)
+            best = g;
+    }
+    return best;
+}
+
+// Launches D = A B^T. `s` needs M, N, K, batch, sym, dyn* and, for split
+// sums, splits and split_blocks; the rest is filled in here.
 template <bool kAMN, bool kBMN, class Epi>
 fsdp_status product(Shape s, const Operand &a, const Operand &b, bool bf16, const typename Epi::Params &ep,
                     int dev, cudaStream_t stream, const char *what)
 {
-    const int64_t blocks = (s.K + kBK - 1) / kBK;
     if (s.splits < 1)
         s.splits = 1;
     if (s.splits == 1)
-        s.split_blocks = (int)blocks;
+        s.split_blocks = (s.K + kBK - 1) / kBK;
     s.group = s.group > 0 ? s.group : 8;
-    const int64_t sms = device_sms(dev);
-    const int64_t nk = s.split_blocks < blocks ? s.split_blocks : blocks;
-    struct Form {
-        int ctas, tn;
-        int64_t tiles, cost;
-    } forms[4] = {{2, 256, 0, 0}, {1, 256, 0, 0}, {1, 128, 0, 0}, {1, 64, 0, 0}};
-    const Form *best = nullptr;
-    for (Form &f : forms) {
-        if (f.tn < Epi::kLeastTN)
-            continue;
-        f.tiles = count_tiles(s, kTM * f.ctas, f.tn);
-        const int64_t slots = sms / f.ctas, waves = (f.tiles + slots - 1) / slots;
-        const int64_t loads = (kTM + f.tn / f.ctas) * 128 / 90, mmas = 2 * f.tn;
-        f.cost = waves * (nk * (loads > mmas ? loads : mmas) + 1500 + 8 * f.tn);
-        if (!best || f.cost < best->cost)
-            best = &f;
-    }
-    if (best->tiles < 1)
+    const Form best = best_form(s, device_sms(dev), Epi::kLeastTN);
+    if (best.tiles < 1)
         return FSDP_OK;
-    if (best->tiles >= (int64_t)1 << 31)
-        return set_error(FSDP_ERANGE, "%s: %lld tiles", what, (long long)best->tiles);
-    if (best->ctas == 2)
-        return product_as<2, 256, kAMN, kBMN, Epi>(s, a, b, bf16, ep, best->tiles, dev, stream, what);
-    if (best->tn == 256)
-        return product_as<1, 256, kAMN, kBMN, Epi>(s, a, b, bf16, ep, best->tiles, dev, stream, what);
+    if (best.tiles >= (int64_t)1 << 31)
+        return set_error(FSDP_ERANGE, "%s: %lld tiles", what, (long long)best.tiles);
+    if (best.ctas == 2)
+        return product_as<2, 256, kAMN, kBMN, Epi>(s, a, b, bf16, ep, best.tiles, dev, stream, what);
+    if (best.tn == 256)
+        return product_as<1, 256, kAMN, kBMN, Epi>(s, a, b, bf16, ep, best.tiles, dev, stream, what);
     if constexpr (Epi::kLeastTN <= 64) {
-        if (best->tn == 128)
-            return product_as<1, 128, kAMN, kBMN, Epi>(s, a, b, bf16, ep, best->tiles, dev, stream, what);
-        return product_as<1, 64, kAMN, kBMN, Epi>(s, a, b, bf16, ep, best->tiles, dev, stream, what);
+        if (best.tn == 128)
+            return product_as<1, 128, kAMN, kBMN, Epi>(s, a, b, bf16, ep, best.tiles, dev, stream, what);
+        return product_as<1, 64, kAMN, kBMN, Epi>(s, a, b, bf16, ep, best.tiles, dev, stream, what);
     }
     return FSDP_OK;
 }
