@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(const uint16_t *src, int
 // from tensor memory twice: for the maximum, then for the exponentials. The
 // exponentials leave by the warp's stage, 64 columns of 32 rows at a time.
 struct LogitsEpi {
-    static constexpr int kLeastTN = kTileN;
+    static constexpr int kLeastTN = kTileN, kBytes = 8;  // 2, and the time of the exponentials
     struct Params {
         uint16_t *e;      // NULL: loss alone
         int64_t lde;
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowsParams p)
 
 // dhidden rows back at their own places, bf16.
 struct HiddenEpi {
-    static constexpr int kLeastTN = 64;
+    static constexpr int kLeastTN = 64, kBytes = 2;
     static constexpr bool kAhead = false;
     struct Params {
         uint16_t *out;
@@ -443,7 +443,7 @@ struct HiddenEpi {
 
 // Partial sums of split products, fp32.
 struct PartEpi {
-    static constexpr int kLeastTN = 64;
+    static constexpr int kLeastTN = 64, kBytes = 4;
     static constexpr bool kAhead = false;
     struct Params {
         float *out;  // [splits][rows][ld], ld a multiple of 8
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(128) join_hidden_kernel(const float *parts, in
 
 // dweight, over the pieces of the rows in fp32 where there are several.
 struct WeightEpi {
-    static constexpr int kLeastTN = 64;
+    static constexpr int kLeastTN = 64, kBytes = 2;
     static constexpr bool kAhead = true;
     struct Params {
         uint16_t *out;

@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kStartThreads) scale_kernel(const float *x32, 
 // S, or P = b S + c S^2 (from != NULL), in fp16, both triangles. Strides are
 // multiples of 16, so groups of 4 and pairs of rows stay inside a padded row.
 struct SquareEpi {
-    static constexpr int kLeastTN = 64;
+    static constexpr int kLeastTN = 64, kBytes = kSquareBytes;
     static constexpr bool kAhead = true;
     struct Params {
         uint16_t *out;
@@ -250,7 +250,7 @@ struct StepParams {
 
 template <Then kThen>
 struct StepEpi {
-    static constexpr int kLeastTN = 64;
+    static constexpr int kLeastTN = 64, kBytes = kStepBytes;
     static constexpr bool kAhead = kThen != Then::kMaster;  // it has twice the reads: registers
     using Params = StepParams;
     static constexpr bool kMaster = kThen == Then::kMaster;

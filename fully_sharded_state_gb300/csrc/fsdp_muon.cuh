@@ -106,7 +106,8 @@ inline SchulzPlan schulz_plan(int64_t batch, int64_t m, int64_t n, void *base)
 
 // Clocks of `steps` steps as one kernel per product: the products' own and,
 // for each, a kernel's start and end.
-constexpr int64_t kLaunchClocks = 6000;
+constexpr int64_t kLaunchClocks = 4500;
+constexpr int kSquareBytes = 5, kStepBytes = 10;  // of an epilogue, per element
 inline int64_t product_clocks(const SchulzArgs &a, int sms)
 {
     const int64_t k = a.m < a.n ? a.m : a.n, l = a.m < a.n ? a.n : a.m;
@@ -117,14 +118,14 @@ inline int64_t product_clocks(const SchulzArgs &a, int sms)
     s.M = s.N = (int)k;
     s.K = (int)l;
     s.split_blocks = (int)((l + kBK - 1) / kBK);
-    int64_t t = best_form(s, sms, 64).cost;
+    int64_t t = best_form(s, sms, 64, kSquareBytes).cost;
     s.K = (int)k;
     s.split_blocks = (int)((k + kBK - 1) / kBK);
-    t += best_form(s, sms, 64).cost;
+    t += best_form(s, sms, 64, kSquareBytes).cost;
     s.sym = 0;
     s.M = (int)a.m;
     s.N = (int)a.n;
-    t += best_form(s, sms, 64).cost;
+    t += best_form(s, sms, 64, kStepBytes).cost;
     return a.steps * (t + 3 * kLaunchClocks);
 }
 

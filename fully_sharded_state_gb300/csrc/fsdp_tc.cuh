@@ -68,6 +68,21 @@ __device__ __forceinline__ void cluster_sync()
                      : "memory");
 }
 
+// One lane of a converged warp. The warps that issue copies and MMAs run their
+// loops whole and elect a lane for the instruction alone: addresses and
+// descriptors stay in uniform registers, which these instructions take. With
+// the loop inside `if (lane == 0)`, four MMAs and their commit took 220 ns.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // ------------------------------------------------------------ copies, MMA ----
 
 // A box of a 3-D tensor map (x innermost) into shared memory, completing on
@@ -418,6 +433,7 @@ struct Slot {
 
 // An epilogue E has
 //   Params, kLeastTN   its arguments; the narrowest tile it takes
+//   kBytes             what it moves per element, for the choice of the tile
 //   Pre                what it reads from memory for one chunk, in registers
 //   fetch(p, x, chunk, pre)   starts those reads
 //   chunk(p, x, chunk, pre)   finishes a chunk with them
@@ -517,67 +533,75 @@ __global__ void __launch_bounds__(kThreads, 1)
     const T tiles(s);
 
     if (warp == 0) {
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            for (uint32_t t = first; ok && t < tiles.total; t += step) {
-                const Work w = tiles.at(s, t);
-                const int row = w.row + (int)rank * kTM, col = w.col + (int)rank * R::kRowsB;
-                for (int kb = 0; kb < w.nkb; kb++) {
-                    if (!(ok = bar_wait(empty + stage, phase ^ 1)))
-                        break;
+        int stage = 0;
+        uint32_t phase = 0;
+        for (uint32_t t = first; ok && t < tiles.total; t += step) {
+            const Work w = tiles.at(s, t);
+            const int row = w.row + (int)rank * kTM, col = w.col + (int)rank * R::kRowsB;
+            for (int kb = 0; kb < w.nkb; kb++) {
+                if (!(ok = warp_wait(empty + stage, phase ^ 1)))
+                    break;
+                if (elect_one()) {
                     if (rank == 0)
                         bar_expect(full + stage, R::kStageBytes * kCtas);
                     unsigned char *a = ring + stage * R::kStageBytes, *b = a + R::kBytesA;
                     const int k = (w.kb + kb) * kBK;
                     if (kAMN) {
+#pragma unroll
                         for (int i = 0; i < kTM / 64; i++)
                             tma_load<kCtas>(a + i * 8192, &map_a, row + i * 64, k, w.z, full + stage);
                     } else {
                         tma_load<kCtas>(a, &map_a, k, row, w.z, full + stage);
                     }
                     if (kBMN) {
+#pragma unroll
                         for (int i = 0; i < R::kRowsB / 64; i++)
                             tma_load<kCtas>(b + i * 8192, &map_b, col + i * 64, k, w.z, full + stage);
                     } else {
                         tma_load<kCtas>(b, &map_b, k, col, w.z, full + stage);
                     }
-                    if (++stage == R::kStages) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
+                }
+                __syncwarp();
+                if (++stage == R::kStages) {
+                    stage = 0;
+                    phase ^= 1;
                 }
             }
-            if (!ok)
-                let_copies_land();
         }
+        if (!ok)
+            let_copies_land();
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             for (uint32_t t = first; ok && t < tiles.total; t += step) {
                 const Work w = tiles.at(s, t);
-                if (!(ok = bar_wait(acc_empty + acc, acc_phase ^ 1)))
+                if (!(ok = warp_wait(acc_empty + acc, acc_phase ^ 1)))
                     break;
                 fence_after();
                 const uint32_t d = tmem + acc * TN;
                 for (int kb = 0; kb < w.nkb; kb++) {
-                    if (!(ok = bar_wait(full + stage, phase)))
+                    if (!(ok = warp_wait(full + stage, phase)))
                         break;
                     fence_after();
                     const uint32_t a = saddr(ring + stage * R::kStageBytes);
                     const uint64_t da = operand_desc(a, kAMN), db = operand_desc(a + R::kBytesA, kBMN);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kBK / 16; k++)
-                        mma_f16<kCtas>(d, da + k * k_step(kAMN), db + k * k_step(kBMN), s.idesc,
-                                       kb > 0 || k > 0);
-                    mma_commit<kCtas>(empty + stage);
+                        for (int k = 0; k < kBK / 16; k++)
+                            mma_f16<kCtas>(d, da + k * k_step(kAMN), db + k * k_step(kBMN), s.idesc,
+                                           kb > 0 || k > 0);
+                        mma_commit<kCtas>(empty + stage);
+                    }
+                    __syncwarp();
                     if (++stage == R::kStages) {
                         stage = 0;
                         phase ^= 1;
                     }
                 }
-                mma_commit<kCtas>(acc_full + acc);
+                if (elect_one())
+                    mma_commit<kCtas>(acc_full + acc);
+                __syncwarp();
                 if (++acc == 2) {
                     acc = 0;
                     acc_phase ^= 1;
@@ -722,9 +746,12 @@ inline int64_t count_tiles(const Shape &s, int64_t rows, int64_t cols)
 
 // The tile of a product. The largest output tile makes the fewest trips to L2,
 // a smaller one spreads a small product over more multiprocessors. Taken is
-// the one with the least estimate of waves * (K blocks * clocks of one + those
-// of a tile's start and end), where a block's clocks are those of its MMAs
-// (2 per column of the tile) or of its loads at 90 bytes per clock.
+// the one with the least estimate: per wave of tiles the longer of the K
+// blocks' clocks and the epilogue's, the shorter once, and a start. A block's
+// clocks are those of its MMAs (2 per column of the tile) or of its loads at
+// 90 bytes per clock; the epilogue moves its bytes at 35 per clock
+// (measured with all multiprocessors at it: 48 x 512 x 512, 10 bytes per
+// element, 11 us a wave).
 struct Form {
     int ctas, tn;
     int64_t tiles, cost;  // clocks
@@ -734,7 +761,7 @@ inline int64_t block_clocks(int ctas, int tn)
     const int64_t loads = (kTM + tn / ctas) * 128 / 90, mmas = 2 * tn;
     return loads > mmas ? loads : mmas;
 }
-inline Form best_form(const Shape &s, int64_t sms, int least_tn)
+inline Form best_form(const Shape &s, int64_t sms, int least_tn, int epi_bytes)
 {
     const int64_t blocks = (s.K + kBK - 1) / kBK;
     const int64_t nk = s.split_blocks < blocks ? s.split_blocks : blocks;
@@ -745,7 +772,8 @@ inline Form best_form(const Shape &s, int64_t sms, int least_tn)
             continue;
         Form g{f[0], f[1], count_tiles(s, kTM * f[0], f[1]), 0};
         const int64_t slots = sms / g.ctas < 1 ? 1 : sms / g.ctas, waves = (g.tiles + slots - 1) / slots;
-        g.cost = waves * (nk * block_clocks(g.ctas, g.tn) + 1500 + 8 * g.tn);
+        const int64_t mma = nk * block_clocks(g.ctas, g.tn), epi = 1000 + kTM * g.tn * epi_bytes / 35;
+        g.cost = (mma > epi ? waves * mma + epi : waves * epi + mma) + 2500;
         if (best.tn == 0 || g.cost < best.cost)
             best = g;
     }
@@ -763,7 +791,7 @@ fsdp_status product(Shape s, const Operand &a, const Operand &b, bool bf16, cons
     if (s.splits == 1)
         s.split_blocks = (s.K + kBK - 1) / kBK;
     s.group = s.group > 0 ? s.group : 8;
-    const Form best = best_form(s, device_sms(dev), Epi::kLeastTN);
+    const Form best = best_form(s, device_sms(dev), Epi::kLeastTN, Epi::kBytes);
     if (best.tiles < 1)
         return FSDP_OK;
     if (best.tiles >= (int64_t)1 << 31)

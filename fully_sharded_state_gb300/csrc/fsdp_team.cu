@@ -8,7 +8,7 @@
 // the accumulator; S, P and x in fp16 go through global memory (L2), where
 // the other blocks' TMA copies read them. After each product the team meets at
 // a counter: the writers' stores, a fence to the asynchronous proxy, one
-// atomic add per block; the thread that issues the copies waits for the sum.
+// atomic add per block; the warp that issues the copies waits for the sum.
 // All blocks are resident (cooperative launch, one per multiprocessor) and
 // every wait is bounded.
 //
@@ -157,76 +157,80 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
     };
 
     if (warp == 0) {
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            unsigned met = 0;
-            for (int z = team; ok && z < q.batch; z += q.teams, met += meetings) {
-                for (int t = 0; ok && t < 3 * q.steps; t++) {
-                    if (!(ok = team_wait(arrived, (unsigned)q.size * (met + 2 + t))))
+        int stage = 0;
+        uint32_t phase = 0;
+        unsigned met = 0;
+        for (int z = team; ok && z < q.batch; z += q.teams, met += meetings) {
+            for (int t = 0; ok && t < 3 * q.steps; t++) {
+                if (!(ok = __all_sync(0xffffffffu, team_wait(arrived, (unsigned)q.size * (met + 2 + t)))))
+                    break;
+                const int which = t % 3;
+                if (which < 2 && !has_k)
+                    continue;
+                async_fence();
+                const CUtensorMap *x = t / 3 % 2 ? &map_x1 : &map_x0;
+                const Side a = which == 0   ? Side{x, !q.wide}
+                               : which == 1 ? Side{&map_s, false}
+                               : q.wide     ? Side{&map_p, false}
+                                            : Side{x, false};
+                const Side b = which == 0   ? Side{x, !q.wide}
+                               : which == 1 ? Side{&map_s, false}
+                               : q.wide     ? Side{x, true}
+                                            : Side{&map_p, false};
+                const int row = which < 2 ? k_row : x_row, col = which < 2 ? k_col : x_col;
+                const int nk = blocks_of(which);
+                for (int kb = 0; kb < nk; kb++) {
+                    if (!(ok = warp_wait(empty + stage, phase ^ 1)))
                         break;
-                    const int which = t % 3;
-                    if (which < 2 && !has_k)
-                        continue;
-                    async_fence();
-                    const CUtensorMap *x = t / 3 % 2 ? &map_x1 : &map_x0;
-                    const Side a = which == 0   ? Side{x, !q.wide}
-                                   : which == 1 ? Side{&map_s, false}
-                                   : q.wide     ? Side{&map_p, false}
-                                                : Side{x, false};
-                    const Side b = which == 0   ? Side{x, !q.wide}
-                                   : which == 1 ? Side{&map_s, false}
-                                   : q.wide     ? Side{x, true}
-                                                : Side{&map_p, false};
-                    const int row = which < 2 ? k_row : x_row, col = which < 2 ? k_col : x_col;
-                    const int nk = blocks_of(which);
-                    for (int kb = 0; kb < nk; kb++) {
-                        if (!(ok = bar_wait(empty + stage, phase ^ 1)))
-                            break;
+                    if (elect_one()) {
                         bar_expect(full + stage, R::kStageBytes);
                         unsigned char *d = ring + stage * R::kStageBytes;
                         load_side<kTM>(d, a, row, kb * kBK, z, full + stage);
                         load_side<TN>(d + R::kBytesA, b, col, kb * kBK, z, full + stage);
-                        if (++stage == R::kStages) {
-                            stage = 0;
-                            phase ^= 1;
-                        }
+                    }
+                    __syncwarp();
+                    if (++stage == R::kStages) {
+                        stage = 0;
+                        phase ^= 1;
                     }
                 }
             }
-            if (!ok)
-                let_copies_land();
         }
+        if (!ok)
+            let_copies_land();
     } else if (warp == 1) {
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            for (int z = team; ok && z < q.batch; z += q.teams) {
-                for (int t = 0; ok && t < 3 * q.steps; t++) {
-                    const int which = t % 3;
-                    if (which < 2 && !has_k)
-                        continue;
-                    const bool a_mn = which == 0 && !q.wide, b_mn = which == 0 ? !q.wide : which == 2 && q.wide;
-                    const uint32_t idesc = instruction(kTM, TN, false, a_mn, b_mn);
-                    const uint32_t a_step = k_step(a_mn), b_step = k_step(b_mn);
-                    const int nk = blocks_of(which);
-                    for (int kb = 0; kb < nk; kb++) {
-                        if (!(ok = bar_wait(full + stage, phase)))
-                            break;
-                        fence_after();
-                        const uint32_t d = saddr(ring + stage * R::kStageBytes);
-                        const uint64_t da = operand_desc(d, a_mn), db = operand_desc(d + R::kBytesA, b_mn);
+        int stage = 0;
+        uint32_t phase = 0;
+        for (int z = team; ok && z < q.batch; z += q.teams) {
+            for (int t = 0; ok && t < 3 * q.steps; t++) {
+                const int which = t % 3;
+                if (which < 2 && !has_k)
+                    continue;
+                const bool a_mn = which == 0 && !q.wide, b_mn = which == 0 ? !q.wide : which == 2 && q.wide;
+                const uint32_t idesc = instruction(kTM, TN, false, a_mn, b_mn);
+                const uint32_t a_step = k_step(a_mn), b_step = k_step(b_mn);
+                const int nk = blocks_of(which);
+                for (int kb = 0; kb < nk; kb++) {
+                    if (!(ok = warp_wait(full + stage, phase)))
+                        break;
+                    fence_after();
+                    const uint32_t d = saddr(ring + stage * R::kStageBytes);
+                    const uint64_t da = operand_desc(d, a_mn), db = operand_desc(d + R::kBytesA, b_mn);
+                    if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < kBK / 16; k++)
                             mma_f16<1>(tmem, da + k * a_step, db + k * b_step, idesc, kb > 0 || k > 0);
                         mma_commit<1>(empty + stage);
-                        if (++stage == R::kStages) {
-                            stage = 0;
-                            phase ^= 1;
-                        }
                     }
-                    mma_commit<1>(acc_full);
+                    __syncwarp();
+                    if (++stage == R::kStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
                 }
+                if (elect_one())
+                    mma_commit<1>(acc_full);
+                __syncwarp();
             }
         }
     } else if (warp >= 4) {

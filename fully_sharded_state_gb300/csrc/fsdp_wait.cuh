@@ -58,6 +58,11 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity)
     }
     return false;
 }
+// The same by a whole warp: one answer for all lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity)
+{
+    return __all_sync(0xffffffffu, bar_wait(bar, parity));
+}
 __device__ __forceinline__ void bar_expect(uint64_t *bar, uint32_t bytes)
 {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(saddr(bar)), "r"(bytes)
