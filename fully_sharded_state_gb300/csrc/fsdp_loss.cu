@@ -26,7 +26,7 @@ namespace {
 using namespace tc;
 
 constexpr int kTileN = 256;
-constexpr int kPieceCols = kTileN / 2;  // columns of one (maximum, sum)
+constexpr int kPieceCols = kTileN / kParts;  // columns of one (maximum, sum): a warp's
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float exp2_fast(float x)
@@ -46,7 +46,7 @@ struct PrepParams {
     int64_t ignore;
     uint16_t *x;      // kept rows, at most ceil64(rows) of them
     int *source, *target;
-    int *meta;        // [0] rows kept, [1] rows that count, [2] a counter, zeroed
+    int *meta;        // [0] rows kept, [1] rows that count, [2] a counter, zeroed, [3] parts of dhidden's sum
     float *row_loss;
     uint16_t *dhidden;
 };
@@ -172,11 +172,11 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(const uint16_t *src, int
 
 // ---------------------------------------------------------------- logits ----
 
-// Each thread has a row of the tile and 128 of its columns, which it reads
+// Each thread has a row of the tile and 128 adjacent columns, which it reads
 // from tensor memory twice: for the maximum, then for the exponentials. The
 // exponentials leave by the warp's stage, 64 columns of 32 rows at a time.
 struct LogitsEpi {
-    static constexpr int kLeastTN = kTileN, kBytes = 8;  // 2, and the time of the exponentials
+    static constexpr int kLeastTN = kTileN, kBytes = 5;  // 2, and the time of the exponentials
     struct Params {
         uint16_t *e;      // NULL: loss alone
         int64_t lde;
@@ -185,29 +185,34 @@ struct LogitsEpi {
         const int *target;
         float *tlogit;
     };
-    using Pre = NoPre;
-    static __device__ __forceinline__ void fetch(const Params &, const Slot &, int, Pre &) {}
-    template <int COLS>
-    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &)
+    struct Pre {
+        int target;
+    };
+    static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int, Pre &pre)
     {
-        static_assert(COLS == kPieceCols, "one thread's columns are one piece");
-        // the columns past the vocabulary are compared only where there are some
-        if (x.N - x.col >= COLS)
-            piece<COLS, true>(p, x);
-        else if (x.col < x.N)
-            piece<COLS, false>(p, x);
+        pre.target = x.row < x.M ? p.target[x.row] : -1;
     }
-    template <int COLS, bool kWhole>
-    static __device__ __forceinline__ void piece(const Params &p, const Slot &x)
+    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre)
     {
+        // the columns past the vocabulary are compared only where there are some
+        const int col = x.col + x.part * kPieceCols;
+        if (x.N - col >= kPieceCols)
+            piece<true>(p, x, col, pre.target - col);
+        else if (col < x.N)
+            piece<false>(p, x, col, pre.target - col);
+    }
+    template <bool kWhole>
+    static __device__ __forceinline__ void piece(const Params &p, const Slot &x, int col, int t)
+    {
+        constexpr int kChunks = kPieceCols / 32;
         const bool live = x.row < x.M;
-        const int t = live ? p.target[x.row] - x.col : -1, n = x.N - x.col;
+        const int n = x.N - col, chunk0 = x.part * kChunks;
         float top = -CUDART_INF_F, at = 0.0f;
 #pragma unroll
-        for (int c = 0; c < COLS / 32; c++) {
+        for (int c = 0; c < kChunks; c++) {
             float v[32];
-            x.load(c, v);
-            if (t >= c * 32 && t < c * 32 + 32) {
+            x.load(chunk0 + c, v);
+            if (live && t >= c * 32 && t < c * 32 + 32) {
 #pragma unroll
                 for (int i = 0; i < 32; i++)
                     at = t == c * 32 + i ? v[i] : at;
@@ -221,38 +226,37 @@ struct LogitsEpi {
         const float ref = top == -CUDART_INF_F ? 0.0f : top;
         const float shift = ref * kLog2e;
         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int c = 0; c < COLS / 32; c++) {
-            float v[32];
-            x.load(c, v);
+        auto exponentials = [&](int chunk, float(&v)[32]) {
+            const int c = (chunk - chunk0) * 32;
 #pragma unroll
             for (int i = 0; i < 32; i++) {
-                v[i] = kWhole || c * 32 + i < n ? exp2_fast(fmaf(v[i], kLog2e, -shift)) : 0.0f;
+                v[i] = kWhole || c + i < n ? exp2_fast(fmaf(v[i], kLog2e, -shift)) : 0.0f;
                 sum[i % 4] += v[i];
             }
-            if (!p.e)
-                continue;
+        };
+        if (p.e) {
+            const int rows = x.M - x.group_row(0);
+            uint16_t *to = p.e + x.group_row(0) * p.lde;
 #pragma unroll
-            for (int g = 0; g < 4; g++)
-                *x.piece(x.lane, c % 2 * 4 + g) =
-                    make_uint4(pack_f16(v[8 * g], v[8 * g + 1]), pack_f16(v[8 * g + 2], v[8 * g + 3]),
-                               pack_f16(v[8 * g + 4], v[8 * g + 5]), pack_f16(v[8 * g + 6], v[8 * g + 7]));
-            if (c % 2) {
-                __syncwarp();
-                const int col = x.col + (c - 1) * 32 + x.lane % 8 * 8;
+            for (int u = 0; u < kChunks / 2; u++) {
+                const int unit = chunk0 / 2 + u, to_col = x.unit_col(unit);
+                x.emit16<false>(unit, exponentials, [&](int i, const uint4 &e) {
+                    if (i * 4 < rows && to_col < p.lde)
+                        *reinterpret_cast<uint4 *>(to + i * 4 * p.lde + to_col) = e;
+                });
+            }
+        } else {
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    const int r = i * 4 + x.lane / 8, row = x.row - x.lane + r;
-                    if (row < x.M && col < p.lde)
-                        *reinterpret_cast<uint4 *>(p.e + (int64_t)row * p.lde + col) = *x.piece(r, x.lane % 8);
-                }
-                __syncwarp();
+            for (int c = 0; c < kChunks; c++) {
+                float v[32];
+                x.load(chunk0 + c, v);
+                exponentials(chunk0 + c, v);
             }
         }
         if (live) {
-            p.stats[(int64_t)x.row * p.pieces + x.col / COLS] =
+            p.stats[(int64_t)x.row * p.pieces + col / kPieceCols] =
                 make_float2(top, (sum[0] + sum[1]) + (sum[2] + sum[3]));
-            if (t >= 0 && t < COLS)
+            if (t >= 0 && t < kPieceCols)
                 p.tlogit[x.row] = at;
         }
     }
@@ -399,7 +403,6 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowsParams p)
 // dhidden rows back at their own places, bf16.
 struct HiddenEpi {
     static constexpr int kLeastTN = 64, kBytes = 2;
-    static constexpr bool kAhead = false;
     struct Params {
         uint16_t *out;
         int64_t ld;
@@ -408,36 +411,34 @@ struct HiddenEpi {
     struct Pre {
         int row[8];
     };
-    static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int chunk, Pre &pre)
+    static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int, Pre &pre)
     {
-        if (chunk == 0) {  // the same rows in every chunk
 #pragma unroll
-            for (int i = 0; i < 8; i++)
-                pre.row[i] = x.group_row(i) < x.M ? p.source[x.group_row(i)] : -1;
-        }
+        for (int i = 0; i < 8; i++)
+            pre.row[i] = x.group_row(i) < x.M ? p.source[x.group_row(i)] : -1;
     }
-    static __device__ __forceinline__ void chunk(const Params &p, const Slot &x, int c, Pre &pre)
-    {
-        if (groups_of_4(p.out, p.ld)) {
-            float mine[32];
-            const int col = x.group_col(c);
-            x.across<false>(c, mine, [&](int i, float(&v)[4]) {
-                if (pre.row[i] >= 0 && col < x.N)
-                    put4_16<true>(p.out + (int64_t)pre.row[i] * p.ld + col, v, x.N - col);
-            });
-        } else {
-            const int col = x.col + c * 32 + x.lane;
-            x.by_rows(c, [&](int r, float v) {
-                const int row = x.row - x.lane + r;
-                if (row < x.M && col < x.N)
-                    p.out[(int64_t)p.source[row] * p.ld + col] = to_bf16(v);
-            });
-        }
-    }
-    template <int COLS>
     static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre)
     {
-        finish_tile<COLS, HiddenEpi>(p, x, pre);
+        if (rows_of_16(p.out, p.ld)) {
+#pragma unroll 1
+            for (int u = x.part; u < x.units(); u += kParts) {
+                const int col = x.unit_col(u);
+                x.emit16<true>(u, [](int, float(&)[32]) {}, [&](int i, const uint4 &e) {
+                    if (pre.row[i] >= 0)
+                        put8_16(p.out + (int64_t)pre.row[i] * p.ld + col, e, x.N - col);
+                });
+            }
+        } else {
+#pragma unroll 1
+            for (int c = x.part; c < x.chunks; c += kParts) {
+                const int col = x.col + c * 32 + x.lane;
+                x.by_rows(c, [&](int r, float v) {
+                    const int row = x.row - x.lane + r;
+                    if (row < x.M && col < x.N)
+                        p.out[(int64_t)p.source[row] * p.ld + col] = to_bf16(v);
+                });
+            }
+        }
     }
 };
 
@@ -446,55 +447,67 @@ struct PartEpi {
     static constexpr int kLeastTN = 64, kBytes = 4;
     static constexpr bool kAhead = false;
     struct Params {
-        float *out;  // [splits][rows][ld], ld a multiple of 8
-        int64_t ld, split_stride;
+        float *out;  // [splits][rows kept][ld], ld a multiple of 8
+        int64_t ld;
     };
     using Pre = NoPre;
     static __device__ __forceinline__ void fetch(const Params &, const Slot &, int, Pre &) {}
-    static __device__ __forceinline__ void chunk(const Params &p, const Slot &x, int c, Pre &)
+    template <class G>
+    static __device__ __forceinline__ void chunk(const Params &p, const Slot &x, int c, Pre &, G staged)
     {
         float mine[32];
         const int rows = x.M - x.group_row(0);
         const bool in = x.group_col(c) < x.N;
-        float *to = p.out + x.split * p.split_stride + x.group_row(0) * p.ld + x.group_col(c);
+        float *to = p.out + ((int64_t)x.split * x.M + x.group_row(0)) * p.ld + x.group_col(c);
         x.across<false>(c, mine, [&](int i, float(&v)[4]) {
             if (i * 4 < rows && in)
                 *reinterpret_cast<float4 *>(to + i * 4 * p.ld) = make_float4(v[0], v[1], v[2], v[3]);
-        });
+        }, staged);
     }
-    template <int COLS>
-    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre)
-    {
-        finish_tile<COLS, PartEpi>(p, x, pre);
-    }
+    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre) { finish_tile<PartEpi>(p, x, pre); }
 };
 
-__global__ void __launch_bounds__(128) join_hidden_kernel(const float *parts, int splits, int64_t split_stride,
-                                                          int64_t ldp, const int *meta, int base, int piece_rows,
-                                                          int cols, const int *source, uint16_t *out, int64_t ld)
+// Adds the parts up: 64 groups of 4 columns, 4 slices of the parts (meta[3] of
+// them) per block.
+__global__ void __launch_bounds__(256) join_hidden_kernel(const float *parts, int64_t ldp, const int *meta, int base,
+                                                          int piece_rows, int cols, const int *source, uint16_t *out,
+                                                          int64_t ld)
 {
+    __shared__ float4 sh[4][64];
     launch_wait();
     launch_next();
-    const int n = min(max(meta[0] - base, 0), piece_rows);
+    const int n = min(max(meta[0] - base, 0), piece_rows), splits = meta[3];
+    const int group = threadIdx.x % 64, slice = threadIdx.x / 64;
+    const int c = (blockIdx.y * 64 + group) * 4;
     for (int r = blockIdx.x; r < n; r += gridDim.x) {
-        uint16_t *row = out + (int64_t)source[r] * ld;
-        const float *src = parts + (int64_t)r * ldp;
-        for (int c = threadIdx.x * 4; c < cols; c += 128 * 4) {
-            float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (c < cols) {
+            const float *src = parts + (int64_t)r * ldp + c;
 #pragma unroll 8
-            for (int q = 0; q < splits; q++) {
-                const float4 f = *reinterpret_cast<const float4 *>(src + q * split_stride + c);
-                s[0] += f.x, s[1] += f.y, s[2] += f.z, s[3] += f.w;
+            for (int q = slice; q < splits; q += 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(src + (int64_t)q * n * ldp);
+                s.x += f.x, s.y += f.y, s.z += f.z, s.w += f.w;
             }
-            put4_16<true>(row + c, s, cols - c);
         }
+        sh[slice][group] = s;
+        __syncthreads();
+        if (slice == 0 && c < cols) {
+#pragma unroll
+            for (int q = 1; q < 4; q++) {
+                const float4 f = sh[q][group];
+                s.x += f.x, s.y += f.y, s.z += f.z, s.w += f.w;
+            }
+            const float v[4] = {s.x, s.y, s.z, s.w};
+            put4_16<true>(out + (int64_t)source[r] * ld + c, v, cols - c);
+        }
+        __syncthreads();
     }
 }
 
 // dweight, over the pieces of the rows in fp32 where there are several.
 struct WeightEpi {
     static constexpr int kLeastTN = 64, kBytes = 2;
-    static constexpr bool kAhead = true;
+    static constexpr bool kAhead = false;
     struct Params {
         uint16_t *out;
         int64_t ld;
@@ -516,7 +529,8 @@ struct WeightEpi {
             if (i * 4 < rows && x.group_col(chunk) < x.N)
                 pre.o[i] = *reinterpret_cast<const float4 *>(from + i * 4 * p.lds);
     }
-    static __device__ __forceinline__ void chunk(const Params &p, const Slot &x, int c, Pre &pre)
+    template <class G>
+    static __device__ __forceinline__ void chunk(const Params &p, const Slot &x, int c, Pre &pre, G staged)
     {
         const int col = x.group_col(c), left = x.N - col, rows = x.M - x.group_row(0);
         uint16_t *to = p.out + x.group_row(0) * p.ld + col;
@@ -536,38 +550,44 @@ struct WeightEpi {
                     put4_16<true>(to + i * 4 * p.ld, v, left);
                 else
                     *reinterpret_cast<float4 *>(sum + i * 4 * p.lds) = make_float4(v[0], v[1], v[2], v[3]);
-            });
-        } else if (groups_of_4(p.out, p.ld)) {
-            x.across<false>(c, mine, [&](int i, float(&v)[4]) {
-                if (i * 4 >= rows || left <= 0)
-                    return;
-                if (left >= 4)
-                    *reinterpret_cast<uint2 *>(to + i * 4 * p.ld) = four_16<true>(v);
-                else
-                    put4_16<true>(to + i * 4 * p.ld, v, left);
-            });
-        } else {
-            // a lane per column: every 32-byte sector is written in one go
-            uint16_t *row = p.out + (x.row - x.lane) * p.ld + x.col + c * 32 + x.lane;
-            const int n = x.M - (x.row - x.lane);
-            const bool in = x.col + c * 32 + x.lane < x.N;
-            x.by_rows(c, [&](int r, float v) {
-                if (r < n && in)
-                    row[r * p.ld] = to_bf16(v);
-            });
+            }, staged);
         }
     }
-    template <int COLS>
     static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre)
     {
-        finish_tile<COLS, WeightEpi>(p, x, pre);
+        if (p.sum) {
+            finish_tile<WeightEpi>(p, x, pre);
+        } else if (rows_of_16(p.out, p.ld)) {
+            const int rows = x.M - x.group_row(0);
+#pragma unroll 1
+            for (int u = x.part; u < x.units(); u += kParts) {
+                uint16_t *to = p.out + x.group_row(0) * p.ld + x.unit_col(u);
+                const int left = x.N - x.unit_col(u);
+                x.emit16<true>(u, [](int, float(&)[32]) {}, [&](int i, const uint4 &e) {
+                    if (i * 4 < rows)
+                        put8_16(to + i * 4 * p.ld, e, left);
+                });
+            }
+        } else {
+            // a lane per column: every 32-byte sector is written in one go
+            const int n = x.M - (x.row - x.lane);
+#pragma unroll 1
+            for (int c = x.part; c < x.chunks; c += kParts) {
+                uint16_t *row = p.out + (x.row - x.lane) * p.ld + x.col + c * 32 + x.lane;
+                const bool in = x.col + c * 32 + x.lane < x.N;
+                x.by_rows(c, [&](int r, float v) {
+                    if (r < n && in)
+                        row[r * p.ld] = to_bf16(v);
+                });
+            }
+        }
     }
 };
 
 // The workspace of one call, and how the call is cut.
 struct Plan {
     int64_t piece, pieces, lde, ldx, ldw, ldp;
-    int stat_pieces, splits, split_blocks;
+    int stat_pieces, splits;
     int *meta, *source, *target;
     float *tlogit;
     float2 *stats;
@@ -578,7 +598,15 @@ struct Plan {
 
 bool map_ok(const void *p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0; }
 
-constexpr int kTargetTiles = 152;  // one for each multiprocessor of a GB300
+
+// fp32 numbers that dhidden's parts take: choose_splits makes four waves of
+// tiles at most, each of 128 x 256 per multiprocessor and a row's padding, and
+// never more than all parts whole.
+int64_t parts_floats(int64_t ldp, int64_t splits, int64_t rows)
+{
+    const int64_t waves = 4 * kSplitSms * int64_t(kTM) * (kTileN + 8), whole = splits * rows * ldp;
+    return waves < whole ? waves : whole;
+}
 
 Plan plan_of(const LossArgs &a, bool grad, void *base, bool with_weight)
 {
@@ -596,22 +624,16 @@ Plan plan_of(const LossArgs &a, bool grad, void *base, bool with_weight)
     q.pieces = a.rows ? (a.rows + q.piece - 1) / q.piece : 0;
     q.ldx = ceil_to(a.cols, 16);
     q.stat_pieces = (int)((a.vocab + kPieceCols - 1) / kPieceCols);
-    // dhidden sums over the vocabulary: where its tiles (of 128 x 128, the
-    // smallest worth it) are few, the sum is cut so that about all
-    // multiprocessors have a part of it
-    const int64_t tiles = (q.piece + 127) / 128 * ((a.cols + 127) / 128);
-    const int64_t blocks = (a.vocab + kBK - 1) / kBK;
-    int64_t splits = tiles ? kTargetTiles / tiles : 1;
-    if (splits > blocks / 8)
-        splits = blocks / 8;
-    if (splits < 1)
-        splits = 1;
-    q.split_blocks = (int)((blocks + splits - 1) / splits);
-    q.splits = (int)((blocks + q.split_blocks - 1) / q.split_blocks);
+    // dhidden sums over the vocabulary. Where its 256-row tiles are few, the
+    // sum may be cut in parts (Tiles::choose_splits), which are then joined.
+    const int64_t tiles = (q.piece + 255) / 256 * ((a.cols + 255) / 256);
+    q.splits = tiles <= kSplitSms / 2 ? (int)((a.vocab + kBK - 1) / kBK / 4) : 1;
+    if (q.splits < 1)
+        q.splits = 1;
     q.ldp = ceil_to(a.cols, 8);
 
     Carver c(base);
-    q.meta = c.take<int>(3);
+    q.meta = c.take<int>(4);
     q.source = c.take<int>(a.rows);
     q.target = c.take<int>(a.rows);
     q.tlogit = c.take<float>(a.rows);
@@ -621,7 +643,7 @@ Plan plan_of(const LossArgs &a, bool grad, void *base, bool with_weight)
     if (grad) {
         q.e = c.take<uint16_t>(ceil_to(q.piece, 64) * q.lde);
         if (q.splits > 1)
-            q.parts = c.take<float>(q.splits * q.piece * q.ldp);
+            q.parts = c.take<float>(parts_floats(q.ldp, q.splits, q.piece));
         if (q.pieces > 1)
             q.dw = c.take<float>(a.vocab * q.ldp);
     }
@@ -736,17 +758,16 @@ fsdp_status launch_linear_cross_entropy(const LossArgs &a, void *workspace, int 
         sd.dyn = q.meta;
         sd.dyn_base = (int)row0;
         sd.splits = q.splits;
-        sd.split_blocks = q.split_blocks;
+        sd.splits_out = q.meta + 3;
         uint16_t *dh = static_cast<uint16_t *>(a.dhidden);
         if (q.splits > 1) {
-            const int64_t stride = q.piece * q.ldp;
-            st = product<false, true, PartEpi>(sd, og, owt, true, {q.parts, q.ldp, stride}, dev, s,
+            st = product<false, true, PartEpi>(sd, og, owt, true, {q.parts, q.ldp}, dev, s,
                                                           "linear_cross_entropy (dhidden)");
             if (st != FSDP_OK)
                 return st;
             st = launch("linear_cross_entropy (dhidden, sum)", join_hidden_kernel,
-                        (unsigned)(rows < 16 * sms ? rows : 16 * sms), 128, 0, s, 1, q.parts, q.splits, stride, q.ldp,
-                        q.meta, row0, rows, a.cols, q.source + row0, dh, a.lddh);
+                        dim3((unsigned)(rows < 16 * sms ? rows : 16 * sms), (unsigned)((a.cols + 255) / 256)), 256, 0,
+                        s, 1, q.parts, q.ldp, q.meta, row0, rows, a.cols, q.source + row0, dh, a.lddh);
         } else {
             st = product<false, true, HiddenEpi>(sd, og, owt, true, {dh, a.lddh, q.source + row0}, dev, s,
                                                             "linear_cross_entropy (dhidden)");

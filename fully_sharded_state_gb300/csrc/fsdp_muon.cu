@@ -160,72 +160,61 @@ __global__ void __launch_bounds__(kStartThreads) scale_kernel(const float *x32, 
 }
 
 // S, or P = b S + c S^2 (from != NULL), in fp16, both triangles. Strides are
-// multiples of 16, so groups of 4 and pairs of rows stay inside a padded row.
+// multiples of 16, so groups of 8 and pairs of rows stay inside a padded row.
+// S is symmetric: a thread reads the elements of its own row from the columns,
+// where the 32 lanes' are adjacent.
 struct SquareEpi {
     static constexpr int kLeastTN = 64, kBytes = kSquareBytes;
-    static constexpr bool kAhead = true;
     struct Params {
         uint16_t *out;
         const uint16_t *from;
         int64_t ld, stride;
         float b, c;
     };
-    struct Pre {
-        uint2 s[8];
-    };
-    static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int chunk, Pre &pre)
-    {
-        if (!p.from)
-            return;
-        const int rows = x.M - x.group_row(0);
-        const uint16_t *from = p.from + x.z * p.stride + x.group_row(0) * p.ld + x.group_col(chunk);
-#pragma unroll
-        for (int i = 0; i < 8; i++)
-            if (i * 4 < rows && x.group_col(chunk) < x.N)
-                pre.s[i] = *reinterpret_cast<const uint2 *>(from + i * 4 * p.ld);
-    }
-    static __device__ __forceinline__ void chunk(const Params &p, const Slot &x, int c, Pre &pre)
+    using Pre = NoPre;
+    static __device__ __forceinline__ void fetch(const Params &, const Slot &, int, Pre &) {}
+    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &)
     {
         uint16_t *out = p.out + x.z * p.stride;
         const int rows = x.M - x.group_row(0);
-        const bool in = x.group_col(c) < x.N;
-        uint16_t *to = out + x.group_row(0) * p.ld + x.group_col(c);
-        float mine[32];
-        auto direct = [&](int i, float(&v)[4]) {
-            if (i * 4 >= rows || !in)
-                return;
-            if (p.from) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&pre.s[i].x));
-                const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&pre.s[i].y));
-                v[0] = fmaf(p.c, v[0], p.b * f.x);
-                v[1] = fmaf(p.c, v[1], p.b * f.y);
-                v[2] = fmaf(p.c, v[2], p.b * g.x);
-                v[3] = fmaf(p.c, v[3], p.b * g.y);
-            }
-            *reinterpret_cast<uint2 *>(to + i * 4 * p.ld) = four_16<false>(v);
-        };
-        if (!x.mirror) {
-            x.across<false>(c, mine, direct);
-            return;
-        }
-        x.across<true>(c, mine, direct);
-        // the transposed elements: two rows' on a pair of lanes make one
-        // 32-bit store, of column j on the even and j + 1 on the odd lane
-        const int odd = x.lane & 1, row = x.row & ~1;
-        const int cols = row < x.M ? x.N - (x.col + c * 32 + odd) : 0;
-        uint16_t *across = out + (x.col + c * 32 + odd) * p.ld + row;
+#pragma unroll 1
+        for (int u = x.part; u < x.units(); u += kParts) {
+            uint16_t *to = out + x.group_row(0) * p.ld + x.unit_col(u);
+            const bool in = x.unit_col(u) < x.N;
+            auto finish = [&](int chunk, float(&v)[32]) {
+                const int col = x.col + chunk * 32;
+                if (p.from) {
+                    const uint16_t *from = p.from + x.z * p.stride + col * p.ld + x.row;
+                    const int n = x.row < x.M ? x.N - col : 0;
+                    uint16_t s[32];
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-            const float other = __shfl_xor_sync(0xffffffffu, odd ? mine[j] : mine[j + 1], 1);
-            const uint32_t pair = odd ? pack_f16(other, mine[j + 1]) : pack_f16(mine[j], other);
-            if (j < cols)
-                *reinterpret_cast<uint32_t *>(across + j * p.ld) = pair;
+                    for (int j = 0; j < 32; j++)
+                        s[j] = j < n ? from[j * p.ld] : 0;
+#pragma unroll
+                    for (int j = 0; j < 32; j++)
+                        v[j] = fmaf(p.c, v[j], p.b * __half2float(__ushort_as_half(s[j])));
+                }
+                if (!x.mirror)
+                    return;
+                // the transposed elements: two rows' on a pair of lanes make
+                // one 32-bit store, of column j on the even and j + 1 on the
+                // odd lane
+                const int odd = x.lane & 1, row = x.row & ~1;
+                const int cols = row < x.M ? x.N - (col + odd) : 0;
+                uint16_t *across = out + (col + odd) * p.ld + row;
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                    const float other = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+                    const uint32_t pair = odd ? pack_f16(other, v[j + 1]) : pack_f16(v[j], other);
+                    if (j < cols)
+                        *reinterpret_cast<uint32_t *>(across + j * p.ld) = pair;
+                }
+            };
+            x.emit16<false>(u, finish, [&](int i, const uint4 &e) {
+                if (i * 4 < rows && in)
+                    *reinterpret_cast<uint4 *>(to + i * 4 * p.ld) = e;
+            });
         }
-    }
-    template <int COLS>
-    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre)
-    {
-        finish_tile<COLS, SquareEpi>(p, x, pre);
     }
 };
 
@@ -251,34 +240,41 @@ struct StepParams {
 template <Then kThen>
 struct StepEpi {
     static constexpr int kLeastTN = 64, kBytes = kStepBytes;
-    static constexpr bool kAhead = kThen != Then::kMaster;  // it has twice the reads: registers
+    static constexpr bool kAhead = kThen != Then::kMaster;  // registers: it has twice the reads
     using Params = StepParams;
     static constexpr bool kMaster = kThen == Then::kMaster;
     struct Pre {
         float a;
         float4 x[8];
-        float w[kMaster ? 8 : 1][4];
     };
     static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int chunk, Pre &pre)
     {
         const int rows = x.M - x.group_row(0), left = x.N - x.group_col(chunk);
         pre.a = p.inv ? p.a * p.inv[x.z] : p.a;
         const float *from = p.x32 + x.z * p.stride + x.group_row(0) * p.ld + x.group_col(chunk);
-        const float *w = kMaster ? p.master[x.z] + x.group_row(0) * p.n + x.group_col(chunk) : nullptr;
 #pragma unroll
         for (int i = 0; i < 8; i++)
-            if (i * 4 < rows && left > 0) {
+            if (i * 4 < rows && left > 0)
                 pre.x[i] = *reinterpret_cast<const float4 *>(from + i * 4 * p.ld);
-                if (kMaster)
-                    get4_f32(w + i * 4 * p.n, pre.w[kMaster ? i : 0], left);
-            }
     }
-    static __device__ __forceinline__ void chunk(const Params &p, const Slot &x, int c, Pre &pre)
+    template <class G>
+    static __device__ __forceinline__ void chunk(const Params &p, const Slot &x, int c, Pre &pre, G staged)
     {
         const int rows = x.M - x.group_row(0), col = x.group_col(c), left = x.N - col;
         const int64_t at = x.z * p.stride + x.group_row(0) * p.ld + col;
         const int64_t to = x.group_row(0) * (kThen == Then::kOut ? p.ldo : p.n) + col;
         float mine[32];
+        // the master's elements are read once the accumulator's registers are free
+        float w[kMaster ? 8 : 1][4];
+        auto read_master = [&] {
+            staged();
+            if (kMaster) {
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    if (i * 4 < rows && left > 0)
+                        get4_f32(p.master[x.z] + to + i * 4 * p.n, w[kMaster ? i : 0], left);
+            }
+        };
         x.across<false>(c, mine, [&](int i, float(&v)[4]) {
             if (i * 4 >= rows || left <= 0)
                 return;
@@ -294,18 +290,14 @@ struct StepEpi {
             } else {
 #pragma unroll
                 for (int k = 0; k < 4; k++)
-                    v[k] = fmaf(-p.lr, v[k], pre.w[kMaster ? i : 0][k] * p.decay);
+                    v[k] = fmaf(-p.lr, v[k], w[kMaster ? i : 0][k] * p.decay);
                 put4_f32(p.master[x.z] + to + i * 4 * p.n, v, left);
                 if (p.param[x.z])
                     put4_16<true>(p.param[x.z] + to + i * 4 * p.n, v, left);
             }
-        });
+        }, read_master);
     }
-    template <int COLS>
-    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre)
-    {
-        finish_tile<COLS, StepEpi>(p, x, pre);
-    }
+    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre) { finish_tile<StepEpi>(p, x, pre); }
 };
 
 // steps = 0: the scaled input is the result.

@@ -117,10 +117,8 @@ inline int64_t product_clocks(const SchulzArgs &a, int sms)
     s.sym = 1;
     s.M = s.N = (int)k;
     s.K = (int)l;
-    s.split_blocks = (int)((l + kBK - 1) / kBK);
     int64_t t = best_form(s, sms, 64, kSquareBytes).cost;
     s.K = (int)k;
-    s.split_blocks = (int)((k + kBK - 1) / kBK);
     t += best_form(s, sms, 64, kSquareBytes).cost;
     s.sym = 0;
     s.M = (int)a.m;

@@ -416,14 +416,20 @@ __global__ void __launch_bounds__(backward_block<TPR>(), backward_block<TPR>() =
     const float inv = 1.0f / (float)p.cols;
     int phase = 0, stage = 0;
     uint32_t parity = 0;
+    float next_mean = 0.0f, next_rstd = 0.0f;  // read a row ahead
+    if (first + sub < p.rows) {
+        next_mean = p.mean[first + sub];
+        next_rstd = p.rstd[first + sub];
+    }
     for (int64_t r0 = first; r0 < p.rows; r0 += step, phase ^= 1) {
         const int64_t r = r0 + sub;
         const bool live = r < p.rows;
         Chunk<T> cx[NV], cy[NV];
-        float mean = 0.0f, rstd = 0.0f;
-        if (live) {
-            mean = p.mean[r];
-            rstd = p.rstd[r];
+        const float mean = next_mean, rstd = next_rstd;
+        next_mean = next_rstd = 0.0f;
+        if (r + step < p.rows) {
+            next_mean = p.mean[r + step];
+            next_rstd = p.rstd[r + step];
         }
         bool ok = true;
         if (kStaged) {

@@ -9,9 +9,12 @@
 //             M, N, K works)
 //   warp 1    one thread issues tcgen05.mma; the accumulator is TN columns of
 //             tensor memory, double-buffered
-//   warps 4.. eight epilogue warps read the finished accumulator (a thread
-//             holds one row of the tile, TN / 2 columns of it) while the next
-//             tile is being multiplied. What they read and write in memory
+//   warps 4.. eight epilogue warps read the finished accumulator, 32 rows
+//             and 32 columns of it at a time (a thread holds one row), while
+//             the next tile is being multiplied. (Sixteen were no faster: an
+//             epilogue is bound by the 128 bytes a clock of shared memory and
+//             L1, which the MMAs' operands use as well.) What they read and
+//             write in memory
 //             goes through 4 KB of shared memory per warp, so that lanes
 //             touch whole lines of a row; with each lane on a row of its own,
 //             a 512 x 512 update spent 17 us per tile on its accesses
@@ -44,6 +47,8 @@ using namespace wait;
 constexpr int kBK = 64;        // K elements of a stage: 128 bytes, one swizzle row
 constexpr int kTM = 128;       // rows of a CTA's tile: the lanes of tensor memory
 constexpr int kEpiWarps = 8;
+constexpr int kSplitSms = 152; // multiprocessors that a split sum is spread over at most
+constexpr int kParts = kEpiWarps / 4;  // warps that share 32 rows of a tile
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 
 // One arrival on the barrier at the same place in CTA `rank` of the cluster.
@@ -232,8 +237,10 @@ __host__ __device__ constexpr uint32_t instruction(int rows, int cols, bool bf16
 struct Shape {
     int M, N, K;      // K: the whole contraction
     int batch;        // matrices, on the maps' third axis
-    int splits;       // parts of K, each its own tile (its results are partial sums)
-    int split_blocks; // K blocks of a part
+    int splits;       // parts of K, each its own tile (its results are partial
+                      // sums): at most so many, chosen by Tiles on the device
+    int *splits_out;  // where the number is left, or NULL
+    int tn;           // columns of a tile, a multiple of 16, at most TN
     int sym;          // only the squares on and above the diagonal (M = N)
     int group;        // row tiles that are walked together, for reuse in L2
     uint32_t idesc;
@@ -253,7 +260,8 @@ struct Tiles {
     static constexpr int kRows = kTM * kCtas;
     static constexpr int kSquare = kRows > TN ? kRows : TN;  // of sym
     int m_tiles, n_tiles, M, K;
-    uint32_t per_z, total;  // below 2^31
+    int splits, split_blocks;  // parts of K and the K blocks of one
+    uint32_t per_z, total;     // below 2^31
 
     __device__ __forceinline__ Tiles(const Shape &s)
     {
@@ -265,14 +273,47 @@ struct Tiles {
             lim = n < 0 ? 0 : n < lim ? n : lim;
         }
         m_tiles = (M + kRows - 1) / kRows;
-        n_tiles = (s.N + TN - 1) / TN;
+        n_tiles = (s.N + s.tn - 1) / s.tn;
         if (s.sym) {
             const uint32_t q = (M + kSquare - 1) / kSquare;
             per_z = q * (q + 1) / 2 * (kSquare / kRows) * (kSquare / TN);
         } else {
             per_z = (uint32_t)m_tiles * n_tiles;
         }
-        total = per_z * s.batch * s.splits;
+        splits = 1;
+        split_blocks = (K + kBK - 1) / kBK;
+        if (s.splits > 1 && per_z > 0)
+            choose_splits(s);
+        total = per_z * s.batch * splits;
+    }
+
+    // K in parts where the tiles, as many as the device's counts leave, do not
+    // fill the grid: one to four waves, whichever is estimated shortest, a
+    // part's clocks being its blocks' and those of its own start and end, and
+    // of the joining (8 bytes per element and part, at 3,000 a clock).
+    __device__ void choose_splits(const Shape &s)
+    {
+        const int blocks = split_blocks, slots = gridDim.x / kCtas, base = (int)per_z * s.batch;
+        const int per_block = kCtas == 2 || s.tn > 128 ? 512 : 364;
+        const float join = (float)M * (float)s.N * (8.0f / 3000.0f);
+        float best = 0.0f;
+        int chosen = 1;
+        for (int w = 1; w <= 4; w++) {
+            int n = slots * w / base;
+            n = n < 1 ? 1 : n < s.splits ? n : s.splits;
+            const int per = (blocks + n - 1) / n;
+            n = (blocks + per - 1) / per;
+            const int waves = (base * n + slots - 1) / slots;
+            const float t = (float)waves * (float)(per * per_block + 4000) + (float)n * join;
+            if (w == 1 || t < best) {
+                best = t;
+                chosen = n;
+            }
+        }
+        split_blocks = (blocks + chosen - 1) / chosen;
+        splits = chosen;
+        if (s.splits_out && blockIdx.x == 0 && threadIdx.x == 0)
+            *s.splits_out = splits;
     }
 
     __device__ __forceinline__ Work at(const Shape &s, uint32_t t) const
@@ -280,8 +321,8 @@ struct Tiles {
         Work w;
         const uint32_t zs = t / per_z;
         int i = (int)(t - zs * per_z);
-        w.split = (int)(zs % (uint32_t)s.splits);
-        w.z = (int)(zs / (uint32_t)s.splits);
+        w.split = (int)(zs % (uint32_t)splits);
+        w.z = (int)(zs / (uint32_t)splits);
         if (s.sym) {
             constexpr int kSubM = kSquare / kRows, kSubN = kSquare / TN;
             const int sub = i % (kSubM * kSubN);
@@ -301,20 +342,40 @@ struct Tiles {
             const int left = m_tiles - g * s.group;
             const int rows = left < s.group ? left : s.group;
             w.row = (g * s.group + i % rows) * kRows;
-            w.col = i / rows * TN;
+            w.col = i / rows * s.tn;
         }
         const int nk = (K + kBK - 1) / kBK;
-        w.kb = w.split * s.split_blocks;
+        w.kb = w.split * split_blocks;
         int n = nk - w.kb;
-        w.nkb = n < 0 ? 0 : n < s.split_blocks ? n : s.split_blocks;
+        w.nkb = n < 0 ? 0 : n < split_blocks ? n : split_blocks;
         return w;
     }
 };
 
-// What an epilogue thread is given: its row and the first of its TN / 2
-// columns, and where they are in tensor memory.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <bool kBf16>
+__device__ __forceinline__ uint32_t two(float lo, float hi)
+{
+    return kBf16 ? pack_bf16(lo, hi) : pack_f16(lo, hi);
+}
+
+// What an epilogue thread is given: its row, the tile's first column, and
+// where they are in tensor memory. The tile's columns are taken in chunks of
+// 32, or units of two chunks: warp `part` of the kParts that share a row takes
+// chunks (or units) part, part + kParts, ... below `chunks` (`units`).
 struct Slot {
     int z, split, row, col, M, N;
+    int part, chunks;
+    __device__ __forceinline__ int units() const { return (chunks + 1) / 2; }
     uint32_t tmem;
     unsigned char *stage;  // the warp's 4 KB: 32 rows of 128 bytes
     int lane;
@@ -391,10 +452,12 @@ struct Slot {
     // Takes the threads' own rows of a chunk to the lanes by groups and calls
     // f(i, v) for each of this lane's 8. What f leaves in v is back in `mine`
     // after it, where kBack is set.
-    template <bool kBack, class F>
-    __device__ __forceinline__ void spread(float (&mine)[32], F f) const
+    // `staged` is called when `mine` is in the stage and its registers are free.
+    template <bool kBack, class F, class G>
+    __device__ __forceinline__ void spread(float (&mine)[32], F f, G staged) const
     {
         put_stage(mine);
+        staged();
 #pragma unroll
         for (int i = 0; i < 8; i++) {
             const uint4 u = *group(i);
@@ -409,11 +472,42 @@ struct Slot {
             get_stage(mine);
     }
     template <bool kBack, class F>
-    __device__ __forceinline__ void across(int chunk, float (&mine)[32], F f) const
+    __device__ __forceinline__ void spread(float (&mine)[32], F f) const
+    {
+        spread<kBack>(mine, f, [] {});
+    }
+    template <bool kBack, class F, class G>
+    __device__ __forceinline__ void across(int chunk, float (&mine)[32], F f, G staged) const
     {
         load_sum(chunk, mine);
-        spread<kBack>(mine, f);
+        spread<kBack>(mine, f, staged);
     }
+    // A unit as 16-bit numbers, for results that need nothing from memory by
+    // groups: op(chunk, v) works on the thread's own row of each of the two
+    // chunks, f(i, u) gets 8 adjacent results for row group_row(i), from column
+    // unit_col(unit) on. Half the traffic of taking fp32 across.
+    __device__ __forceinline__ int unit_col(int unit) const { return col + unit * 64 + lane % 8 * 8; }
+    template <bool kBf16, class Op, class F>
+    __device__ __forceinline__ void emit16(int unit, Op op, F f) const
+    {
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            float v[32];
+            load_sum(unit * 2 + h, v);
+            op(unit * 2 + h, v);
+#pragma unroll
+            for (int g = 0; g < 4; g++)
+                *piece(lane, h * 4 + g) = make_uint4(
+                    two<kBf16>(v[8 * g], v[8 * g + 1]), two<kBf16>(v[8 * g + 2], v[8 * g + 3]),
+                    two<kBf16>(v[8 * g + 4], v[8 * g + 5]), two<kBf16>(v[8 * g + 6], v[8 * g + 7]));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            f(i, *group(i));
+        __syncwarp();
+    }
+
     // The reverse: f(i, v) makes this lane's 8 groups, `mine` becomes the
     // thread's own row of them.
     template <class F>
@@ -436,30 +530,36 @@ struct Slot {
 //   kBytes             what it moves per element, for the choice of the tile
 //   Pre                what it reads from memory for one chunk, in registers
 //   fetch(p, x, chunk, pre)   starts those reads
-//   chunk(p, x, chunk, pre)   finishes a chunk with them
+//   chunk(p, x, chunk, pre, staged)   finishes a chunk with them; calls
+//                      staged() once the accumulator's registers are free
 // The first chunk's reads are started before the accumulator is waited for,
-// and with kAhead each chunk's before the one before it is finished: with
-// reads and stores in turn, their latency made up most of a short product.
-template <int COLS, class E>
+// and with kAhead each chunk's while the one before it is finished: with reads and
+// stores in turn, their latency made up most of a short product.
+template <class E>
 __device__ __forceinline__ void finish_tile(const typename E::Params &p, const Slot &x, typename E::Pre &a)
 {
-    constexpr int n = COLS / 32;
-    if (E::kAhead && n > 1) {
-        typename E::Pre b;
+    typename E::Pre b;
 #pragma unroll 1
-        for (int c = 0; c < n; c += 2) {
-            E::fetch(p, x, c + 1, b);
-            E::chunk(p, x, c, a);
-            if (c + 2 < n)
-                E::fetch(p, x, c + 2, a);
-            E::chunk(p, x, c + 1, b);
-        }
-    } else {
-#pragma unroll 1
-        for (int c = 0; c < n; c++) {
-            if (c > 0)
-                E::fetch(p, x, c, a);
-            E::chunk(p, x, c, a);
+    for (int c = x.part; c < x.chunks; c += 2 * kParts) {
+        const int d = c + kParts, e = d + kParts;
+        if (E::kAhead) {
+            E::chunk(p, x, c, a, [&] {
+                if (d < x.chunks)
+                    E::fetch(p, x, d, b);
+            });
+            if (d < x.chunks)
+                E::chunk(p, x, d, b, [&] {
+                    if (e < x.chunks)
+                        E::fetch(p, x, e, a);
+                });
+        } else {
+            E::chunk(p, x, c, a, [] {});
+            if (d < x.chunks) {
+                E::fetch(p, x, d, a);
+                E::chunk(p, x, d, a, [] {});
+            }
+            if (e < x.chunks)
+                E::fetch(p, x, e, a);
         }
     }
 }
@@ -531,19 +631,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     launch_wait();
     launch_next();
     const T tiles(s);
+    const int rows_b = s.tn / kCtas;  // of B in this CTA
+    const uint32_t stage_bytes = R::kBytesA + (kBMN ? (rows_b + 63) / 64 * 8192 : rows_b * 128);
 
     if (warp == 0) {
         int stage = 0;
         uint32_t phase = 0;
         for (uint32_t t = first; ok && t < tiles.total; t += step) {
             const Work w = tiles.at(s, t);
-            const int row = w.row + (int)rank * kTM, col = w.col + (int)rank * R::kRowsB;
+            const int row = w.row + (int)rank * kTM, col = w.col + (int)rank * rows_b;
             for (int kb = 0; kb < w.nkb; kb++) {
                 if (!(ok = warp_wait(empty + stage, phase ^ 1)))
                     break;
                 if (elect_one()) {
                     if (rank == 0)
-                        bar_expect(full + stage, R::kStageBytes * kCtas);
+                        bar_expect(full + stage, stage_bytes * kCtas);
                     unsigned char *a = ring + stage * R::kStageBytes, *b = a + R::kBytesA;
                     const int k = (w.kb + kb) * kBK;
                     if (kAMN) {
@@ -556,7 +658,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (kBMN) {
 #pragma unroll
                         for (int i = 0; i < R::kRowsB / 64; i++)
-                            tma_load<kCtas>(b + i * 8192, &map_b, col + i * 64, k, w.z, full + stage);
+                            if (i * 64 < rows_b)
+                                tma_load<kCtas>(b + i * 8192, &map_b, col + i * 64, k, w.z, full + stage);
                     } else {
                         tma_load<kCtas>(b, &map_b, k, col, w.z, full + stage);
                     }
@@ -611,29 +714,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= 4) {
         int acc = 0;
         uint32_t acc_phase = 0;
-        const int quarter = warp % 4, half = (warp - 4) / 4;
+        const int quarter = warp % 4, part = (warp - 4) / 4;
         for (uint32_t t = first; t < tiles.total; t += step) {
             const Work w = tiles.at(s, t);
             Slot x;
             x.z = w.z;
             x.split = w.split;
             x.row = w.row + (int)rank * kTM + quarter * 32 + lane;
-            x.col = w.col + half * (TN / 2);
+            x.col = w.col;
             x.M = tiles.M;
-            x.N = s.N;
+            x.N = s.N - w.col < s.tn ? s.N : w.col + s.tn;
+            x.part = part;
+            x.chunks = (x.N - w.col + 31) / 32;
             x.lane = lane;
             x.stage = epi + (warp - 4) * 4096;
-            x.tmem = tmem + acc * TN + half * (TN / 2) + ((uint32_t)(quarter * 32) << 16);
+            x.tmem = tmem + acc * TN + ((uint32_t)(quarter * 32) << 16);
             x.mirror = s.sym && w.row / T::kSquare != w.col / T::kSquare;
             x.empty = w.nkb == 0;
             typename Epi::Pre pre;
-            Epi::fetch(ep, x, 0, pre);
+            Epi::fetch(ep, x, part, pre);
             ok = bar_wait(acc_full + acc, acc_phase);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok)
                 break;
             fence_after();
-            Epi::template run<TN / 2>(ep, x, pre);
+            Epi::run(ep, x, pre);
             fence_before();
             __syncwarp();
             if (lane == 0)
@@ -724,12 +829,14 @@ fsdp_status product_as(Shape s, const Operand &a, const Operand &b, bool bf16, c
     CUtensorMap ma, mb;
     fsdp_status st = make_map(&ma, a, s.batch, kAMN ? kBK : kTM, bf16);
     if (st == FSDP_OK)
-        st = make_map(&mb, b, s.batch, kBMN ? kBK : R::kRowsB, bf16);
+        st = make_map(&mb, b, s.batch, kBMN ? kBK : s.tn / kCtas, bf16);
     if (st != FSDP_OK)
         return st;
-    s.idesc = instruction(kTM * kCtas, TN, bf16, kAMN, kBMN);
-    const int64_t most = device_sms(dev) / kCtas;
-    return launch(what, kernel, dim3((unsigned)((tiles < most ? tiles : most) * kCtas)), kThreads, R::kSmem, stream,
+    s.idesc = instruction(kTM * kCtas, s.tn, bf16, kAMN, kBMN);
+    const int sms = device_sms(dev);
+    const int64_t most = (s.splits > 1 && sms > kSplitSms ? kSplitSms : sms) / kCtas;
+    const int64_t grid = s.splits > 1 || tiles > most ? most : tiles;
+    return launch(what, kernel, dim3((unsigned)(grid * kCtas)), kThreads, R::kSmem, stream,
                   kCtas, ma, mb, s, ep);
 }
 
@@ -741,7 +848,7 @@ inline int64_t count_tiles(const Shape &s, int64_t rows, int64_t cols)
         const int64_t square = rows > cols ? rows : cols, q = (s.M + square - 1) / square;
         n = q * (q + 1) / 2 * (square / rows) * (square / cols);
     }
-    return n * s.batch * s.splits;
+    return n * s.batch;
 }
 
 // The tile of a product. The largest output tile makes the fewest trips to L2,
@@ -754,6 +861,7 @@ inline int64_t count_tiles(const Shape &s, int64_t rows, int64_t cols)
 // element, 11 us a wave).
 struct Form {
     int ctas, tn;
+    int columns;          // of a tile: tn, or less where that leaves less of the last tile empty
     int64_t tiles, cost;  // clocks
 };
 inline int64_t block_clocks(int ctas, int tn)
@@ -763,17 +871,20 @@ inline int64_t block_clocks(int ctas, int tn)
 }
 inline Form best_form(const Shape &s, int64_t sms, int least_tn, int epi_bytes)
 {
-    const int64_t blocks = (s.K + kBK - 1) / kBK;
-    const int64_t nk = s.split_blocks < blocks ? s.split_blocks : blocks;
-    Form best{0, 0, 0, 0};
+    const int64_t nk = (s.K + kBK - 1) / kBK;
+    Form best{};
     static const int kForms[4][2] = {{2, 256}, {1, 256}, {1, 128}, {1, 64}};
     for (const int *f : kForms) {
         if (f[1] < least_tn)
             continue;
-        Form g{f[0], f[1], count_tiles(s, kTM * f[0], f[1]), 0};
+        const int64_t across = (s.N + f[1] - 1) / f[1];
+        const int columns = s.sym || least_tn == 256 ? f[1] : (int)ceil_to((s.N + across - 1) / across, 16);
+        Form g{f[0], f[1], columns, count_tiles(s, kTM * f[0], f[1]), 0};
         const int64_t slots = sms / g.ctas < 1 ? 1 : sms / g.ctas, waves = (g.tiles + slots - 1) / slots;
-        const int64_t mma = nk * block_clocks(g.ctas, g.tn), epi = 1000 + kTM * g.tn * epi_bytes / 35;
+        const int64_t mma = nk * block_clocks(g.ctas, columns), epi = 1000 + kTM * columns * epi_bytes / 35;
         g.cost = (mma > epi ? waves * mma + epi : waves * epi + mma) + 2500;
+        if (s.splits > 1)  // spread over the grid whatever the tiles: what one costs, times their number
+            g.cost = g.tiles * g.ctas * mma;
         if (best.tn == 0 || g.cost < best.cost)
             best = g;
     }
@@ -781,17 +892,14 @@ inline Form best_form(const Shape &s, int64_t sms, int least_tn, int epi_bytes)
 }
 
 // Launches D = A B^T. `s` needs M, N, K, batch, sym, dyn* and, for split
-// sums, splits and split_blocks; the rest is filled in here.
+// sums, splits; the rest is filled in here.
 template <bool kAMN, bool kBMN, class Epi>
 fsdp_status product(Shape s, const Operand &a, const Operand &b, bool bf16, const typename Epi::Params &ep,
                     int dev, cudaStream_t stream, const char *what)
 {
-    if (s.splits < 1)
-        s.splits = 1;
-    if (s.splits == 1)
-        s.split_blocks = (s.K + kBK - 1) / kBK;
     s.group = s.group > 0 ? s.group : 8;
     const Form best = best_form(s, device_sms(dev), Epi::kLeastTN, Epi::kBytes);
+    s.tn = best.columns;
     if (best.tiles < 1)
         return FSDP_OK;
     if (best.tiles >= (int64_t)1 << 31)
@@ -810,16 +918,6 @@ fsdp_status product(Shape s, const Operand &a, const Operand &b, bool bf16, cons
 
 // ------------------------------------------------- rows of an epilogue ----
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
-{
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
-{
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
 __device__ __forceinline__ float bf16_at(const uint16_t *p) { return __uint_as_float((uint32_t)*p << 16); }
 __device__ __forceinline__ uint16_t to_bf16(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
 
@@ -828,16 +926,29 @@ __device__ __forceinline__ bool aligned(const void *p, unsigned bytes)
     return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
 }
 
-// Whether all rows from p on, ld 16-bit elements apart, hold whole groups of 4.
-__device__ __forceinline__ bool groups_of_4(const uint16_t *p, int64_t ld)
+// Whether all rows from p on, ld 16-bit elements apart, start on 16 bytes.
+__device__ __forceinline__ bool rows_of_16(const uint16_t *p, int64_t ld)
 {
-    return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * 2)) & 7) == 0;
+    return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * 2)) & 15) == 0;
 }
 template <bool kBf16>
 __device__ __forceinline__ uint2 four_16(const float (&v)[4])
 {
-    return kBf16 ? make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]))
-                 : make_uint2(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]));
+    return make_uint2(two<kBf16>(v[0], v[1]), two<kBf16>(v[2], v[3]));
+}
+// 8 adjacent 16-bit elements, of which the first n exist; p is aligned where
+// all do.
+__device__ __forceinline__ void put8_16(uint16_t *p, const uint4 &u, int n)
+{
+    if (n >= 8) {
+        *reinterpret_cast<uint4 *>(p) = u;
+    } else {
+        const uint16_t *e = reinterpret_cast<const uint16_t *>(&u);
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (i < n)
+                p[i] = e[i];
+    }
 }
 // 4 adjacent elements of a row, of which the first n exist; one access where
 // all do and p is aligned.

@@ -234,19 +234,19 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
             }
         }
     } else if (warp >= 4) {
-        const int quarter = warp % 4, half = (warp - 4) / 4, t0 = threadIdx.x - 128;
+        const int quarter = warp % 4, part = (warp - 4) / 4, t0 = threadIdx.x - 128;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         Slot x{};  // this thread's part of the x tile; the accumulator's columns
         x.row = x_row + quarter * 32 + lane;
-        x.col = x_col + half * (TN / 2);
+        x.col = x_col;
         x.M = q.m;
         x.N = q.n;
         x.lane = lane;
         x.stage = epi + (warp - 4) * 4096;
-        x.tmem = tmem + half * (TN / 2) + lanes;
+        x.tmem = tmem + lanes;
         Slot y = x;  // and of the S or P tile
         y.row = k_row + quarter * 32 + lane;
-        y.col = k_col + half * (TN / 2);
+        y.col = k_col;
         y.M = y.N = q.k;
         const uint32_t held = x.tmem + TN;  // x itself, fp32
         uint32_t parity = 0;
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
             float sq = 0.0f;
             const int rows = q.m - x.group_row(0);
 #pragma unroll 1
-            for (int c = 0; c < TN / 64; c++) {
+            for (int c = part; c < TN / 32; c += kParts) {
                 const int col = x.group_col(c), left = q.n - col;
                 float mine[32];
                 x.collect(mine, [&](int i, float(&v)[4]) {
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
                 });
             };
 #pragma unroll 1
-            for (int c = 0; c < TN / 64; c++) {
+            for (int c = part; c < TN / 32; c += kParts) {
                 float mine[32];
                 __syncwarp();
                 tmem_load32(held + c * 32, mine);
@@ -359,8 +359,8 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
                             if (i * 4 < yrows && y.group_col(c) < q.k)
                                 s4[i] = *reinterpret_cast<const uint2 *>(from + i * 4 * q.ldk);
                     };
-                    if (which == 1)
-                        fetch_s(0);
+                    if (which == 1 && part < TN / 32)
+                        fetch_s(part);
                     ok = !epi_any(!bar_wait(acc_full, parity));
                     parity ^= 1;
                     if (!ok)
@@ -369,8 +369,8 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
                     if (which < 2) {
                         uint16_t *out = (which ? q.p : q.s) + z * q.ks;
 #pragma unroll 1
-                        for (int c = 0; c < TN / 64; c++) {
-                            if (which == 1 && c > 0)
+                        for (int c = part; c < TN / 32; c += kParts) {
+                            if (which == 1 && c > part)
                                 fetch_s(c);
                             float mine[32];
                             y.load(c, mine);
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
                         }
                     } else {
 #pragma unroll 1
-                        for (int c = 0; c < TN / 64; c++) {
+                        for (int c = part; c < TN / 32; c += kParts) {
                             float mine[32], old[32];
                             x.load(c, mine);
                             tmem_load32(held + c * 32, old);
