@@ -268,6 +268,7 @@ struct RowsParams {
     const int *meta;
     int base, piece_rows;  // this piece's first kept row; its buffer's rows
     int vocab, pieces;
+    int segment;           // columns of a block, a multiple of 8
     int64_t lde, rows;
     uint16_t *e;           // exponentials in, G out; NULL: loss alone
     const float2 *stats;
@@ -318,6 +319,9 @@ __device__ __forceinline__ uint32_t two_of_g(uint32_t e, float f, float scale, i
     return pack_bf16(a * scale, b * scale);
 }
 
+// Grid (rows, segments of the columns): with few rows several blocks share
+// one, each joining its pieces for itself (256 x 32000: 16 us with one block
+// per row).
 __global__ void __launch_bounds__(256) rows_kernel(const RowsParams p)
 {
     __shared__ float sh[8];
@@ -327,12 +331,12 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowsParams p)
     const int n = min(max(p.meta[0] - p.base, 0), p.piece_rows);
     const int end = p.e ? (n + 63) / 64 * 64 : n;  // up to the next whole K block: zeros of G
     const float scale = p.mean ? p.grad_scale / (float)max(p.meta[1], 1) : p.grad_scale;
-    const int cols = (p.vocab + 7) / 8 * 8;
+    const int cols = min((p.vocab + 7) / 8 * 8, (int)(blockIdx.y + 1) * p.segment), col0 = blockIdx.y * p.segment;
     constexpr int kStep = 256 * 8, kFlight = 4;
     for (int r = blockIdx.x; r < end; r += gridDim.x) {
         uint16_t *e = p.e + (int64_t)r * p.lde;
         if (r >= n) {
-            for (int c = threadIdx.x * 8; c < cols; c += kStep)
+            for (int c = col0 + threadIdx.x * 8; c < cols; c += kStep)
                 *reinterpret_cast<uint4 *>(e + c) = make_uint4(0, 0, 0, 0);
             continue;
         }
@@ -349,7 +353,7 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowsParams p)
             sum += q.y * expf((q.x == -CUDART_INF_F ? 0.0f : q.x) - ref);
         }
         sum = reduce_sum(sum, sh);
-        if (threadIdx.x == 0)
+        if (threadIdx.x == 0 && blockIdx.y == 0)
             p.row_loss[p.source[r]] = ref + logf(sum) - p.tlogit[r];
         if (!p.e)
             continue;
@@ -364,7 +368,7 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowsParams p)
             u.w = two_of_g(u.w, f, scale, t - c - 6);
             *reinterpret_cast<uint4 *>(e + c) = u;
         };
-        int c = threadIdx.x * 8;
+        int c = col0 + threadIdx.x * 8;
         for (; c + (kFlight - 1) * kStep < cols; c += kFlight * kStep) {
             uint4 u[kFlight];
 #pragma unroll
@@ -384,7 +388,7 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowsParams p)
     __syncthreads();
     if (threadIdx.x == 0) {
         __threadfence();
-        last = atomicAdd(p.done, 1) == (int)gridDim.x - 1;
+        last = atomicAdd(p.done, 1) == (int)(gridDim.x * gridDim.y) - 1;
     }
     __syncthreads();
     if (!last)
@@ -742,7 +746,14 @@ fsdp_status launch_linear_cross_entropy(const LossArgs &a, void *workspace, int 
         rp.grad_scale = a.grad_scale;
         rp.mean = a.mean;
         const int64_t rows_grid = ceil_to(rows, 64) < 8 * sms ? ceil_to(rows, 64) : 8 * sms;
-        if ((st = launch("linear_cross_entropy (rows)", rows_kernel, (unsigned)rows_grid, 256, 0, s, 1, rp)) != FSDP_OK)
+        int64_t segments = grad ? 8 * sms / rows_grid : 1;
+        if (segments > (a.vocab + 4095) / 4096)
+            segments = (a.vocab + 4095) / 4096;
+        if (segments < 1)
+            segments = 1;
+        rp.segment = (int)ceil_to((a.vocab + segments - 1) / segments, 8);
+        if ((st = launch("linear_cross_entropy (rows)", rows_kernel, dim3((unsigned)rows_grid, (unsigned)segments), 256,
+                         0, s, 1, rp)) != FSDP_OK)
             return st;
         if (!grad)
             continue;

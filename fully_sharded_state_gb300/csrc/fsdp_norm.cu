@@ -217,7 +217,8 @@ constexpr int forward_block()
 // 16 chunks a thread needs no barrier, but its unrolled code missed the
 // instruction cache: 16384 x 4096 bf16 took 132 us.)
 template <typename T, bool kFull, int TPR, int NV>
-__global__ void __launch_bounds__(forward_block<TPR>()) norm_forward_kernel(const ForwardParams p)
+__global__ void __launch_bounds__(forward_block<TPR>(), NV <= 4 ? 1024 / forward_block<TPR>() : 1)
+    norm_forward_kernel(const ForwardParams p)
 {
     constexpr int kRowsPerBlock = forward_block<TPR>() / TPR, kWarps = TPR / 32, V = Chunk<T>::V;
     __shared__ float4 sh[2][32];
@@ -281,15 +282,22 @@ __global__ void __launch_bounds__(forward_block<TPR>()) norm_forward_kernel(cons
             if (threadIdx.x % 32 == 0)
                 sh[phase][warp] = make_float4(mean, m2, count, 0.0f);
             __syncthreads();
-            mean = m2 = 0.0f;
+            if (kWarps <= 4) {
+                mean = m2 = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kWarps; w++)
-                mean += sh[phase][warp0 + w].x * sh[phase][warp0 + w].z;
-            mean *= inv_cols;
+                for (int w = 0; w < kWarps; w++)
+                    mean += sh[phase][warp0 + w].x * sh[phase][warp0 + w].z;
+                mean *= inv_cols;
 #pragma unroll
-            for (int w = 0; w < kWarps; w++) {
-                const float4 f = sh[phase][warp0 + w];
-                m2 += f.y + f.z * (f.x - mean) * (f.x - mean);
+                for (int w = 0; w < kWarps; w++) {
+                    const float4 f = sh[phase][warp0 + w];
+                    m2 += f.y + f.z * (f.x - mean) * (f.x - mean);
+                }
+            } else {  // a lane per warp of the row
+                const int w = threadIdx.x % 32;
+                const float4 f = w < kWarps ? sh[phase][warp0 + w] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                mean = warp_sum(f.x * f.z) * inv_cols;
+                m2 = warp_sum(f.y + f.z * (f.x - mean) * (f.x - mean));
             }
         }
         const float rstd = 1.0f / sqrtf(m2 * inv_cols + p.eps);
@@ -356,11 +364,15 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
 // Staged (kStaged, for rows of whole chunks): a block's rows of x and dy come
 // into a ring of `stages` shared-memory stages by bulk copies, so that loads
 // are under way while a row waits for its sums. The one barrier per row, that
-// of the sums, comes after every thread has its chunks in registers: behind
-// it the stage is free and is filled again. Registers alone held too little:
-// 16384 x 4096 bf16 took 107 us.
+// of the sums, comes after every thread has read its chunks: behind it the
+// stage is free and is filled again. Registers alone held too little: 16384 x
+// 4096 bf16 took 107 us.
+//
+// bf16 rows are bound by instructions as much as by HBM. Two elements share
+// each fp32 one (Pair), xhat is one multiply-add, and xhat and dy gamma stay in
+// registers for dx, which is two more.
 template <typename T, bool kFull, bool kStaged, int TPR, int NV>
-__global__ void __launch_bounds__(backward_block<TPR>(), backward_block<TPR>() == 256 ? 2 : 1)
+__global__ void __launch_bounds__(backward_block<TPR>(), backward_block<TPR>() > 256 ? 1 : 2)
     norm_backward_kernel(const BackwardParams p)
 {
     constexpr int kSub = backward_block<TPR>() / TPR, kWarps = TPR / 32, V = Chunk<T>::V;
@@ -452,20 +464,33 @@ __global__ void __launch_bounds__(backward_block<TPR>(), backward_block<TPR>() =
                 }
             }
         }
-        Pair sa(0.0f), sb(0.0f);
-#pragma unroll
-        for (int q = 0; q < NV; q++) {
-            Pair x[V / 2], g[V / 2];
-            cx[q].pairs(x);
+        // xhat and dy gamma of a chunk; past the row's end dy and gamma are 0,
+        // and so is all that xhat enters
+        const Pair scale(rstd), shift(-mean * rstd);
+        auto widen = [&](int q, Pair(&xhat)[V / 2], Pair(&gg)[V / 2], Pair(&g)[V / 2]) {
+            cx[q].pairs(xhat);
             cy[q].pairs(g);
 #pragma unroll
             for (int i = 0; i < V / 2; i++) {
-                // past the row's end dy and gamma are 0, and so is all that xhat enters
-                const Pair xh = (x[i] + Pair(-mean)) * Pair(rstd), gg = g[i] * gamma[q][i];
-                dg[q][i] = fma2(g[i], xh, dg[q][i]);
+                xhat[i] = fma2(xhat[i], scale, shift);
+                gg[i] = g[i] * gamma[q][i];
+            }
+        };
+        constexpr bool kHold = NV * V <= 16;  // registers
+        Pair held_x[kHold ? NV : 1][V / 2], held_g[kHold ? NV : 1][V / 2];
+        Pair sa(0.0f), sb(0.0f);
+#pragma unroll
+        for (int q = 0; q < NV; q++) {
+            Pair g[V / 2];
+            Pair(&xhat)[V / 2] = held_x[kHold ? q : 0];
+            Pair(&gg)[V / 2] = held_g[kHold ? q : 0];
+            widen(q, xhat, gg, g);
+#pragma unroll
+            for (int i = 0; i < V / 2; i++) {
+                dg[q][i] = fma2(g[i], xhat[i], dg[q][i]);
                 db[q][i] = db[q][i] + g[i];
-                sa = sa + gg;
-                sb = fma2(gg, xh, sb);
+                sa = sa + gg[i];
+                sb = fma2(gg[i], xhat[i], sb);
             }
         }
         float a = warp_sum(sa.sum()), b = warp_sum(sb.sum());
@@ -500,8 +525,8 @@ __global__ void __launch_bounds__(backward_block<TPR>(), backward_block<TPR>() =
         }
         if (!live)
             continue;
-        a *= inv;
-        b *= inv;
+        // dx = rstd (dy gamma - mean(dy gamma) - xhat mean(dy gamma xhat))
+        const Pair ca(-a * inv * rstd), cb(-b * inv * rstd);
         T *dx = static_cast<T *>(p.dx) + r * p.lddx;
 #pragma unroll
         for (int q = 0; q < NV; q++) {
@@ -509,16 +534,17 @@ __global__ void __launch_bounds__(backward_block<TPR>(), backward_block<TPR>() =
             if (c >= p.cols)
                 break;
             float out[V];
-            Pair x[V / 2], g[V / 2];
-            cx[q].keep_packed();
-            cy[q].keep_packed();
-            cx[q].pairs(x);
-            cy[q].pairs(g);
-#pragma unroll
-            for (int i = 0; i < V / 2; i++) {
-                const Pair xh = (x[i] + Pair(-mean)) * Pair(rstd);
-                (Pair(rstd) * fma2(xh, Pair(-b), fma2(g[i], gamma[q][i], Pair(-a)))).get(out[2 * i], out[2 * i + 1]);
+            Pair(&xhat)[V / 2] = held_x[kHold ? q : 0];
+            Pair(&gg)[V / 2] = held_g[kHold ? q : 0];
+            if (!kHold) {
+                Pair g[V / 2];
+                cx[q].keep_packed();
+                cy[q].keep_packed();
+                widen(q, xhat, gg, g);
             }
+#pragma unroll
+            for (int i = 0; i < V / 2; i++)
+                fma2(gg[i], scale, fma2(xhat[i], cb, ca)).get(out[2 * i], out[2 * i + 1]);
             store_chunk<T, kFull>(dx, c, p.cols, out);
         }
     }
@@ -692,18 +718,19 @@ bool forward_shape(int64_t rows, int64_t cols, int sms, F f)
     const int64_t chunks = (cols + Chunk<T>::V - 1) / Chunk<T>::V;
     // 4 chunks a thread where the rows fill the multiprocessors; with few rows
     // their latency counts, and a thread has one chunk.
+    const bool many = rows >= 4 * sms;
     if (chunks <= 32)
         f.template run<T, kFull, 32, 1>();
-    else if (chunks <= 32 * 4 && rows >= 4 * sms)
+    else if (chunks <= 32 * 4 && many)
         f.template run<T, kFull, 32, 4>();
     else if (chunks <= 128)
         f.template run<T, kFull, 128, 1>();
-    else if (chunks <= 128 * 4 && rows >= 4 * sms)
+    else if (chunks <= 128 * 4 && many)
         f.template run<T, kFull, 128, 4>();
+    else if (chunks <= 256 * 4 && many)
+        f.template run<T, kFull, 256, 4>();
     else if (chunks <= 512)
         f.template run<T, kFull, 512, 1>();
-    else if (chunks <= 512 * 2)
-        f.template run<T, kFull, 512, 2>();
     else if (chunks <= 512 * 4)
         f.template run<T, kFull, 512, 4>();
     else if (chunks <= 512 * 8)
@@ -765,7 +792,7 @@ struct Backward {
     {
         constexpr int kBlock = backward_block<TPR>(), kSub = kBlock / TPR;
         constexpr int kJoin = kSub > 1 ? kSub * TPR * NV * Chunk<T>::V * 4 : 0;
-        constexpr int kBudget = kStageBudget * (kBlock / kBackThreads);
+        constexpr int kBudget = kBlock > kBackThreads ? 192 * 1024 : kStageBudget;
         const int stage = 2 * kSub * p.cols * (int)sizeof(T);
         p.stages = kBudget / stage < kMaxStages ? kBudget / stage : kMaxStages;
         if (kFull && p.stages >= 2) {

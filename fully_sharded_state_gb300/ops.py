@@ -17,6 +17,7 @@ from __future__ import annotations
 import ctypes
 from contextlib import nullcontext
 from dataclasses import dataclass
+from functools import lru_cache
 
 import torch
 
@@ -83,10 +84,17 @@ def _on(stream, device):
     return stream.cuda_stream, torch.cuda.stream(stream)
 
 
-def _workspace(query, *sizes, device):
+@lru_cache(maxsize=1024)
+def _workspace_bytes(query, *sizes):
+    """What the library's query `query` says for these sizes."""
     n = _i64(0)
-    capi._check(query(*sizes, ctypes.byref(n)))
-    return torch.empty(max(n.value, 1), dtype=torch.uint8, device=device), n.value
+    capi._check(getattr(capi.load(), query)(*sizes, ctypes.byref(n)))
+    return n.value
+
+
+def _workspace(query, *sizes, device):
+    n = _workspace_bytes(query, *sizes)
+    return torch.empty(n or 1, dtype=torch.uint8, device=device), n
 
 
 def _ptr(t):
@@ -118,9 +126,9 @@ def layer_norm(x, gamma, beta=None, eps: float = 1e-5, out=None, stream=None):
         _vector(beta, "beta", cols, gamma.dtype, x.device)
     handle, ctx = _on(stream, x.device)
     with ctx:
-        y = torch.empty_like(x, memory_format=torch.contiguous_format) if out is None else out
+        y = torch.empty((rows, cols), dtype=x.dtype, device=x.device) if out is None else out
         mean, rstd = torch.empty((2, rows), dtype=torch.float32, device=x.device).unbind(0)
-    ldy = _matrix(y, "out", rows, cols, x.dtype, x.device)
+    ldy = cols if out is None else _matrix(y, "out", rows, cols, x.dtype, x.device)
     capi._check(lib.fsdp_layer_norm(rows, cols, x.data_ptr(), ldx, _DT[x.dtype], gamma.data_ptr(), _ptr(beta),
                                     _DT[gamma.dtype], eps, y.data_ptr(), ldy, mean.data_ptr(),
                                     rstd.data_ptr(), handle))
@@ -140,20 +148,21 @@ def layer_norm_backward(dy, x, gamma, mean, rstd, with_beta: bool = True, dx=Non
     pm = _vector(mean, "mean", rows, torch.float32, dev)
     pr = _vector(rstd, "rstd", rows, torch.float32, dev)
     handle, ctx = _on(stream, dev)
+    lddx = cols if dx is None else _matrix(dx, "dx", rows, cols, x.dtype, dev)
+    if dgamma is not None:
+        _vector(dgamma, "dgamma", cols, gamma.dtype, dev)
+    if dbeta is not None:
+        if not with_beta:
+            _refuse("dbeta is given, but with_beta is false")
+        _vector(dbeta, "dbeta", cols, gamma.dtype, dev)
     with ctx:
         if dx is None:
-            dx = torch.empty_like(x, memory_format=torch.contiguous_format)
+            dx = torch.empty((rows, cols), dtype=x.dtype, device=dev)
         if dgamma is None:
             dgamma = torch.empty(cols, dtype=gamma.dtype, device=dev)
         if with_beta and dbeta is None:
             dbeta = torch.empty(cols, dtype=gamma.dtype, device=dev)
-        ws, nws = _workspace(lib.fsdp_layer_norm_backward_workspace, rows, cols, device=dev)
-    if not (with_beta or dbeta is None):
-        _refuse("dbeta is given, but with_beta is false")
-    lddx = _matrix(dx, "dx", rows, cols, x.dtype, dev)
-    _vector(dgamma, "dgamma", cols, gamma.dtype, dev)
-    if dbeta is not None:
-        _vector(dbeta, "dbeta", cols, gamma.dtype, dev)
+        ws, nws = _workspace("fsdp_layer_norm_backward_workspace", rows, cols, device=dev)
     capi._check(lib.fsdp_layer_norm_backward(
         rows, cols, dy.data_ptr(), lddy, x.data_ptr(), ldx, _DT[x.dtype], gamma.data_ptr(), _DT[gamma.dtype], pm, pr,
         dx.data_ptr(), lddx, dgamma.data_ptr(), _ptr(dbeta), ws.data_ptr(), nws, handle))
@@ -180,16 +189,16 @@ def _loss_call(hidden, weight, targets, ignore_index, reduction, grad, grad_scal
         loss = torch.empty((), dtype=torch.float32, device=dev)
         row_loss = torch.empty(rows, dtype=torch.float32, device=dev)
         if grad:
+            lddh = cols if dhidden is None else _matrix(dhidden, "dhidden", rows, cols, torch.bfloat16, dev)
+            lddw = cols if dweight is None else _matrix(dweight, "dweight", vocab, cols, torch.bfloat16, dev)
             if dhidden is None:
                 dhidden = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
             if dweight is None:
                 dweight = torch.empty((vocab, cols), dtype=torch.bfloat16, device=dev)
-        ws, nws = _workspace(lib.fsdp_linear_cross_entropy_workspace, rows, cols, vocab, int(grad), piece_rows,
+        else:
+            lddh = lddw = cols
+        ws, nws = _workspace("fsdp_linear_cross_entropy_workspace", rows, cols, vocab, int(grad), piece_rows,
                              device=dev)
-    lddh = lddw = cols
-    if grad:
-        lddh = _matrix(dhidden, "dhidden", rows, cols, torch.bfloat16, dev)
-        lddw = _matrix(dweight, "dweight", vocab, cols, torch.bfloat16, dev)
     capi._check(lib.fsdp_linear_cross_entropy(
         rows, cols, vocab, hidden.data_ptr(), ldh, weight.data_ptr(), ldw, pt, int(ignore_index),
         0 if reduction == "mean" else 1, float(grad_scale), loss.data_ptr(), row_loss.data_ptr(), _ptr(dhidden), lddh,
@@ -236,7 +245,7 @@ def newton_schulz(g, steps: int = 5, eps: float = 1e-7, coefficients=NEWTON_SCHU
         batch, m, n = g3.shape
         if not (m > 0 and n > 0):
             _refuse("g has no rows or no columns")
-        ws, nws = _workspace(lib.fsdp_newton_schulz_workspace, batch, m, n, device=g.device)
+        ws, nws = _workspace("fsdp_newton_schulz_workspace", batch, m, n, device=g.device)
     if not (isinstance(out, torch.Tensor) and out.shape == g.shape and out.dtype == torch.bfloat16 and out.device == g.device):
         _refuse(f"out needs shape {tuple(g.shape)}, bfloat16, on {g.device}")
     o3 = out if out.dim() == 3 else out.unsqueeze(0)
@@ -319,7 +328,7 @@ def muon_step(grads, master, momentum, params, hp: MuonHP, stream=None) -> None:
     handle, ctx = _on(stream, dev)
     for k, m, n, R, g, dt, mo, ma, po in calls:
         with ctx:
-            ws, nws = _workspace(lib.fsdp_muon_workspace, k, m, n, device=dev)
+            ws, nws = _workspace("fsdp_muon_workspace", k, m, n, device=dev)
         c = hp._c(m, n)
         capi._check(lib.fsdp_muon(k, m, n, R, g, dt, mo, ma, po, ctypes.byref(c), ws.data_ptr(), nws, handle))
 
