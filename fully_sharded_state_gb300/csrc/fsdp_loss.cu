@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(const uint16_t *src, int
 // from tensor memory twice: for the maximum, then for the exponentials. The
 // exponentials leave by the warp's stage, 64 columns of 32 rows at a time.
 struct LogitsEpi {
-    static constexpr int kLeastTN = kTileN, kBytes = 5;  // 2, and the time of the exponentials
+    static constexpr int kLeastTN = kTileN;
     struct Params {
         uint16_t *e;      // NULL: loss alone
         int64_t lde;
@@ -226,8 +226,8 @@ struct LogitsEpi {
         const float ref = top == -CUDART_INF_F ? 0.0f : top;
         const float shift = ref * kLog2e;
         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        auto exponentials = [&](int chunk, float(&v)[32]) {
-            const int c = (chunk - chunk0) * 32;
+        auto exponentials = [&](int c0, float(&v)[32]) {
+            const int c = c0 * 32;
 #pragma unroll
             for (int i = 0; i < 32; i++) {
                 v[i] = kWhole || c + i < n ? exp2_fast(fmaf(v[i], kLog2e, -shift)) : 0.0f;
@@ -240,7 +240,7 @@ struct LogitsEpi {
 #pragma unroll
             for (int u = 0; u < kChunks / 2; u++) {
                 const int unit = chunk0 / 2 + u, to_col = x.unit_col(unit);
-                x.emit16<false>(unit, exponentials, [&](int i, const uint4 &e) {
+                x.emit16<false>(unit, [&](int h, float(&v)[32]) { exponentials(u * 2 + h, v); }, [&](int i, const uint4 &e) {
                     if (i * 4 < rows && to_col < p.lde)
                         *reinterpret_cast<uint4 *>(to + i * 4 * p.lde + to_col) = e;
                 });
@@ -250,7 +250,7 @@ struct LogitsEpi {
             for (int c = 0; c < kChunks; c++) {
                 float v[32];
                 x.load(chunk0 + c, v);
-                exponentials(chunk0 + c, v);
+                exponentials(c, v);
             }
         }
         if (live) {
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowsParams p)
 
 // dhidden rows back at their own places, bf16.
 struct HiddenEpi {
-    static constexpr int kLeastTN = 64, kBytes = 2;
+    static constexpr int kLeastTN = 64;
     struct Params {
         uint16_t *out;
         int64_t ld;
@@ -448,7 +448,7 @@ struct HiddenEpi {
 
 // Partial sums of split products, fp32.
 struct PartEpi {
-    static constexpr int kLeastTN = 64, kBytes = 4;
+    static constexpr int kLeastTN = 64;
     static constexpr bool kAhead = false;
     struct Params {
         float *out;  // [splits][rows kept][ld], ld a multiple of 8
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(256) join_hidden_kernel(const float *parts, in
 
 // dweight, over the pieces of the rows in fp32 where there are several.
 struct WeightEpi {
-    static constexpr int kLeastTN = 64, kBytes = 2;
+    static constexpr int kLeastTN = 64;
     static constexpr bool kAhead = false;
     struct Params {
         uint16_t *out;
@@ -718,6 +718,7 @@ fsdp_status launch_linear_cross_entropy(const LossArgs &a, void *workspace, int 
         sh.N = (int)a.vocab;
         sh.K = (int)a.cols;
         sh.batch = 1;
+        sh.epi_bytes = 5;  // 2 of each element, and the time of its exponential
         sh.dyn = q.meta;
         sh.dyn_base = (int)row0;
         const Operand ox{x, a.cols, ceil_to(rows, 64), q.ldx, 0};
@@ -766,6 +767,7 @@ fsdp_status launch_linear_cross_entropy(const LossArgs &a, void *workspace, int 
         sd.N = (int)a.cols;
         sd.K = (int)a.vocab;
         sd.batch = 1;
+        sd.epi_bytes = 3;
         sd.dyn = q.meta;
         sd.dyn_base = (int)row0;
         sd.splits = q.splits;
@@ -794,6 +796,7 @@ fsdp_status launch_linear_cross_entropy(const LossArgs &a, void *workspace, int 
         sw.N = (int)a.cols;
         sw.K = rows;
         sw.batch = 1;
+        sw.epi_bytes = 3;
         sw.dyn = q.meta;
         sw.dyn_base = (int)row0;
         sw.dyn_is_k = 1;

@@ -159,49 +159,73 @@ __global__ void __launch_bounds__(kStartThreads) scale_kernel(const float *x32, 
     }
 }
 
-// S, or P = b S + c S^2 (from != NULL), in fp16, both triangles. Strides are
-// multiples of 16, so groups of 8 and pairs of rows stay inside a padded row.
-// S is symmetric: a thread reads the elements of its own row from the columns,
-// where the 32 lanes' are adjacent.
+// S, or (kPoly) P = b S + c S^2, in fp16; both triangles where one is
+// multiplied. Strides are multiples of 16, so groups of 8 and pairs of rows
+// stay inside a padded row.
+template <bool kPoly>
 struct SquareEpi {
-    static constexpr int kLeastTN = 64, kBytes = kSquareBytes;
+    static constexpr int kLeastTN = 64;
     struct Params {
         uint16_t *out;
-        const uint16_t *from;
+        const uint16_t *from;  // S
         int64_t ld, stride;
         float b, c;
     };
-    using Pre = NoPre;
-    static __device__ __forceinline__ void fetch(const Params &, const Slot &, int, Pre &) {}
-    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &)
+    struct Pre {
+        uint4 s[kPoly ? 8 : 1];  // this lane's groups of a unit of S
+    };
+    static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int unit, Pre &pre)
+    {
+        if (!kPoly)
+            return;
+        const int rows = x.M - x.group_row(0);
+        const uint16_t *from = p.from + x.z * p.stride + x.group_row(0) * p.ld + x.unit_col(unit);
+        const bool in = x.unit_col(unit) < x.N;
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (i * 4 < rows && in)
+                pre.s[kPoly ? i : 0] = *reinterpret_cast<const uint4 *>(from + i * 4 * p.ld);
+    }
+    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre)
     {
         uint16_t *out = p.out + x.z * p.stride;
         const int rows = x.M - x.group_row(0);
 #pragma unroll 1
         for (int u = x.part; u < x.units(); u += kParts) {
+            uint4 own[kPoly ? 8 : 1];  // the thread's own row of the unit
+            if (kPoly) {
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    *x.group(i) = pre.s[kPoly ? i : 0];
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    own[kPoly ? i : 0] = *x.piece(x.lane, i);
+                __syncwarp();
+                if (u + kParts < x.units())
+                    fetch(p, x, u + kParts, pre);
+            }
             uint16_t *to = out + x.group_row(0) * p.ld + x.unit_col(u);
             const bool in = x.unit_col(u) < x.N;
-            auto finish = [&](int chunk, float(&v)[32]) {
-                const int col = x.col + chunk * 32;
-                if (p.from) {
-                    const uint16_t *from = p.from + x.z * p.stride + col * p.ld + x.row;
-                    const int n = x.row < x.M ? x.N - col : 0;
-                    uint16_t s[32];
+            auto finish = [&](int h, float(&v)[32]) {
+                if (kPoly) {
 #pragma unroll
-                    for (int j = 0; j < 32; j++)
-                        s[j] = j < n ? from[j * p.ld] : 0;
-#pragma unroll
-                    for (int j = 0; j < 32; j++)
-                        v[j] = fmaf(p.c, v[j], p.b * __half2float(__ushort_as_half(s[j])));
+                    for (int j = 0; j < 16; j++) {
+                        const uint4 &q = own[kPoly ? h * 4 + j / 4 : 0];
+                        const uint32_t w = j % 4 == 0 ? q.x : j % 4 == 1 ? q.y : j % 4 == 2 ? q.z : q.w;
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+                        v[2 * j] = fmaf(p.c, v[2 * j], p.b * f.x);
+                        v[2 * j + 1] = fmaf(p.c, v[2 * j + 1], p.b * f.y);
+                    }
                 }
                 if (!x.mirror)
                     return;
                 // the transposed elements: two rows' on a pair of lanes make
                 // one 32-bit store, of column j on the even and j + 1 on the
                 // odd lane
-                const int odd = x.lane & 1, row = x.row & ~1;
-                const int cols = row < x.M ? x.N - (col + odd) : 0;
-                uint16_t *across = out + (col + odd) * p.ld + row;
+                const int odd = x.lane & 1, row = x.row & ~1, col = x.col + (u * 2 + h) * 32 + odd;
+                const int cols = row < x.M ? x.N - col : 0;
+                uint16_t *across = out + col * p.ld + row;
 #pragma unroll
                 for (int j = 0; j < 32; j += 2) {
                     const float other = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
@@ -239,7 +263,7 @@ struct StepParams {
 
 template <Then kThen>
 struct StepEpi {
-    static constexpr int kLeastTN = 64, kBytes = kStepBytes;
+    static constexpr int kLeastTN = 64;
     static constexpr bool kAhead = kThen != Then::kMaster;  // registers: it has twice the reads
     using Params = StepParams;
     static constexpr bool kMaster = kThen == Then::kMaster;
@@ -430,25 +454,23 @@ fsdp_status launch_newton_schulz(const SchulzArgs &a, void *workspace, int dev, 
     for (int step = 0; step < a.steps; step++) {
         const Operand x{q.x16[step % 2], a.n, a.m, q.ldx, xs};
         const Operand gram{q.s, q.k, q.k, q.ldk, ks}, poly{q.p, q.k, q.k, q.ldk, ks};
-        Shape sq{};
-        sq.M = sq.N = (int)q.k;
-        sq.K = wide ? n : m;
-        sq.batch = batch;
-        sq.sym = 1;
-        const SquareEpi::Params e1{q.s, nullptr, q.ldk, ks, 0.0f, 0.0f};
-        const SquareEpi::Params e2{q.p, q.s, q.ldk, ks, a.b, a.c};
-        st = wide ? product<false, false, SquareEpi>(sq, x, x, false, e1, dev, s, "newton_schulz (S)")
-                  : product<true, true, SquareEpi>(sq, x, x, false, e1, dev, s, "newton_schulz (S)");
+        Shape sq = square_shape(q.k, wide ? n : m, batch, sms, false);
+        const typename SquareEpi<false>::Params e1{q.s, nullptr, q.ldk, ks, 0.0f, 0.0f};
+        const typename SquareEpi<true>::Params e2{q.p, q.s, q.ldk, ks, a.b, a.c};
+        st = wide ? product<false, false, SquareEpi<false>>(sq, x, x, false, e1, dev, s, "newton_schulz (S)")
+                  : product<true, true, SquareEpi<false>>(sq, x, x, false, e1, dev, s, "newton_schulz (S)");
         if (st != FSDP_OK)
             return st;
-        sq.K = (int)q.k;
-        if ((st = product<false, false, SquareEpi>(sq, gram, gram, false, e2, dev, s, "newton_schulz (P)")) != FSDP_OK)
+        sq = square_shape(q.k, q.k, batch, sms, true);
+        if ((st = product<false, false, SquareEpi<true>>(sq, gram, gram, false, e2, dev, s, "newton_schulz (P)")) !=
+            FSDP_OK)
             return st;
         Shape up{};
         up.M = m;
         up.N = n;
         up.K = (int)q.k;
         up.batch = batch;
+        up.epi_bytes = kStepBytes;
         ep.inv = step == 0 ? q.inv : nullptr;
         ep.x16 = q.x16[(step + 1) % 2];
         auto update = [&](auto epi) {

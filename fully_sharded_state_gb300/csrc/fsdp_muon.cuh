@@ -104,26 +104,37 @@ inline SchulzPlan schulz_plan(int64_t batch, int64_t m, int64_t n, void *base)
     return q;
 }
 
+// The product S (or P) of k x k matrices over K: one triangle and its mirror
+// image, or the whole square. The mirror image is scattered stores, 7 bytes'
+// time per element against 3 (S), 9 against 4 (P): it pays where K is long.
+constexpr int kStepBytes = 10;
+inline Shape square_shape(int64_t k, int64_t K, int64_t batch, int sms, bool poly)
+{
+    Shape whole{}, half{};
+    whole.M = whole.N = (int)k;
+    whole.K = (int)K;
+    whole.batch = (int)batch;
+    whole.epi_bytes = poly ? 4 : 3;
+    half = whole;
+    half.sym = 1;
+    half.epi_bytes = poly ? 9 : 7;
+    return best_form(half, sms, 64).cost < best_form(whole, sms, 64).cost ? half : whole;
+}
+
 // Clocks of `steps` steps as one kernel per product: the products' own and,
 // for each, a kernel's start and end.
 constexpr int64_t kLaunchClocks = 4500;
-constexpr int kSquareBytes = 5, kStepBytes = 10;  // of an epilogue, per element
 inline int64_t product_clocks(const SchulzArgs &a, int sms)
 {
     const int64_t k = a.m < a.n ? a.m : a.n, l = a.m < a.n ? a.n : a.m;
-    Shape s{};
-    s.batch = (int)a.batch;
-    s.splits = 1;
-    s.sym = 1;
-    s.M = s.N = (int)k;
-    s.K = (int)l;
-    int64_t t = best_form(s, sms, 64, kSquareBytes).cost;
-    s.K = (int)k;
-    t += best_form(s, sms, 64, kSquareBytes).cost;
-    s.sym = 0;
-    s.M = (int)a.m;
-    s.N = (int)a.n;
-    t += best_form(s, sms, 64, kStepBytes).cost;
+    Shape up{};
+    up.M = (int)a.m;
+    up.N = (int)a.n;
+    up.K = (int)k;
+    up.batch = (int)a.batch;
+    up.epi_bytes = kStepBytes;
+    const int64_t t = best_form(square_shape(k, l, a.batch, sms, false), sms, 64).cost +
+                      best_form(square_shape(k, k, a.batch, sms, true), sms, 64).cost + best_form(up, sms, 64).cost;
     return a.steps * (t + 3 * kLaunchClocks);
 }
 

@@ -241,6 +241,7 @@ struct Shape {
                       // sums): at most so many, chosen by Tiles on the device
     int *splits_out;  // where the number is left, or NULL
     int tn;           // columns of a tile, a multiple of 16, at most TN
+    int epi_bytes;    // what the epilogue moves per element, for the choice of the tile
     int sym;          // only the squares on and above the diagonal (M = N)
     int group;        // row tiles that are walked together, for reuse in L2
     uint32_t idesc;
@@ -483,8 +484,8 @@ struct Slot {
         spread<kBack>(mine, f, staged);
     }
     // A unit as 16-bit numbers, for results that need nothing from memory by
-    // groups: op(chunk, v) works on the thread's own row of each of the two
-    // chunks, f(i, u) gets 8 adjacent results for row group_row(i), from column
+    // groups: op(h, v) works on the thread's own row of chunk h (0, 1) of the
+    // unit, f(i, u) gets 8 adjacent results for row group_row(i), from column
     // unit_col(unit) on. Half the traffic of taking fp32 across.
     __device__ __forceinline__ int unit_col(int unit) const { return col + unit * 64 + lane % 8 * 8; }
     template <bool kBf16, class Op, class F>
@@ -494,7 +495,7 @@ struct Slot {
         for (int h = 0; h < 2; h++) {
             float v[32];
             load_sum(unit * 2 + h, v);
-            op(unit * 2 + h, v);
+            op(h, v);
 #pragma unroll
             for (int g = 0; g < 4; g++)
                 *piece(lane, h * 4 + g) = make_uint4(
@@ -527,7 +528,6 @@ struct Slot {
 
 // An epilogue E has
 //   Params, kLeastTN   its arguments; the narrowest tile it takes
-//   kBytes             what it moves per element, for the choice of the tile
 //   Pre                what it reads from memory for one chunk, in registers
 //   fetch(p, x, chunk, pre)   starts those reads
 //   chunk(p, x, chunk, pre, staged)   finishes a chunk with them; calls
@@ -856,9 +856,8 @@ inline int64_t count_tiles(const Shape &s, int64_t rows, int64_t cols)
 // the one with the least estimate: per wave of tiles the longer of the K
 // blocks' clocks and the epilogue's, the shorter once, and a start. A block's
 // clocks are those of its MMAs (2 per column of the tile) or of its loads at
-// 90 bytes per clock; the epilogue moves its bytes at 35 per clock
-// (measured with all multiprocessors at it: 48 x 512 x 512, 10 bytes per
-// element, 11 us a wave).
+// 90 bytes per clock; the epilogue moves its bytes at 35 per clock (measured
+// with all multiprocessors at it, 48 x 512 x 512).
 struct Form {
     int ctas, tn;
     int columns;          // of a tile: tn, or less where that leaves less of the last tile empty
@@ -869,7 +868,7 @@ inline int64_t block_clocks(int ctas, int tn)
     const int64_t loads = (kTM + tn / ctas) * 128 / 90, mmas = 2 * tn;
     return loads > mmas ? loads : mmas;
 }
-inline Form best_form(const Shape &s, int64_t sms, int least_tn, int epi_bytes)
+inline Form best_form(const Shape &s, int64_t sms, int least_tn)
 {
     const int64_t nk = (s.K + kBK - 1) / kBK;
     Form best{};
@@ -881,7 +880,7 @@ inline Form best_form(const Shape &s, int64_t sms, int least_tn, int epi_bytes)
         const int columns = s.sym || least_tn == 256 ? f[1] : (int)ceil_to((s.N + across - 1) / across, 16);
         Form g{f[0], f[1], columns, count_tiles(s, kTM * f[0], f[1]), 0};
         const int64_t slots = sms / g.ctas < 1 ? 1 : sms / g.ctas, waves = (g.tiles + slots - 1) / slots;
-        const int64_t mma = nk * block_clocks(g.ctas, columns), epi = 1000 + kTM * columns * epi_bytes / 35;
+        const int64_t mma = nk * block_clocks(g.ctas, columns), epi = 1000 + kTM * columns * s.epi_bytes / 35;
         g.cost = (mma > epi ? waves * mma + epi : waves * epi + mma) + 2500;
         if (s.splits > 1)  // spread over the grid whatever the tiles: what one costs, times their number
             g.cost = g.tiles * g.ctas * mma;
@@ -891,14 +890,14 @@ inline Form best_form(const Shape &s, int64_t sms, int least_tn, int epi_bytes)
     return best;
 }
 
-// Launches D = A B^T. `s` needs M, N, K, batch, sym, dyn* and, for split
-// sums, splits; the rest is filled in here.
+// Launches D = A B^T. `s` needs M, N, K, batch, epi_bytes, sym, dyn* and, for
+// split sums, splits; the rest is filled in here.
 template <bool kAMN, bool kBMN, class Epi>
 fsdp_status product(Shape s, const Operand &a, const Operand &b, bool bf16, const typename Epi::Params &ep,
                     int dev, cudaStream_t stream, const char *what)
 {
     s.group = s.group > 0 ? s.group : 8;
-    const Form best = best_form(s, device_sms(dev), Epi::kLeastTN, Epi::kBytes);
+    const Form best = best_form(s, device_sms(dev), Epi::kLeastTN);
     s.tn = best.columns;
     if (best.tiles < 1)
         return FSDP_OK;
