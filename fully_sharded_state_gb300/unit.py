@@ -11,6 +11,8 @@ Per rank r the unit keeps: ``master[r]`` (fp32 master shard), ``m[r]`` and
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import capi
@@ -115,6 +117,36 @@ class ShardedUnit:
         t = self._next_step(step)
         capi.fsdp_adamw_from_reduced(self.layout, grad_avg_full, self.master, self.m, self.v,
                                      self.param_shard, hp, t, stream)
+        self.step = t
+
+    def reduce_scatter_muon(self, grads, hp, step: int | None = None, stream=None) -> None:
+        """One Muon step (``ops.MuonHP``) from the R ranks' full local
+        gradients: fold, momentum and orthogonal update of every parameter at
+        its owner rank, ``m`` being the momentum. The update needs whole
+        matrices at one rank, so the unit has mode "zero3" and no vectors
+        (norm scales and biases go into a unit of their own, with AdamW).
+        A parameter of more than two dimensions is the matrix of its rows."""
+        from . import ops
+        if self.mode != "zero3":
+            raise capi.FsdpArgumentError(f"Muon needs mode 'zero3' (whole matrices at one rank), not '{self.mode}'")
+        flat = [n for n, s in zip(self.names, self.shapes) if len(s) < 2]
+        if flat:
+            raise capi.FsdpArgumentError(f"Muon updates matrices; {flat} are vectors")
+        capi._Args().array(grads, self.R, "grad_full", self.P, _DT[self.grad_dtype][0])
+        t = self._next_step(step)
+        work = ([], [], [], [])  # grads, master, momentum, params
+        for i, shape in enumerate(self.shapes):
+            rows, n = shape[0], math.prod(shape)
+            if n == 0:
+                continue
+            r, at, full = (self.layout.param_owner(i), self.layout.param_shard_offset(i),
+                           self.layout.param_full_offset(i))
+            work[0].append([g[full:full + n].view(rows, -1) for g in grads])
+            work[1].append(self.master[r][at:at + n].view(rows, -1))
+            work[2].append(self.m[r][at:at + n].view(rows, -1))
+            if self.param_shard is not None:
+                work[3].append(self.param_shard[r][at:at + n].view(rows, -1))
+        ops.muon_step(*work[:3], work[3] if self.param_shard is not None else None, hp, stream)
         self.step = t
 
     # -- prepared calls (checked once, re-issued every step) -----------------
