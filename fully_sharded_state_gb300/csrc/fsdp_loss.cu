@@ -10,10 +10,11 @@
 //             fp16 (2^-11 of a number in (0, 1]; the logits themselves are
 //             never stored)
 //   rows      joins a row's pieces: log-sum-exp and loss; for the gradients it
-//             turns the exponentials into G = (softmax - onehot) * scale, in
-//             place, as bf16: the one rounding of G
+//             turns the exponentials into G = softmax - onehot, in place, as
+//             bf16: the one rounding of G. Unscaled, because 1 - p of a
+//             target is near 1, which is exact, and 1/3 of it is not
 //   dhidden   G weight, and dweight = G^T hidden, on the tensor cores, reading
-//             weight, G and hidden as they lie (no transposes)
+//             weight, G and hidden as they lie (no transposes), scaled in fp32
 //
 // 6 * rows * cols * vocab flops for a step: nothing is computed twice.
 #include <math_constants.h>
@@ -277,7 +278,6 @@ struct RowsParams {
     float *row_loss;
     float *loss;           // the last piece: where the loss goes
     int *done;             // blocks that are through (zero before)
-    float grad_scale;
     int mean;
 };
 
@@ -312,12 +312,22 @@ __device__ __forceinline__ float reduce_sum(float v, float *sh)
 
 // Two exponentials as fp16 -> two elements of G as bf16; t: which of them is
 // the target's, if any.
-__device__ __forceinline__ uint32_t two_of_g(uint32_t e, float f, float scale, int t)
+__device__ __forceinline__ uint32_t two_of_g(uint32_t e, float f, int t)
 {
     const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&e));
-    const float a = v.x * f - (t == 0 ? 1.0f : 0.0f), b = v.y * f - (t == 1 ? 1.0f : 0.0f);
-    return pack_bf16(a * scale, b * scale);
+    return pack_bf16(v.x * f - (t == 0 ? 1.0f : 0.0f), v.y * f - (t == 1 ? 1.0f : 0.0f));
 }
+
+// What the gradients are multiplied by.
+struct Scale {
+    const int *meta;
+    float grad_scale;
+    int mean;
+    __device__ __forceinline__ float get() const
+    {
+        return mean ? grad_scale / (float)max(meta[1], 1) : grad_scale;
+    }
+};
 
 // Grid (rows, segments of the columns): with few rows several blocks share
 // one, each joining its pieces for itself (256 x 32000: 16 us with one block
@@ -330,7 +340,6 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowsParams p)
     launch_next();
     const int n = min(max(p.meta[0] - p.base, 0), p.piece_rows);
     const int end = p.e ? (n + 63) / 64 * 64 : n;  // up to the next whole K block: zeros of G
-    const float scale = p.mean ? p.grad_scale / (float)max(p.meta[1], 1) : p.grad_scale;
     const int cols = min((p.vocab + 7) / 8 * 8, (int)(blockIdx.y + 1) * p.segment), col0 = blockIdx.y * p.segment;
     constexpr int kStep = 256 * 8, kFlight = 4;
     for (int r = blockIdx.x; r < end; r += gridDim.x) {
@@ -362,10 +371,10 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowsParams p)
         auto turn = [&](uint4 u, int c) {
             const float q = st[c / kPieceCols].x;
             const float f = expf((q == -CUDART_INF_F ? 0.0f : q) - ref) * inv;
-            u.x = two_of_g(u.x, f, scale, t - c);
-            u.y = two_of_g(u.y, f, scale, t - c - 2);
-            u.z = two_of_g(u.z, f, scale, t - c - 4);
-            u.w = two_of_g(u.w, f, scale, t - c - 6);
+            u.x = two_of_g(u.x, f, t - c);
+            u.y = two_of_g(u.y, f, t - c - 2);
+            u.z = two_of_g(u.z, f, t - c - 4);
+            u.w = two_of_g(u.w, f, t - c - 6);
             *reinterpret_cast<uint4 *>(e + c) = u;
         };
         int c = col0 + threadIdx.x * 8;
@@ -411,15 +420,18 @@ struct HiddenEpi {
         uint16_t *out;
         int64_t ld;
         const int *source;
+        Scale scale;
     };
     struct Pre {
         int row[8];
+        float scale;
     };
     static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int, Pre &pre)
     {
 #pragma unroll
         for (int i = 0; i < 8; i++)
             pre.row[i] = x.group_row(i) < x.M ? p.source[x.group_row(i)] : -1;
+        pre.scale = p.scale.get();
     }
     static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre)
     {
@@ -427,7 +439,12 @@ struct HiddenEpi {
 #pragma unroll 1
             for (int u = x.part; u < x.units(); u += kParts) {
                 const int col = x.unit_col(u);
-                x.emit16<true>(u, [](int, float(&)[32]) {}, [&](int i, const uint4 &e) {
+                auto scaled = [&](int, float(&v)[32]) {
+#pragma unroll
+                    for (int i = 0; i < 32; i++)
+                        v[i] *= pre.scale;
+                };
+                x.emit16<true>(u, scaled, [&](int i, const uint4 &e) {
                     if (pre.row[i] >= 0)
                         put8_16(p.out + (int64_t)pre.row[i] * p.ld + col, e, x.N - col);
                 });
@@ -439,7 +456,7 @@ struct HiddenEpi {
                 x.by_rows(c, [&](int r, float v) {
                     const int row = x.row - x.lane + r;
                     if (row < x.M && col < x.N)
-                        p.out[(int64_t)p.source[row] * p.ld + col] = to_bf16(v);
+                        p.out[(int64_t)p.source[row] * p.ld + col] = to_bf16(v * pre.scale);
                 });
             }
         }
@@ -455,6 +472,7 @@ struct PartEpi {
         int64_t ld;
     };
     using Pre = NoPre;
+    static __device__ __forceinline__ void carry(const Pre &, Pre &) {}
     static __device__ __forceinline__ void fetch(const Params &, const Slot &, int, Pre &) {}
     template <class G>
     static __device__ __forceinline__ void chunk(const Params &p, const Slot &x, int c, Pre &, G staged)
@@ -475,7 +493,7 @@ struct PartEpi {
 // them) per block.
 __global__ void __launch_bounds__(256) join_hidden_kernel(const float *parts, int64_t ldp, const int *meta, int base,
                                                           int piece_rows, int cols, const int *source, uint16_t *out,
-                                                          int64_t ld)
+                                                          int64_t ld, Scale scale)
 {
     __shared__ float4 sh[4][64];
     launch_wait();
@@ -501,7 +519,7 @@ __global__ void __launch_bounds__(256) join_hidden_kernel(const float *parts, in
                 const float4 f = sh[q][group];
                 s.x += f.x, s.y += f.y, s.z += f.z, s.w += f.w;
             }
-            const float v[4] = {s.x, s.y, s.z, s.w};
+            const float k = scale.get(), v[4] = {s.x * k, s.y * k, s.z * k, s.w * k};
             put4_16<true>(out + (int64_t)source[r] * ld + c, v, cols - c);
         }
         __syncthreads();
@@ -518,12 +536,17 @@ struct WeightEpi {
         float *sum;  // NULL: one piece
         int64_t lds; // a multiple of 8
         int first, last;
+        Scale scale;
     };
     struct Pre {
         float4 o[8];
+        float scale;
     };
+    static __device__ __forceinline__ void carry(const Pre &from, Pre &to) { to.scale = from.scale; }
     static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int chunk, Pre &pre)
     {
+        if (chunk == x.part)
+            pre.scale = p.scale.get();
         if (!p.sum || p.first)
             return;
         const int rows = x.M - x.group_row(0);
@@ -550,9 +573,12 @@ struct WeightEpi {
                     v[2] += pre.o[i].z;
                     v[3] += pre.o[i].w;
                 }
-                if (p.last)
+                if (p.last) {
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        v[k] *= pre.scale;
                     put4_16<true>(to + i * 4 * p.ld, v, left);
-                else
+                } else
                     *reinterpret_cast<float4 *>(sum + i * 4 * p.lds) = make_float4(v[0], v[1], v[2], v[3]);
             }, staged);
         }
@@ -567,7 +593,12 @@ struct WeightEpi {
             for (int u = x.part; u < x.units(); u += kParts) {
                 uint16_t *to = p.out + x.group_row(0) * p.ld + x.unit_col(u);
                 const int left = x.N - x.unit_col(u);
-                x.emit16<true>(u, [](int, float(&)[32]) {}, [&](int i, const uint4 &e) {
+                auto scaled = [&](int, float(&v)[32]) {
+#pragma unroll
+                    for (int i = 0; i < 32; i++)
+                        v[i] *= pre.scale;
+                };
+                x.emit16<true>(u, scaled, [&](int i, const uint4 &e) {
                     if (i * 4 < rows)
                         put8_16(to + i * 4 * p.ld, e, left);
                 });
@@ -581,7 +612,7 @@ struct WeightEpi {
                 const bool in = x.col + c * 32 + x.lane < x.N;
                 x.by_rows(c, [&](int r, float v) {
                     if (r < n && in)
-                        row[r * p.ld] = to_bf16(v);
+                        row[r * p.ld] = to_bf16(v * pre.scale);
                 });
             }
         }
@@ -744,7 +775,6 @@ fsdp_status launch_linear_cross_entropy(const LossArgs &a, void *workspace, int 
         rp.done = q.meta + 2;
         rp.tlogit = q.tlogit + row0;
         rp.row_loss = a.row_loss;
-        rp.grad_scale = a.grad_scale;
         rp.mean = a.mean;
         const int64_t rows_grid = ceil_to(rows, 64) < 8 * sms ? ceil_to(rows, 64) : 8 * sms;
         int64_t segments = grad ? 8 * sms / rows_grid : 1;
@@ -773,6 +803,7 @@ fsdp_status launch_linear_cross_entropy(const LossArgs &a, void *workspace, int 
         sd.splits = q.splits;
         sd.splits_out = q.meta + 3;
         uint16_t *dh = static_cast<uint16_t *>(a.dhidden);
+        const Scale scale{q.meta, a.grad_scale, a.mean};
         if (q.splits > 1) {
             st = product<false, true, PartEpi>(sd, og, owt, true, {q.parts, q.ldp}, dev, s,
                                                           "linear_cross_entropy (dhidden)");
@@ -780,9 +811,9 @@ fsdp_status launch_linear_cross_entropy(const LossArgs &a, void *workspace, int 
                 return st;
             st = launch("linear_cross_entropy (dhidden, sum)", join_hidden_kernel,
                         dim3((unsigned)(rows < 16 * sms ? rows : 16 * sms), (unsigned)((a.cols + 255) / 256)), 256, 0,
-                        s, 1, q.parts, q.ldp, q.meta, row0, rows, a.cols, q.source + row0, dh, a.lddh);
+                        s, 1, q.parts, q.ldp, q.meta, row0, rows, a.cols, q.source + row0, dh, a.lddh, scale);
         } else {
-            st = product<false, true, HiddenEpi>(sd, og, owt, true, {dh, a.lddh, q.source + row0}, dev, s,
+            st = product<false, true, HiddenEpi>(sd, og, owt, true, {dh, a.lddh, q.source + row0, scale}, dev, s,
                                                             "linear_cross_entropy (dhidden)");
         }
         if (st != FSDP_OK)
@@ -801,7 +832,7 @@ fsdp_status launch_linear_cross_entropy(const LossArgs &a, void *workspace, int 
         sw.dyn_base = (int)row0;
         sw.dyn_is_k = 1;
         const WeightEpi::Params we{static_cast<uint16_t *>(a.dweight), a.lddw, q.dw, q.ldp, piece == 0,
-                                   piece + 1 == q.pieces};
+                                   piece + 1 == q.pieces, scale};
         if ((st = product<true, true, WeightEpi>(sw, ogt, oxt, true, we, dev, s,
                                                             "linear_cross_entropy (dweight)")) != FSDP_OK)
             return st;

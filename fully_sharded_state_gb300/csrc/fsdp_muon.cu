@@ -5,18 +5,18 @@
 //            step also the fold of the R ranks' gradients and the momentum
 //   scale    x = u / (||u||_F + eps) in fp16, for the products; the fp32 u
 //            is scaled where it is read next, in the first step's epilogue
-//   steps x  S = x x^T (or x^T x: the smaller side), P = b S + c S^2 and
-//            x = a x + P x, three products on the tensor cores. S and P are
+//   steps x  S = x x^T (or x^T x: the smaller side), P = b S + c S^2 - d I and
+//            x = (a + d) x + P x, three products on the tensor cores. S and P are
 //            symmetric: only the squares on and above the diagonal are
 //            multiplied, and the epilogue stores both triangles.
 //   the last product's epilogue writes the result, or updates the master
 //
-// Numbers: the operands are fp16 (all are at most about 1 in size; 2^-11
+// Numbers: the operands are fp16 (all are at most about 5 in size; 2^-11
 // each), sums are fp32, and x itself is carried in fp32, so that the linear
-// term a x is never rounded: with x kept in fp16 alone, a 512 x 512 gradient
-// of rank 16 under 1 % noise comes out 4e-2 off (its small directions grow by
-// a per step, and the rounding with them); so it is 4e-4 off. Full-rank
-// gradients: 1.5e-3 either way.
+// term is never rounded: with x kept in fp16 alone, a 512 x 512 gradient of
+// rank 16 under 1 % noise comes out 4e-2 off (its small directions grow by a
+// per step, and the rounding with them). P is shifted along its diagonal
+// (shift_of): 4e-4 to 7e-4 off for that gradient, 8e-4 for a Gaussian one.
 #include "fsdp_muon.cuh"
 
 namespace fsdp {
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kStartThreads) scale_kernel(const float *x32, 
     }
 }
 
-// S, or (kPoly) P = b S + c S^2, in fp16; both triangles where one is
+// S, or (kPoly) P = b S + c S^2 - d I, in fp16; both triangles where one is
 // multiplied. Strides are multiples of 16, so groups of 8 and pairs of rows
 // stay inside a padded row.
 template <bool kPoly>
@@ -170,14 +170,19 @@ struct SquareEpi {
         const uint16_t *from;  // S
         int64_t ld, stride;
         float b, c;
+        float *trace;          // [batch][groups], of S
+        int groups;
     };
     struct Pre {
         uint4 s[kPoly ? 8 : 1];  // this lane's groups of a unit of S
+        float shift;
     };
     static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int unit, Pre &pre)
     {
         if (!kPoly)
             return;
+        if (unit == x.part)
+            pre.shift = shift_of(p.trace + x.z * p.groups, x.M, p.b, p.c, x.lane);
         const int rows = x.M - x.group_row(0);
         const uint16_t *from = p.from + x.z * p.stride + x.group_row(0) * p.ld + x.unit_col(unit);
         const bool in = x.unit_col(unit) < x.N;
@@ -218,6 +223,17 @@ struct SquareEpi {
                         v[2 * j + 1] = fmaf(p.c, v[2 * j + 1], p.b * f.y);
                     }
                 }
+                if (x.col + (u * 2 + h) * 32 == x.row - x.lane) {  // the diagonal's chunk
+                    if (kPoly) {
+#pragma unroll
+                        for (int j = 0; j < 32; j++)
+                            v[j] -= x.lane == j ? pre.shift : 0.0f;
+                    } else {
+                        const float sum = diagonal_sum(v, x.lane);
+                        if (x.lane == 0 && x.row < x.M)
+                            p.trace[x.z * p.groups + x.row / 32] = sum;
+                    }
+                }
                 if (!x.mirror)
                     return;
                 // the transposed elements: two rows' on a pair of lanes make
@@ -242,7 +258,7 @@ struct SquareEpi {
     }
 };
 
-// x = a x + (P x), x the fp32 one. What becomes of it:
+// x = (a + d) x + (P x), x the fp32 one. What becomes of it:
 //   kKeep    fp32 in place, and the next step's fp16 operand
 //   kOut     the result, in bf16
 //   kMaster  w = w decay - lr x, and the bf16 parameter
@@ -252,7 +268,9 @@ struct StepParams {
     float *x32;
     const float *inv;  // the first step's factor of x32, per matrix; NULL: 1
     int64_t ld, stride;
-    float a;
+    float a, b, c;
+    const float *trace;
+    int groups, k;
     uint16_t *x16;
     uint16_t *out;
     int64_t ldo, out_stride, n;
@@ -267,6 +285,8 @@ struct StepEpi {
     static constexpr bool kAhead = kThen != Then::kMaster;  // registers: it has twice the reads
     using Params = StepParams;
     static constexpr bool kMaster = kThen == Then::kMaster;
+    struct Pre;
+    static __device__ __forceinline__ void carry(const Pre &from, Pre &to) { to.a = from.a; }
     struct Pre {
         float a;
         float4 x[8];
@@ -274,7 +294,11 @@ struct StepEpi {
     static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int chunk, Pre &pre)
     {
         const int rows = x.M - x.group_row(0), left = x.N - x.group_col(chunk);
-        pre.a = p.inv ? p.a * p.inv[x.z] : p.a;
+        if (chunk == x.part) {
+            pre.a = p.a + shift_of(p.trace + x.z * p.groups, p.k, p.b, p.c, x.lane);
+            if (p.inv)
+                pre.a *= p.inv[x.z];
+        }
         const float *from = p.x32 + x.z * p.stride + x.group_row(0) * p.ld + x.group_col(chunk);
 #pragma unroll
         for (int i = 0; i < 8; i++)
@@ -440,7 +464,10 @@ fsdp_status launch_newton_schulz(const SchulzArgs &a, void *workspace, int dev, 
     ep.x32 = q.x32;
     ep.ld = q.ldx;
     ep.stride = xs;
-    ep.a = a.a;
+    ep.a = a.a, ep.b = a.b, ep.c = a.c;
+    ep.trace = q.trace;
+    ep.groups = (int)q.groups;
+    ep.k = (int)q.k;
     ep.out = static_cast<uint16_t *>(a.out);
     ep.ldo = a.ldo;
     ep.out_stride = a.out_stride;
@@ -455,8 +482,8 @@ fsdp_status launch_newton_schulz(const SchulzArgs &a, void *workspace, int dev, 
         const Operand x{q.x16[step % 2], a.n, a.m, q.ldx, xs};
         const Operand gram{q.s, q.k, q.k, q.ldk, ks}, poly{q.p, q.k, q.k, q.ldk, ks};
         Shape sq = square_shape(q.k, wide ? n : m, batch, sms, false);
-        const typename SquareEpi<false>::Params e1{q.s, nullptr, q.ldk, ks, 0.0f, 0.0f};
-        const typename SquareEpi<true>::Params e2{q.p, q.s, q.ldk, ks, a.b, a.c};
+        const typename SquareEpi<false>::Params e1{q.s, nullptr, q.ldk, ks, 0.0f, 0.0f, q.trace, (int)q.groups};
+        const typename SquareEpi<true>::Params e2{q.p, q.s, q.ldk, ks, a.b, a.c, q.trace, (int)q.groups};
         st = wide ? product<false, false, SquareEpi<false>>(sq, x, x, false, e1, dev, s, "newton_schulz (S)")
                   : product<true, true, SquareEpi<false>>(sq, x, x, false, e1, dev, s, "newton_schulz (S)");
         if (st != FSDP_OK)

@@ -243,6 +243,7 @@ struct Shape {
     int tn;           // columns of a tile, a multiple of 16, at most TN
     int epi_bytes;    // what the epilogue moves per element, for the choice of the tile
     int sym;          // only the squares on and above the diagonal (M = N)
+    int square;       // tiles' columns start on multiples of 32, as their rows do
     int group;        // row tiles that are walked together, for reuse in L2
     uint32_t idesc;
     const int *dyn;   // NULL, or a device count that limits M or K:
@@ -532,6 +533,7 @@ struct Slot {
 //   fetch(p, x, chunk, pre)   starts those reads
 //   chunk(p, x, chunk, pre, staged)   finishes a chunk with them; calls
 //                      staged() once the accumulator's registers are free
+//   carry(from, to)    copies what all chunks of a tile share
 // The first chunk's reads are started before the accumulator is waited for,
 // and with kAhead each chunk's while the one before it is finished: with reads and
 // stores in turn, their latency made up most of a short product.
@@ -539,6 +541,7 @@ template <class E>
 __device__ __forceinline__ void finish_tile(const typename E::Params &p, const Slot &x, typename E::Pre &a)
 {
     typename E::Pre b;
+    E::carry(a, b);
 #pragma unroll 1
     for (int c = x.part; c < x.chunks; c += 2 * kParts) {
         const int d = c + kParts, e = d + kParts;
@@ -877,7 +880,7 @@ inline Form best_form(const Shape &s, int64_t sms, int least_tn)
         if (f[1] < least_tn)
             continue;
         const int64_t across = (s.N + f[1] - 1) / f[1];
-        const int columns = s.sym || least_tn == 256 ? f[1] : (int)ceil_to((s.N + across - 1) / across, 16);
+        const int columns = s.square || least_tn == 256 ? f[1] : (int)ceil_to((s.N + across - 1) / across, 16);
         Form g{f[0], f[1], columns, count_tiles(s, kTM * f[0], f[1]), 0};
         const int64_t slots = sms / g.ctas < 1 ? 1 : sms / g.ctas, waves = (g.tiles + slots - 1) / slots;
         const int64_t mma = nk * block_clocks(g.ctas, columns), epi = 1000 + kTM * columns * s.epi_bytes / 35;

@@ -28,7 +28,8 @@ struct TeamParams {
     float eps, a, b, c;
     int64_t ldx, xs, ldk, ks;
     uint16_t *x16[2], *s, *p;
-    float *partial;
+    float *partial, *trace;
+    int groups;  // of 32 rows of S
     unsigned *arrived;
     // newton_schulz
     const void *g;
@@ -361,7 +362,16 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
                     };
                     if (which == 1 && part < TN / 32)
                         fetch_s(part);
-                    ok = !epi_any(!bar_wait(acc_full, parity));
+                    // P's shift, while the product runs. S is complete once its
+                    // meeting is; x comes a meeting later.
+                    const bool diagonal = k_row + quarter * 32 >= k_col && k_row + quarter * 32 < k_col + TN;
+                    float shift = 0.0f;
+                    bool seen = true;
+                    if (which == 1 && diagonal)
+                        seen = __all_sync(0xffffffffu, team_wait(arrived, (unsigned)q.size * (met + 2 + t)));
+                    if (seen && (which == 2 || (which == 1 && diagonal)))
+                        shift = shift_of(q.trace + z * q.groups, q.k, q.b, q.c, lane);
+                    ok = !epi_any(!seen || !bar_wait(acc_full, parity));
                     parity ^= 1;
                     if (!ok)
                         break;
@@ -374,6 +384,12 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
                                 fetch_s(c);
                             float mine[32];
                             y.load(c, mine);
+                            const bool here = y.col + c * 32 == y.row - lane;  // the diagonal's chunk
+                            if (here && which == 0) {
+                                const float sum = diagonal_sum(mine, lane);
+                                if (lane == 0 && y.row < q.k)
+                                    q.trace[z * q.groups + y.row / 32] = sum;
+                            }
                             uint16_t *to = out + y.group_row(0) * q.ldk + y.group_col(c);
                             const bool in = y.group_col(c) < q.k;
                             y.spread<false>(mine, [&](int i, float(&v)[4]) {
@@ -386,6 +402,11 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
                                     v[1] = fmaf(q.c, v[1], q.b * f.y);
                                     v[2] = fmaf(q.c, v[2], q.b * g.x);
                                     v[3] = fmaf(q.c, v[3], q.b * g.y);
+                                    if (here) {
+#pragma unroll
+                                        for (int k = 0; k < 4; k++)
+                                            v[k] -= lane % 8 * 4 + k == i * 4 + lane / 8 ? shift : 0.0f;
+                                    }
                                 }
                                 *reinterpret_cast<uint2 *>(to + i * 4 * q.ldk) = four_16<false>(v);
                             });
@@ -398,7 +419,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
                             tmem_load32(held + c * 32, old);
 #pragma unroll
                             for (int i = 0; i < 32; i++)
-                                mine[i] = fmaf(q.a, old[i], mine[i]);
+                                mine[i] = fmaf(q.a + shift, old[i], mine[i]);
                             if (!last) {
                                 tmem_store32(held + c * 32, mine);
                                 keep(q.x16[(t / 3 + 1) % 2], c, mine);
@@ -531,6 +552,8 @@ fsdp_status launch_team(const SchulzArgs &a, void *workspace, int dev, void *str
     p.ldx = q.ldx, p.xs = a.m * q.ldx, p.ldk = q.ldk, p.ks = q.k * q.ldk;
     p.x16[0] = q.x16[0], p.x16[1] = q.x16[1], p.s = q.s, p.p = q.p;
     p.partial = q.partial;
+    p.trace = q.trace;
+    p.groups = (int)q.groups;
     p.arrived = q.arrived;
     uintptr_t low = 0;  // of every row's start
     if (muon) {

@@ -71,9 +71,9 @@ typedef enum { FSDP_MEAN = 0, FSDP_SUM = 1 } fsdp_reduction;
 /* Softmax cross entropy of a linear head, without the rows x vocab logits:
  *   z = hidden weight^T;  row_loss_n = log sum_v exp(z_nv) - z_n,target_n
  *   loss = sum_n row_loss_n / count (FSDP_MEAN) or the sum (FSDP_SUM)
- * and, where dhidden is not NULL, with G = (softmax(z) - onehot(target)) * s,
+ * and, where dhidden is not NULL, with G = softmax(z) - onehot(target) and
  * s = grad_scale / count or grad_scale:
- *   dhidden = G weight;  dweight = G^T hidden
+ *   dhidden = s G weight;  dweight = s G^T hidden
  * hidden [rows, cols], weight [vocab, cols], dhidden, dweight: bf16.
  * targets [rows] int64. A row whose target is ignore_index counts for
  * nothing, whatever its hidden holds: row_loss 0, dhidden 0, no part in
