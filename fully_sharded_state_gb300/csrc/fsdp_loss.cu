@@ -463,32 +463,6 @@ struct HiddenEpi {
     }
 };
 
-// Partial sums of split products, fp32.
-struct PartEpi {
-    static constexpr int kLeastTN = 64;
-    static constexpr bool kAhead = false;
-    struct Params {
-        float *out;  // [splits][rows kept][ld], ld a multiple of 8
-        int64_t ld;
-    };
-    using Pre = NoPre;
-    static __device__ __forceinline__ void carry(const Pre &, Pre &) {}
-    static __device__ __forceinline__ void fetch(const Params &, const Slot &, int, Pre &) {}
-    template <class G>
-    static __device__ __forceinline__ void chunk(const Params &p, const Slot &x, int c, Pre &, G staged)
-    {
-        float mine[32];
-        const int rows = x.M - x.group_row(0);
-        const bool in = x.group_col(c) < x.N;
-        float *to = p.out + ((int64_t)x.split * x.M + x.group_row(0)) * p.ld + x.group_col(c);
-        x.across<false>(c, mine, [&](int i, float(&v)[4]) {
-            if (i * 4 < rows && in)
-                *reinterpret_cast<float4 *>(to + i * 4 * p.ld) = make_float4(v[0], v[1], v[2], v[3]);
-        }, staged);
-    }
-    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre) { finish_tile<PartEpi>(p, x, pre); }
-};
-
 // Adds the parts up: 64 groups of 4 columns, 4 slices of the parts (meta[3] of
 // them) per block.
 __global__ void __launch_bounds__(256) join_hidden_kernel(const float *parts, int64_t ldp, const int *meta, int base,
@@ -633,15 +607,6 @@ struct Plan {
 
 bool map_ok(const void *p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0; }
 
-
-// fp32 numbers that dhidden's parts take: choose_splits makes four waves of
-// tiles at most, each of 128 x 256 per multiprocessor and a row's padding, and
-// never more than all parts whole.
-int64_t parts_floats(int64_t ldp, int64_t splits, int64_t rows)
-{
-    const int64_t waves = 4 * kSplitSms * int64_t(kTM) * (kTileN + 8), whole = splits * rows * ldp;
-    return waves < whole ? waves : whole;
-}
 
 Plan plan_of(const LossArgs &a, bool grad, void *base, bool with_weight)
 {

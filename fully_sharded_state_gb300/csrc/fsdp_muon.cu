@@ -258,6 +258,46 @@ struct SquareEpi {
     }
 };
 
+// S from the parts of its sum: a block has 32 rows, and their diagonal's sum.
+__global__ void __launch_bounds__(256) join_square_kernel(const float *parts, const int *splits_used, int k, int64_t ld,
+                                                          uint16_t *out, int64_t stride, float *trace, int groups)
+{
+    __shared__ float diagonal[32];
+    launch_wait();
+    launch_next();
+    const int splits = *splits_used, z = blockIdx.y, row0 = blockIdx.x * 32;
+    const float *src = parts + (int64_t)z * splits * k * ld;
+    const int quads = (k + 3) / 4;  // groups of 4 columns
+    if (threadIdx.x < 32)
+        diagonal[threadIdx.x] = 0.0f;
+    __syncthreads();
+    for (int i = threadIdx.x; i < 32 * quads; i += 256) {
+        const int r = i / quads, row = row0 + r, c = (i - r * quads) * 4;
+        if (row >= k)
+            break;
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+        for (int q = 0; q < splits; q++) {
+            const float4 f = *reinterpret_cast<const float4 *>(src + ((int64_t)q * k + row) * ld + c);
+            v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+        }
+        *reinterpret_cast<uint2 *>(out + z * stride + row * ld + c) = four_16<false>(v);
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            if (c + j == row)
+                diagonal[r] = v[j];
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        float s = diagonal[threadIdx.x];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (threadIdx.x == 0)
+            trace[z * groups + blockIdx.x] = s;
+    }
+}
+
 // x = (a + d) x + (P x), x the fp32 one. What becomes of it:
 //   kKeep    fp32 in place, and the next step's fp16 operand
 //   kOut     the result, in bf16
@@ -484,8 +524,20 @@ fsdp_status launch_newton_schulz(const SchulzArgs &a, void *workspace, int dev, 
         Shape sq = square_shape(q.k, wide ? n : m, batch, sms, false);
         const typename SquareEpi<false>::Params e1{q.s, nullptr, q.ldk, ks, 0.0f, 0.0f, q.trace, (int)q.groups};
         const typename SquareEpi<true>::Params e2{q.p, q.s, q.ldk, ks, a.b, a.c, q.trace, (int)q.groups};
-        st = wide ? product<false, false, SquareEpi<false>>(sq, x, x, false, e1, dev, s, "newton_schulz (S)")
-                  : product<true, true, SquareEpi<false>>(sq, x, x, false, e1, dev, s, "newton_schulz (S)");
+        if (q.splits > 1) {
+            sq.sym = sq.square = 0;
+            sq.splits = q.splits;
+            sq.splits_out = q.splits_used;
+            const PartEpi::Params pe{q.parts, q.ldk};
+            st = wide ? product<false, false, PartEpi>(sq, x, x, false, pe, dev, s, "newton_schulz (S, parts)")
+                      : product<true, true, PartEpi>(sq, x, x, false, pe, dev, s, "newton_schulz (S, parts)");
+            if (st == FSDP_OK)
+                st = launch("newton_schulz (S, sum)", join_square_kernel, dim3((unsigned)q.groups, batch), 256, 0, s, 1,
+                            q.parts, q.splits_used, q.k, q.ldk, q.s, ks, q.trace, q.groups);
+        } else {
+            st = wide ? product<false, false, SquareEpi<false>>(sq, x, x, false, e1, dev, s, "newton_schulz (S)")
+                      : product<true, true, SquareEpi<false>>(sq, x, x, false, e1, dev, s, "newton_schulz (S)");
+        }
         if (st != FSDP_OK)
             return st;
         sq = square_shape(q.k, q.k, batch, sms, true);

@@ -106,11 +106,25 @@ __device__ __forceinline__ float diagonal_sum(const float (&v)[32], int lane)
     return s;
 }
 
+// S sums over the matrix's longer side. Where even its smallest tiles (128 x
+// 64) leave two thirds of the multiprocessors idle and that side is long, the
+// sum may be cut in parts (Tiles::choose_splits): 8 Muon steps of 7 x 13053,
+// with 8 tiles of 204 K blocks for each S, took 345 us whole and take 171 in
+// parts; 6 matrices of 3823 x 271, with 90 tiles, 226 whole and 262 in parts.
+inline int square_splits(int64_t k, int64_t l, int64_t batch)
+{
+    const int64_t tiles = (k + 127) / 128 * ((k + 63) / 64) * batch, blocks = (l + kBK - 1) / kBK;
+    return tiles <= kSplitSms / 3 && blocks >= 32 ? (int)(blocks / 4) : 1;
+}
+
 // The workspace of one call.
 struct SchulzPlan {
     int64_t ldx, ldk, k;
     float *x32, *partial, *inv, *trace;
     int64_t groups;     // of 32 rows of S
+    int splits;         // parts of S's sum over the longer side, at most
+    int *splits_used;
+    float *parts;
     unsigned *arrived;  // of each team
     uint16_t *x16[2], *s, *p;
     int64_t bytes;
@@ -131,6 +145,10 @@ inline SchulzPlan schulz_plan(int64_t batch, int64_t m, int64_t n, void *base)
     q.x32 = c.take<float>(batch * m * q.ldx);
     q.x16[0] = c.take<uint16_t>(batch * m * q.ldx);
     q.x16[1] = c.take<uint16_t>(batch * m * q.ldx);
+    q.splits = square_splits(q.k, m < n ? n : m, batch);
+    q.splits_used = c.take<int>(1);
+    if (q.splits > 1)
+        q.parts = c.take<float>(parts_floats(q.ldk, q.splits, batch * q.k));
     q.s = c.take<uint16_t>(batch * q.k * q.ldk);
     q.p = c.take<uint16_t>(batch * q.k * q.ldk);
     q.bytes = c.used();
@@ -167,7 +185,12 @@ inline int64_t product_clocks(const SchulzArgs &a, int sms)
     up.K = (int)k;
     up.batch = (int)a.batch;
     up.epi_bytes = kStepBytes;
-    const int64_t t = best_form(square_shape(k, l, a.batch, sms, false), sms, 64).cost +
+    const Shape sum = square_shape(k, l, a.batch, sms, false);
+    const Form f = best_form(sum, sms, 64);
+    int64_t gram = f.cost;
+    if (square_splits(k, l, a.batch) > 1)  // spread over the grid, and joined
+        gram = f.tiles * f.ctas * ((l + kBK - 1) / kBK) * block_clocks(f.ctas, f.columns) / sms + 2 * kLaunchClocks;
+    const int64_t t = gram +
                       best_form(square_shape(k, k, a.batch, sms, true), sms, 64).cost + best_form(up, sms, 64).cost;
     return a.steps * (t + 3 * kLaunchClocks);
 }

@@ -375,7 +375,7 @@ __device__ __forceinline__ uint32_t two(float lo, float hi)
 // 32, or units of two chunks: warp `part` of the kParts that share a row takes
 // chunks (or units) part, part + kParts, ... below `chunks` (`units`).
 struct Slot {
-    int z, split, row, col, M, N;
+    int z, split, splits, row, col, M, N;
     int part, chunks;
     __device__ __forceinline__ int units() const { return (chunks + 1) / 2; }
     uint32_t tmem;
@@ -723,6 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Slot x;
             x.z = w.z;
             x.split = w.split;
+            x.splits = tiles.splits;
             x.row = w.row + (int)rank * kTM + quarter * 32 + lane;
             x.col = w.col;
             x.M = tiles.M;
@@ -987,6 +988,41 @@ __device__ __forceinline__ void put4_f32(float *p, const float (&v)[4], int n)
             if (i < n)
                 p[i] = v[i];
     }
+}
+
+// Partial sums of split products, fp32.
+struct PartEpi {
+    static constexpr int kLeastTN = 64;
+    static constexpr bool kAhead = false;
+    struct Params {
+        float *out;  // [batch][splits][M][ld], M as the device's counts leave it, ld a multiple of 8
+        int64_t ld;
+    };
+    using Pre = NoPre;
+    static __device__ __forceinline__ void carry(const Pre &, Pre &) {}
+    static __device__ __forceinline__ void fetch(const Params &, const Slot &, int, Pre &) {}
+    template <class G>
+    static __device__ __forceinline__ void chunk(const Params &p, const Slot &x, int c, Pre &, G staged)
+    {
+        float mine[32];
+        const int rows = x.M - x.group_row(0);
+        const bool in = x.group_col(c) < x.N;
+        float *to = p.out + (((int64_t)x.z * x.splits + x.split) * x.M + x.group_row(0)) * p.ld + x.group_col(c);
+        x.across<false>(c, mine, [&](int i, float(&v)[4]) {
+            if (i * 4 < rows && in)
+                *reinterpret_cast<float4 *>(to + i * 4 * p.ld) = make_float4(v[0], v[1], v[2], v[3]);
+        }, staged);
+    }
+    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre) { finish_tile<PartEpi>(p, x, pre); }
+};
+
+// fp32 numbers that the parts of split sums take: choose_splits makes four
+// waves of tiles at most, each of 128 x 256 per multiprocessor and a row's
+// padding, and never more than all parts whole.
+inline int64_t parts_floats(int64_t ld, int64_t splits, int64_t rows)
+{
+    const int64_t waves = 4 * kSplitSms * int64_t(kTM) * (256 + 8), whole = splits * rows * ld;
+    return waves < whole ? waves : whole;
 }
 
 }  // namespace

@@ -58,6 +58,16 @@ def test_newton_schulz(cuda_lib, batch, m, n, dtype):
     assert ops_wait_timeouts() == 0
 
 
+@pytest.mark.parametrize("batch,m,n", [(2, 7, 4099), (1, 300, 6001), (3, 5000, 20), (1, 2100, 256), (8, 3, 2500)])
+def test_long_sums(cuda_lib, batch, m, n):
+    """Few tiles and a long side: S is summed in parts."""
+    g = _gauss((batch, m, n), m + n)
+    out = newton_schulz(g)
+    for i in range(batch):
+        _check(out[i], g[i])
+    assert torch.equal(newton_schulz(g), out)
+
+
 def test_nearly_low_rank(cuda_lib):
     g = _gauss((512, 16), 1, 1.0) @ _gauss((16, 768), 2, 1.0) + 0.01 * _gauss((512, 768), 3, 1.0)
     _check(newton_schulz(g), g)
