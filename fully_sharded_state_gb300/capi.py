@@ -143,7 +143,7 @@ def _declare_ops(L) -> None:
         "fsdp_layer_norm_backward_workspace": [i64, i64, _i64p],
         "fsdp_linear_cross_entropy": [i64, i64, i64, _vp, i64, _vp, i64, _vp, i64, i32, f64, _vp, _vp, _vp, i64, _vp,
                                       i64, i64, _vp, i64, _vp],
-        "fsdp_linear_cross_entropy_workspace": [i64, i64, i64, i32, i64, _i64p],
+        "fsdp_linear_cross_entropy_workspace": [i64, i64, i64, i32, i32, i64, _i64p],
         "fsdp_newton_schulz": [i64, i64, i64, _vp, i64, i64, i32, _vp, i64, i64, i32, f64, f64, f64, f64, _vp, i64,
                                _vp],
         "fsdp_newton_schulz_workspace": [i64, i64, i64, _i64p],

@@ -3,7 +3,8 @@
 //
 //   prep      keeps the rows that count, one after the other (zeros past
 //             them), so ignored rows cost no products and what they hold
-//             reaches nothing; their own outputs are written here
+//             reaches nothing; their own outputs are written here. A weight
+//             whose rows do not start on 16 bytes is copied to rows that do
 //   logits    z = hidden weight^T on the tensor cores; the epilogue turns each
 //             128-column piece of a row into its maximum, its sum of
 //             exp(z - maximum) and, for the gradients, those exponentials in
@@ -50,6 +51,11 @@ struct PrepParams {
     int *meta;        // [0] rows kept, [1] rows that count, [2] a counter, zeroed, [3] parts of dhidden's sum
     float *row_loss;
     uint16_t *dhidden;
+    // the weight's copy with aligned rows, by the blocks from `packers` on
+    int packers;
+    const uint16_t *weight;
+    uint16_t *w;
+    int64_t ldw;
 };
 
 __device__ __forceinline__ bool kept(int64_t t, const PrepParams &p)
@@ -94,6 +100,12 @@ __global__ void __launch_bounds__(256) prep_kernel(const PrepParams p)
     launch_wait();
     launch_next();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    if ((int)blockIdx.x >= p.packers) {
+        const int64_t step = (int64_t)(gridDim.x - p.packers) * 8;
+        for (int64_t r = (int64_t)(blockIdx.x - p.packers) * 8 + warp; r < p.vocab; r += step)
+            copy_row(p.w + r * p.ldx, p.weight + r * p.ldw, p.cols, lane);
+        return;
+    }
     const int64_t lo = (int64_t)blockIdx.x * p.chunk;
     const int64_t hi = lo + p.chunk < p.rows ? lo + p.chunk : p.rows;
     if (threadIdx.x < 2)
@@ -160,17 +172,6 @@ __global__ void __launch_bounds__(256) prep_kernel(const PrepParams p)
     }
 }
 
-// [rows, cols] with any stride or alignment -> stride ldd, for the tensor maps.
-__global__ void __launch_bounds__(256) pack_rows_kernel(const uint16_t *src, int64_t lds, uint16_t *dst, int64_t ldd,
-                                                        int64_t rows, int cols)
-{
-    launch_wait();
-    launch_next();
-    const int lane = threadIdx.x % 32;
-    for (int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; r < rows; r += (int64_t)gridDim.x * 8)
-        copy_row(dst + r * ldd, src + r * lds, cols, lane);
-}
-
 // ---------------------------------------------------------------- logits ----
 
 // Each thread has a row of the tile and 128 adjacent columns, which it reads
@@ -179,8 +180,7 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(const uint16_t *src, int
 struct LogitsEpi {
     static constexpr int kLeastTN = kTileN;
     struct Params {
-        uint16_t *e;      // NULL: loss alone
-        int64_t lde;
+        bool e;           // whether the exponentials are kept, in the output's map
         float2 *stats;    // [rows][pieces]
         int pieces;
         const int *target;
@@ -193,17 +193,18 @@ struct LogitsEpi {
     {
         pre.target = x.row < x.M ? p.target[x.row] : -1;
     }
-    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre)
+    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre, const CUtensorMap *map)
     {
         // the columns past the vocabulary are compared only where there are some
         const int col = x.col + x.part * kPieceCols;
         if (x.N - col >= kPieceCols)
-            piece<true>(p, x, col, pre.target - col);
+            piece<true>(p, x, col, pre.target - col, map);
         else if (col < x.N)
-            piece<false>(p, x, col, pre.target - col);
+            piece<false>(p, x, col, pre.target - col, map);
     }
     template <bool kWhole>
-    static __device__ __forceinline__ void piece(const Params &p, const Slot &x, int col, int t)
+    static __device__ __forceinline__ void piece(const Params &p, const Slot &x, int col, int t,
+                                                 const CUtensorMap *map)
     {
         constexpr int kChunks = kPieceCols / 32;
         const bool live = x.row < x.M;
@@ -236,16 +237,11 @@ struct LogitsEpi {
             }
         };
         if (p.e) {
-            const int rows = x.M - x.group_row(0);
-            uint16_t *to = p.e + x.group_row(0) * p.lde;
 #pragma unroll
-            for (int u = 0; u < kChunks / 2; u++) {
-                const int unit = chunk0 / 2 + u, to_col = x.unit_col(unit);
-                x.emit16<false>(unit, [&](int h, float(&v)[32]) { exponentials(u * 2 + h, v); }, [&](int i, const uint4 &e) {
-                    if (i * 4 < rows && to_col < p.lde)
-                        *reinterpret_cast<uint4 *>(to + i * 4 * p.lde + to_col) = e;
-                });
-            }
+            for (int u = 0; u < kChunks / 2; u++)
+                if (x.col + (chunk0 / 2 + u) * 64 < x.N)
+                    x.emit_map<false>(map, chunk0 / 2 + u,
+                                      [&](int h, float(&v)[32]) { exponentials(u * 2 + h, v); });
         } else {
 #pragma unroll
             for (int c = 0; c < kChunks; c++) {
@@ -433,7 +429,7 @@ struct HiddenEpi {
             pre.row[i] = x.group_row(i) < x.M ? p.source[x.group_row(i)] : -1;
         pre.scale = p.scale.get();
     }
-    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre)
+    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre, const CUtensorMap *)
     {
         if (rows_of_16(p.out, p.ld)) {
 #pragma unroll 1
@@ -510,6 +506,7 @@ struct WeightEpi {
         float *sum;  // NULL: one piece
         int64_t lds; // a multiple of 8
         int first, last;
+        bool mapped;  // out has its tensor map
         Scale scale;
     };
     struct Pre {
@@ -557,26 +554,19 @@ struct WeightEpi {
             }, staged);
         }
     }
-    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre)
+    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre, const CUtensorMap *map)
     {
         if (p.sum) {
             finish_tile<WeightEpi>(p, x, pre);
-        } else if (rows_of_16(p.out, p.ld)) {
-            const int rows = x.M - x.group_row(0);
-#pragma unroll 1
-            for (int u = x.part; u < x.units(); u += kParts) {
-                uint16_t *to = p.out + x.group_row(0) * p.ld + x.unit_col(u);
-                const int left = x.N - x.unit_col(u);
-                auto scaled = [&](int, float(&v)[32]) {
+        } else if (p.mapped) {
+            auto scaled = [&](int, float(&v)[32]) {
 #pragma unroll
-                    for (int i = 0; i < 32; i++)
-                        v[i] *= pre.scale;
-                };
-                x.emit16<true>(u, scaled, [&](int i, const uint4 &e) {
-                    if (i * 4 < rows)
-                        put8_16(to + i * 4 * p.ld, e, left);
-                });
-            }
+                for (int i = 0; i < 32; i++)
+                    v[i] *= pre.scale;
+            };
+#pragma unroll 1
+            for (int u = x.part; u < x.units(); u += kParts)
+                x.emit_map<true>(map, u, scaled);
         } else {
             // a lane per column: every 32-byte sector is written in one go
             const int n = x.M - (x.row - x.lane);
@@ -604,8 +594,6 @@ struct Plan {
     float *parts, *dw;
     int64_t bytes;
 };
-
-bool map_ok(const void *p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0; }
 
 
 Plan plan_of(const LossArgs &a, bool grad, void *base, bool with_weight)
@@ -653,14 +641,17 @@ Plan plan_of(const LossArgs &a, bool grad, void *base, bool with_weight)
 
 }  // namespace
 
-int64_t loss_workspace(const LossArgs &a, bool grad) { return plan_of(a, grad, nullptr, true).bytes; }
+int64_t loss_workspace(const LossArgs &a, bool grad, bool aligned_weight)
+{
+    return plan_of(a, grad, nullptr, !aligned_weight).bytes;
+}
 
 fsdp_status launch_linear_cross_entropy(const LossArgs &a, void *workspace, int dev, void *stream)
 {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool grad = a.dweight != nullptr;
     const int sms = device_sms(dev);
-    const bool direct = map_ok(a.weight, a.ldw);
+    const bool direct = loss_weight_aligned(a.weight, a.ldw);
     const Plan q = plan_of(a, grad, workspace, !direct);
     fsdp_status st;
     if (a.rows == 0) {
@@ -689,21 +680,21 @@ fsdp_status launch_linear_cross_entropy(const LossArgs &a, void *workspace, int 
     pp.dhidden = static_cast<uint16_t *>(a.dhidden);
     int64_t chunk = (a.rows + 4 * sms - 1) / (4 * sms);
     pp.chunk = (int)(chunk < 8 ? 8 : chunk);
-    const unsigned prep_grid = (unsigned)((a.rows + pp.chunk - 1) / pp.chunk);
-    if ((st = launch("linear_cross_entropy (rows kept)", prep_kernel, prep_grid, 256, 0, s, 1, pp)) != FSDP_OK)
-        return st;
-
+    unsigned prep_grid = (unsigned)((a.rows + pp.chunk - 1) / pp.chunk);
+    pp.packers = (int)prep_grid;
     const uint16_t *w = static_cast<const uint16_t *>(a.weight);
     int64_t ldw = a.ldw;
     if (!direct) {
         const int64_t blocks = (a.vocab + 7) / 8;
-        if ((st = launch("linear_cross_entropy (weight)", pack_rows_kernel,
-                         (unsigned)(blocks < 8 * sms ? blocks : 8 * sms), 256, 0, s, 1, w, ldw, q.w, q.ldx, a.vocab,
-                         a.cols)) != FSDP_OK)
-            return st;
+        prep_grid += (unsigned)(blocks < 8 * sms ? blocks : 8 * sms);
+        pp.weight = w;
+        pp.w = q.w;
+        pp.ldw = ldw;
         w = q.w;
         ldw = q.ldx;
     }
+    if ((st = launch("linear_cross_entropy (rows kept)", prep_kernel, prep_grid, 256, 0, s, 1, pp)) != FSDP_OK)
+        return st;
 
     for (int64_t piece = 0; piece < q.pieces; piece++) {
         const int64_t row0 = piece * q.piece;
@@ -719,9 +710,10 @@ fsdp_status launch_linear_cross_entropy(const LossArgs &a, void *workspace, int 
         sh.dyn_base = (int)row0;
         const Operand ox{x, a.cols, ceil_to(rows, 64), q.ldx, 0};
         const Operand ow{w, a.cols, a.vocab, ldw, 0};
-        const LogitsEpi::Params le{q.e, q.lde, q.stats, q.stat_pieces, q.target + row0, q.tlogit + row0};
-        if ((st = product<false, false, LogitsEpi>(sh, ox, ow, true, le, dev, s,
-                                                              "linear_cross_entropy (logits)")) != FSDP_OK)
+        const Operand oe{q.e, q.lde, ceil_to(rows, 64), q.lde, 0};
+        const LogitsEpi::Params le{grad, q.stats, q.stat_pieces, q.target + row0, q.tlogit + row0};
+        if ((st = product<false, false, LogitsEpi>(sh, ox, ow, true, le, dev, s, "linear_cross_entropy (logits)",
+                                                   grad ? &oe : nullptr)) != FSDP_OK)
             return st;
 
         RowsParams rp{};
@@ -796,10 +788,12 @@ fsdp_status launch_linear_cross_entropy(const LossArgs &a, void *workspace, int 
         sw.dyn = q.meta;
         sw.dyn_base = (int)row0;
         sw.dyn_is_k = 1;
+        const bool mapped = !q.dw && (reinterpret_cast<uintptr_t>(a.dweight) & 15u) == 0 && a.lddw % 8 == 0;
+        const Operand odw{a.dweight, a.cols, a.vocab, a.lddw, 0};
         const WeightEpi::Params we{static_cast<uint16_t *>(a.dweight), a.lddw, q.dw, q.ldp, piece == 0,
-                                   piece + 1 == q.pieces, scale};
-        if ((st = product<true, true, WeightEpi>(sw, ogt, oxt, true, we, dev, s,
-                                                            "linear_cross_entropy (dweight)")) != FSDP_OK)
+                                   piece + 1 == q.pieces, mapped, scale};
+        if ((st = product<true, true, WeightEpi>(sw, ogt, oxt, true, we, dev, s, "linear_cross_entropy (dweight)",
+                                                 mapped ? &odw : nullptr)) != FSDP_OK)
             return st;
     }
     return FSDP_OK;

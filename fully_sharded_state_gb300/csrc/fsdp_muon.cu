@@ -191,14 +191,14 @@ struct SquareEpi {
             if (i * 4 < rows && in)
                 pre.s[kPoly ? i : 0] = *reinterpret_cast<const uint4 *>(from + i * 4 * p.ld);
     }
-    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre)
+    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre, const CUtensorMap *map)
     {
         uint16_t *out = p.out + x.z * p.stride;
-        const int rows = x.M - x.group_row(0);
 #pragma unroll 1
         for (int u = x.part; u < x.units(); u += kParts) {
             uint4 own[kPoly ? 8 : 1];  // the thread's own row of the unit
             if (kPoly) {
+                x.stage_free();
 #pragma unroll
                 for (int i = 0; i < 8; i++)
                     *x.group(i) = pre.s[kPoly ? i : 0];
@@ -210,8 +210,6 @@ struct SquareEpi {
                 if (u + kParts < x.units())
                     fetch(p, x, u + kParts, pre);
             }
-            uint16_t *to = out + x.group_row(0) * p.ld + x.unit_col(u);
-            const bool in = x.unit_col(u) < x.N;
             auto finish = [&](int h, float(&v)[32]) {
                 if (kPoly) {
 #pragma unroll
@@ -250,10 +248,7 @@ struct SquareEpi {
                         *reinterpret_cast<uint32_t *>(across + j * p.ld) = pair;
                 }
             };
-            x.emit16<false>(u, finish, [&](int i, const uint4 &e) {
-                if (i * 4 < rows && in)
-                    *reinterpret_cast<uint4 *>(to + i * 4 * p.ld) = e;
-            });
+            x.emit_map<false>(map, u, finish);
         }
     }
 };
@@ -385,7 +380,10 @@ struct StepEpi {
             }
         }, read_master);
     }
-    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre) { finish_tile<StepEpi>(p, x, pre); }
+    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre, const CUtensorMap *)
+    {
+        finish_tile<StepEpi>(p, x, pre);
+    }
 };
 
 // steps = 0: the scaled input is the result.
@@ -535,14 +533,14 @@ fsdp_status launch_newton_schulz(const SchulzArgs &a, void *workspace, int dev, 
                 st = launch("newton_schulz (S, sum)", join_square_kernel, dim3((unsigned)q.groups, batch), 256, 0, s, 1,
                             q.parts, q.splits_used, q.k, q.ldk, q.s, ks, q.trace, q.groups);
         } else {
-            st = wide ? product<false, false, SquareEpi<false>>(sq, x, x, false, e1, dev, s, "newton_schulz (S)")
-                      : product<true, true, SquareEpi<false>>(sq, x, x, false, e1, dev, s, "newton_schulz (S)");
+            st = wide ? product<false, false, SquareEpi<false>>(sq, x, x, false, e1, dev, s, "newton_schulz (S)", &gram)
+                      : product<true, true, SquareEpi<false>>(sq, x, x, false, e1, dev, s, "newton_schulz (S)", &gram);
         }
         if (st != FSDP_OK)
             return st;
         sq = square_shape(q.k, q.k, batch, sms, true);
-        if ((st = product<false, false, SquareEpi<true>>(sq, gram, gram, false, e2, dev, s, "newton_schulz (P)")) !=
-            FSDP_OK)
+        if ((st = product<false, false, SquareEpi<true>>(sq, gram, gram, false, e2, dev, s, "newton_schulz (P)",
+                                                         &poly)) != FSDP_OK)
             return st;
         Shape up{};
         up.M = m;

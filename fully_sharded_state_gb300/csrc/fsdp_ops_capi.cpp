@@ -315,7 +315,7 @@ fsdp_status fsdp_layer_norm_backward(int64_t rows, int64_t cols, const void *dy,
 }
 
 fsdp_status fsdp_linear_cross_entropy_workspace(int64_t rows, int64_t cols, int64_t vocab, int with_gradients,
-                                                int64_t piece_rows, int64_t *bytes)
+                                                int aligned_weight, int64_t piece_rows, int64_t *bytes)
 {
     const char *fn = "fsdp_linear_cross_entropy_workspace";
     if (bytes == nullptr)
@@ -325,7 +325,7 @@ fsdp_status fsdp_linear_cross_entropy_workspace(int64_t rows, int64_t cols, int6
         return st;
     LossArgs a{};
     a.rows = rows, a.cols = cols, a.vocab = vocab, a.piece_rows = piece_rows;
-    *bytes = loss_workspace(a, with_gradients != 0);
+    *bytes = loss_workspace(a, with_gradients != 0, aligned_weight != 0);
     return FSDP_OK;
 }
 
@@ -362,7 +362,7 @@ fsdp_status fsdp_linear_cross_entropy(int64_t rows, int64_t cols, int64_t vocab,
             b.matrix("dhidden", dhidden, rows, cols, lddh, 2, true);
             b.matrix("dweight", dweight, vocab, cols, lddw, 2, true);
         }
-        b.workspace(workspace, workspace_bytes, loss_workspace(a, grad));
+        b.workspace(workspace, workspace_bytes, loss_workspace(a, grad, loss_weight_aligned(weight, ldw)));
         if ((st = b.done()) != FSDP_OK)
             return st;
         return launch_linear_cross_entropy(a, workspace, b.device(), stream);

@@ -75,8 +75,13 @@ struct LossArgs {
     int64_t lddw;
     int64_t piece_rows;
 };
-// Lays the workspace out (base may be NULL) and returns its size.
-int64_t loss_workspace(const LossArgs &a, bool grad);
+// Whether the weight's rows can be copied as they lie; else a copy of it that
+// can be is part of the workspace.
+inline bool loss_weight_aligned(const void *weight, int64_t ldw)
+{
+    return (reinterpret_cast<uintptr_t>(weight) & 15u) == 0 && ldw % 8 == 0;
+}
+int64_t loss_workspace(const LossArgs &a, bool grad, bool aligned_weight);  // bytes
 fsdp_status launch_linear_cross_entropy(const LossArgs &a, void *workspace, int dev, void *stream);
 
 constexpr int kMuonMaxMats = FSDP_MUON_MAX_MATRICES;

@@ -112,6 +112,19 @@ __device__ __forceinline__ void tma_load(void *dst, const CUtensorMap *map, int 
     }
 }
 
+// A box of 64 x 32 16-bit elements from shared memory to a tensor map, as one
+// of this thread's bulk stores; and waits until those have read their source,
+// or are done.
+__device__ __forceinline__ void tma_store(const CUtensorMap *map, const void *src, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
+                 "r"(y), "r"(z), "r"(saddr(src))
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void store_read_wait() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 template <int kCtas>
 __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
 {
@@ -241,6 +254,7 @@ struct Shape {
                       // sums): at most so many, chosen by Tiles on the device
     int *splits_out;  // where the number is left, or NULL
     int tn;           // columns of a tile, a multiple of 16, at most TN
+    int whole_units;  // tiles' columns are multiples of 64
     int epi_bytes;    // what the epilogue moves per element, for the choice of the tile
     int sym;          // only the squares on and above the diagonal (M = N)
     int square;       // tiles' columns start on multiples of 32, as their rows do
@@ -510,6 +524,39 @@ struct Slot {
         __syncwarp();
     }
 
+    // The stage is free of the bulk store before.
+    __device__ __forceinline__ void stage_free() const
+    {
+        if (lane == 0)
+            store_read_wait();
+        __syncwarp();
+    }
+    // A unit as 16-bit numbers to its place in the output's tensor map, whose
+    // swizzle is the stage's: no thread reads it back or stores it. Rows and
+    // columns past the map are dropped; a tile's columns are whole units.
+    template <bool kBf16, class Op>
+    __device__ __forceinline__ void emit_map(const CUtensorMap *map, int unit, Op op) const
+    {
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            float v[32];
+            load_sum(unit * 2 + h, v);
+            op(h, v);
+            if (h == 0)
+                stage_free();
+#pragma unroll
+            for (int g = 0; g < 4; g++)
+                *piece(lane, h * 4 + g) = make_uint4(
+                    two<kBf16>(v[8 * g], v[8 * g + 1]), two<kBf16>(v[8 * g + 2], v[8 * g + 3]),
+                    two<kBf16>(v[8 * g + 4], v[8 * g + 5]), two<kBf16>(v[8 * g + 6], v[8 * g + 7]));
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0 && row < M)
+            tma_store(map, stage, col + unit * 64, row, z);
+        __syncwarp();
+    }
+
     // The reverse: f(i, v) makes this lane's 8 groups, `mine` becomes the
     // thread's own row of them.
     template <class F>
@@ -588,7 +635,7 @@ struct Ring {
 template <int kCtas, int TN, bool kAMN, bool kBMN, class Epi>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                   const __grid_constant__ Shape s, const __grid_constant__ typename Epi::Params ep)
+                   const __grid_constant__ CUtensorMap map_out, const __grid_constant__ Shape s, const __grid_constant__ typename Epi::Params ep)
 {
     using R = Ring<kCtas, TN>;
     extern __shared__ unsigned char raw[];
@@ -742,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok)
                 break;
             fence_after();
-            Epi::run(ep, x, pre);
+            Epi::run(ep, x, pre, &map_out);
             fence_before();
             __syncwarp();
             if (lane == 0)
@@ -752,6 +799,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 acc_phase ^= 1;
             }
         }
+        if (lane == 0)
+            store_wait();
     }
     if (!ok && lane == 0)
         atomicAdd(&g_wait_timeouts, 1ull);
@@ -817,7 +866,7 @@ inline fsdp_status make_map(CUtensorMap *map, const Operand &o, int batch, int b
 
 template <int kCtas, int TN, bool kAMN, bool kBMN, class Epi>
 fsdp_status product_as(Shape s, const Operand &a, const Operand &b, bool bf16, const typename Epi::Params &ep,
-                       int64_t tiles, int dev, cudaStream_t stream, const char *what)
+                       const Operand *out, int64_t tiles, int dev, cudaStream_t stream, const char *what)
 {
     using R = Ring<kCtas, TN>;
     auto kernel = product_kernel<kCtas, TN, kAMN, kBMN, Epi>;
@@ -830,10 +879,12 @@ fsdp_status product_as(Shape s, const Operand &a, const Operand &b, bool bf16, c
             return set_error(FSDP_ECUDA, "%s: cudaFuncSetAttribute: %s", what, cudaGetErrorString(e));
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    CUtensorMap ma, mb;
+    CUtensorMap ma, mb, mo{};
     fsdp_status st = make_map(&ma, a, s.batch, kAMN ? kBK : kTM, bf16);
     if (st == FSDP_OK)
         st = make_map(&mb, b, s.batch, kBMN ? kBK : s.tn / kCtas, bf16);
+    if (st == FSDP_OK && out)
+        st = make_map(&mo, *out, s.batch, 32, bf16);
     if (st != FSDP_OK)
         return st;
     s.idesc = instruction(kTM * kCtas, s.tn, bf16, kAMN, kBMN);
@@ -841,7 +892,7 @@ fsdp_status product_as(Shape s, const Operand &a, const Operand &b, bool bf16, c
     const int64_t most = (s.splits > 1 && sms > kSplitSms ? kSplitSms : sms) / kCtas;
     const int64_t grid = s.splits > 1 || tiles > most ? most : tiles;
     return launch(what, kernel, dim3((unsigned)(grid * kCtas)), kThreads, R::kSmem, stream,
-                  kCtas, ma, mb, s, ep);
+                  kCtas, ma, mb, mo, s, ep);
 }
 
 // Output tiles of rows x cols, over the batch and the parts of K.
@@ -881,7 +932,7 @@ inline Form best_form(const Shape &s, int64_t sms, int least_tn)
         if (f[1] < least_tn)
             continue;
         const int64_t across = (s.N + f[1] - 1) / f[1];
-        const int columns = s.square || least_tn == 256 ? f[1] : (int)ceil_to((s.N + across - 1) / across, 16);
+        const int columns = s.square || least_tn == 256 ? f[1] : (int)ceil_to((s.N + across - 1) / across, s.whole_units ? 64 : 16);
         Form g{f[0], f[1], columns, count_tiles(s, kTM * f[0], f[1]), 0};
         const int64_t slots = sms / g.ctas < 1 ? 1 : sms / g.ctas, waves = (g.tiles + slots - 1) / slots;
         const int64_t mma = nk * block_clocks(g.ctas, columns), epi = 1000 + kTM * columns * s.epi_bytes / 35;
@@ -895,12 +946,14 @@ inline Form best_form(const Shape &s, int64_t sms, int least_tn)
 }
 
 // Launches D = A B^T. `s` needs M, N, K, batch, epi_bytes, sym, dyn* and, for
-// split sums, splits; the rest is filled in here.
+// split sums, splits; the rest is filled in here. `out`: the output, where the
+// epilogue stores through its tensor map (16-bit, of the operands' type).
 template <bool kAMN, bool kBMN, class Epi>
 fsdp_status product(Shape s, const Operand &a, const Operand &b, bool bf16, const typename Epi::Params &ep,
-                    int dev, cudaStream_t stream, const char *what)
+                    int dev, cudaStream_t stream, const char *what, const Operand *out = nullptr)
 {
     s.group = s.group > 0 ? s.group : 8;
+    s.whole_units = out != nullptr;
     const Form best = best_form(s, device_sms(dev), Epi::kLeastTN);
     s.tn = best.columns;
     if (best.tiles < 1)
@@ -908,13 +961,13 @@ fsdp_status product(Shape s, const Operand &a, const Operand &b, bool bf16, cons
     if (best.tiles >= (int64_t)1 << 31)
         return set_error(FSDP_ERANGE, "%s: %lld tiles", what, (long long)best.tiles);
     if (best.ctas == 2)
-        return product_as<2, 256, kAMN, kBMN, Epi>(s, a, b, bf16, ep, best.tiles, dev, stream, what);
+        return product_as<2, 256, kAMN, kBMN, Epi>(s, a, b, bf16, ep, out, best.tiles, dev, stream, what);
     if (best.tn == 256)
-        return product_as<1, 256, kAMN, kBMN, Epi>(s, a, b, bf16, ep, best.tiles, dev, stream, what);
+        return product_as<1, 256, kAMN, kBMN, Epi>(s, a, b, bf16, ep, out, best.tiles, dev, stream, what);
     if constexpr (Epi::kLeastTN <= 64) {
         if (best.tn == 128)
-            return product_as<1, 128, kAMN, kBMN, Epi>(s, a, b, bf16, ep, best.tiles, dev, stream, what);
-        return product_as<1, 64, kAMN, kBMN, Epi>(s, a, b, bf16, ep, best.tiles, dev, stream, what);
+            return product_as<1, 128, kAMN, kBMN, Epi>(s, a, b, bf16, ep, out, best.tiles, dev, stream, what);
+        return product_as<1, 64, kAMN, kBMN, Epi>(s, a, b, bf16, ep, out, best.tiles, dev, stream, what);
     }
     return FSDP_OK;
 }
@@ -1013,7 +1066,10 @@ struct PartEpi {
                 *reinterpret_cast<float4 *>(to + i * 4 * p.ld) = make_float4(v[0], v[1], v[2], v[3]);
         }, staged);
     }
-    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre) { finish_tile<PartEpi>(p, x, pre); }
+    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre, const CUtensorMap *)
+    {
+        finish_tile<PartEpi>(p, x, pre);
+    }
 };
 
 // fp32 numbers that the parts of split sums take: choose_splits makes four

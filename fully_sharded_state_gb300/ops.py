@@ -197,7 +197,8 @@ def _loss_call(hidden, weight, targets, ignore_index, reduction, grad, grad_scal
                 dweight = torch.empty((vocab, cols), dtype=torch.bfloat16, device=dev)
         else:
             lddh = lddw = cols
-        ws, nws = _workspace("fsdp_linear_cross_entropy_workspace", rows, cols, vocab, int(grad), piece_rows,
+        aligned = int(weight.data_ptr() % 16 == 0 and ldw % 8 == 0)
+        ws, nws = _workspace("fsdp_linear_cross_entropy_workspace", rows, cols, vocab, int(grad), aligned, piece_rows,
                              device=dev)
     capi._check(lib.fsdp_linear_cross_entropy(
         rows, cols, vocab, hidden.data_ptr(), ldh, weight.data_ptr(), ldw, pt, int(ignore_index),

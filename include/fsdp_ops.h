@@ -94,9 +94,11 @@ fsdp_status fsdp_linear_cross_entropy(int64_t rows, int64_t cols, int64_t vocab,
                                       float *row_loss, void *dhidden, int64_t lddh, void *dweight,
                                       int64_t lddw, int64_t piece_rows, void *workspace,
                                       int64_t workspace_bytes, void *stream);
+/* aligned_weight: weight starts on 16 bytes and ldw is a multiple of 8; else
+ * the workspace holds a copy of it that does. */
 fsdp_status fsdp_linear_cross_entropy_workspace(int64_t rows, int64_t cols, int64_t vocab,
-                                                int with_gradients, int64_t piece_rows,
-                                                int64_t *bytes);
+                                                int with_gradients, int aligned_weight,
+                                                int64_t piece_rows, int64_t *bytes);
 
 /* Newton-Schulz iteration on `batch` matrices g [m, n] (batch stride in
  * elements), each on its own:

@@ -127,8 +127,8 @@ def test_workspace_queries(lib):
     n = ctypes.c_int64(-1)
     q = ctypes.byref(n)
     for fn, sizes in ((lib.fsdp_layer_norm_backward_workspace, (1000, 513)),
-                      (lib.fsdp_linear_cross_entropy_workspace, (1000, 513, 5001, 1, 0)),
-                      (lib.fsdp_linear_cross_entropy_workspace, (0, 8, 5, 0, 0)),
+                      (lib.fsdp_linear_cross_entropy_workspace, (1000, 513, 5001, 1, 0, 0)),
+                      (lib.fsdp_linear_cross_entropy_workspace, (0, 8, 5, 0, 1, 0)),
                       (lib.fsdp_newton_schulz_workspace, (3, 100, 7)), (lib.fsdp_muon_workspace, (3, 100, 7))):
         assert fn(*sizes, q) == OK and n.value > 0 and n.value % 256 == 0 or fn is lib.fsdp_layer_norm_backward_workspace
         assert fn(*sizes, None) == EINVAL
@@ -136,9 +136,9 @@ def test_workspace_queries(lib):
     # pieces of the rows bound the exponentials' share: 2 GiB by default
     big, small = [], []
     for rows in (16384, 65536, 262144):
-        assert lib.fsdp_linear_cross_entropy_workspace(rows, 64, 128000, 1, 0, q) == OK
+        assert lib.fsdp_linear_cross_entropy_workspace(rows, 64, 128000, 1, 1, 0, q) == OK
         big.append(n.value)
-        assert lib.fsdp_linear_cross_entropy_workspace(rows, 64, 128000, 1, 1024, q) == OK
+        assert lib.fsdp_linear_cross_entropy_workspace(rows, 64, 128000, 1, 1, 1024, q) == OK
         small.append(n.value)
     assert big[2] < 2 * (1 << 31) and small[2] < 1 << 30 and big == sorted(big)
 
