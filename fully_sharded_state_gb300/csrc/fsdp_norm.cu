@@ -217,7 +217,8 @@ constexpr int forward_block()
 // 16 chunks a thread needs no barrier, but its unrolled code missed the
 // instruction cache: 16384 x 4096 bf16 took 132 us.)
 template <typename T, bool kFull, int TPR, int NV>
-__global__ void __launch_bounds__(forward_block<TPR>(), NV <= 4 ? 1024 / forward_block<TPR>() : 1)
+__global__ void __launch_bounds__(forward_block<TPR>(),
+                                  NV > 4 ? 1 : 1024 / forward_block<TPR>())
     norm_forward_kernel(const ForwardParams p)
 {
     constexpr int kRowsPerBlock = forward_block<TPR>() / TPR, kWarps = TPR / 32, V = Chunk<T>::V;
