@@ -174,46 +174,85 @@ __global__ void __launch_bounds__(256) prep_kernel(const PrepParams p)
 
 // ---------------------------------------------------------------- logits ----
 
-// Each thread has a row of the tile and 128 adjacent columns, which it reads
-// from tensor memory twice: for the maximum, then for the exponentials. The
-// exponentials leave by the warp's stage, 64 columns of 32 rows at a time.
-struct LogitsEpi {
-    static constexpr int kLeastTN = kTileN;
-    struct Params {
-        bool e;           // whether the exponentials are kept, in the output's map
-        float2 *stats;    // [rows][pieces]
-        int pieces;
-        const int *target;
-        float *tlogit;
-    };
+// Each thread has a row of the tile and 128 adjacent columns, for the maximum
+// and then the exponentials. Those leave by the warp's stage, 64 columns of 32
+// rows at a time.
+//
+// kLong: the sums over K are joined in registers from parts of 512, which
+// keeps the row losses 7e-8 off (relative) however wide the rows are; one sum
+// in tensor memory, read twice, leaves them 7e-8 off at 512 columns, 6e-7 at
+// 4096 and 2e-6 at 12288. It costs 1001 x 513 x 50021 8 us of 209, where an
+// epilogue's time shows, and nothing at 8192 x 4096 x 65536: taken above 1024
+// columns.
+constexpr int kLongCols = 1024;
+struct LogitsParams {
+    bool e;           // whether the exponentials are kept, in the output's map
+    float2 *stats;    // [rows][pieces]
+    int pieces;
+    const int *target;
+    float *tlogit;
+};
+template <bool kLong>
+struct LogitsEpi : EpiDefaults {
+    static constexpr int kLeastTN = kTileN, kPromote = kLong ? 8 : 0;
+    static constexpr int kChunks = kPieceCols / 32;
+    using Params = LogitsParams;
     struct Pre {
         int target;
+        float sum[kLong ? kChunks : 1][32];
     };
-    static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int, Pre &pre)
+    static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int, Pre &pre, const EpiMaps &)
     {
         pre.target = x.row < x.M ? p.target[x.row] : -1;
+        if constexpr (kLong) {
+#pragma unroll
+            for (int c = 0; c < kChunks; c++)
+#pragma unroll
+                for (int i = 0; i < 32; i++)
+                    pre.sum[c][i] = 0.0f;
+        }
     }
-    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre, const CUtensorMap *map)
+    static __device__ __forceinline__ void get(const Slot &x, const Pre &pre, int c, float (&v)[32])
+    {
+        if constexpr (kLong) {
+#pragma unroll
+            for (int i = 0; i < 32; i++)
+                v[i] = pre.sum[c][i];
+        } else {
+            x.load(x.part * kChunks + c, v);
+        }
+    }
+    static __device__ __forceinline__ void add(const Slot &x, Pre &pre)
+    {
+#pragma unroll
+        for (int c = 0; c < kChunks; c++) {
+            float v[32];
+            x.load(x.part * kChunks + c, v);
+#pragma unroll
+            for (int i = 0; i < 32; i++)
+                pre.sum[c][i] += v[i];
+        }
+    }
+    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre, const EpiMaps &maps)
     {
         // the columns past the vocabulary are compared only where there are some
         const int col = x.col + x.part * kPieceCols;
         if (x.N - col >= kPieceCols)
-            piece<true>(p, x, col, pre.target - col, map);
+            piece<true>(p, x, col, pre, maps.m);
         else if (col < x.N)
-            piece<false>(p, x, col, pre.target - col, map);
+            piece<false>(p, x, col, pre, maps.m);
     }
     template <bool kWhole>
-    static __device__ __forceinline__ void piece(const Params &p, const Slot &x, int col, int t,
+    static __device__ __forceinline__ void piece(const Params &p, const Slot &x, int col, const Pre &pre,
                                                  const CUtensorMap *map)
     {
-        constexpr int kChunks = kPieceCols / 32;
         const bool live = x.row < x.M;
-        const int n = x.N - col, chunk0 = x.part * kChunks;
+        const int n = x.N - col, chunk0 = x.part * kChunks, t = pre.target - col;
         float top = -CUDART_INF_F, at = 0.0f;
 #pragma unroll
         for (int c = 0; c < kChunks; c++) {
             float v[32];
-            x.load(chunk0 + c, v);
+            get(x, pre, c, v);
             if (live && t >= c * 32 && t < c * 32 + 32) {
 #pragma unroll
                 for (int i = 0; i < 32; i++)
@@ -228,11 +267,11 @@ struct LogitsEpi {
         const float ref = top == -CUDART_INF_F ? 0.0f : top;
         const float shift = ref * kLog2e;
         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        auto exponentials = [&](int c0, float(&v)[32]) {
-            const int c = c0 * 32;
+        auto exponentials = [&](int c, float(&v)[32]) {
+            get(x, pre, c, v);
 #pragma unroll
             for (int i = 0; i < 32; i++) {
-                v[i] = kWhole || c + i < n ? exp2_fast(fmaf(v[i], kLog2e, -shift)) : 0.0f;
+                v[i] = kWhole || c * 32 + i < n ? exp2_fast(fmaf(v[i], kLog2e, -shift)) : 0.0f;
                 sum[i % 4] += v[i];
             }
         };
@@ -246,7 +285,6 @@ struct LogitsEpi {
 #pragma unroll
             for (int c = 0; c < kChunks; c++) {
                 float v[32];
-                x.load(chunk0 + c, v);
                 exponentials(c, v);
             }
         }
@@ -410,8 +448,7 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowsParams p)
 // ------------------------------------------------------------- gradients ----
 
 // dhidden rows back at their own places, bf16.
-struct HiddenEpi {
-    static constexpr int kLeastTN = 64;
+struct HiddenEpi : EpiDefaults {
     struct Params {
         uint16_t *out;
         int64_t ld;
@@ -422,14 +459,14 @@ struct HiddenEpi {
         int row[8];
         float scale;
     };
-    static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int, Pre &pre)
+    static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int, Pre &pre, const EpiMaps &)
     {
 #pragma unroll
         for (int i = 0; i < 8; i++)
             pre.row[i] = x.group_row(i) < x.M ? p.source[x.group_row(i)] : -1;
         pre.scale = p.scale.get();
     }
-    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre, const CUtensorMap *)
+    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre, const EpiMaps &)
     {
         if (rows_of_16(p.out, p.ld)) {
 #pragma unroll 1
@@ -497,9 +534,7 @@ __global__ void __launch_bounds__(256) join_hidden_kernel(const float *parts, in
 }
 
 // dweight, over the pieces of the rows in fp32 where there are several.
-struct WeightEpi {
-    static constexpr int kLeastTN = 64;
-    static constexpr bool kAhead = false;
+struct WeightEpi : EpiDefaults {
     struct Params {
         uint16_t *out;
         int64_t ld;
@@ -513,12 +548,9 @@ struct WeightEpi {
         float4 o[8];
         float scale;
     };
-    static __device__ __forceinline__ void carry(const Pre &from, Pre &to) { to.scale = from.scale; }
-    static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int chunk, Pre &pre)
+    static __device__ __forceinline__ void read_sum(const Params &p, const Slot &x, int chunk, Pre &pre)
     {
-        if (chunk == x.part)
-            pre.scale = p.scale.get();
-        if (!p.sum || p.first)
+        if (!p.sum || p.first || chunk >= x.chunks)
             return;
         const int rows = x.M - x.group_row(0);
         const float *from = p.sum + x.group_row(0) * p.lds + x.group_col(chunk);
@@ -527,46 +559,47 @@ struct WeightEpi {
             if (i * 4 < rows && x.group_col(chunk) < x.N)
                 pre.o[i] = *reinterpret_cast<const float4 *>(from + i * 4 * p.lds);
     }
-    template <class G>
-    static __device__ __forceinline__ void chunk(const Params &p, const Slot &x, int c, Pre &pre, G staged)
+    static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int chunk, Pre &pre, const EpiMaps &)
     {
-        const int col = x.group_col(c), left = x.N - col, rows = x.M - x.group_row(0);
-        uint16_t *to = p.out + x.group_row(0) * p.ld + col;
-        float mine[32];
-        if (p.sum) {
-            float *sum = p.sum + x.group_row(0) * p.lds + col;
-            x.across<false>(c, mine, [&](int i, float(&v)[4]) {
-                if (i * 4 >= rows || left <= 0)
-                    return;
-                if (!p.first) {
-                    v[0] += pre.o[i].x;
-                    v[1] += pre.o[i].y;
-                    v[2] += pre.o[i].z;
-                    v[3] += pre.o[i].w;
-                }
-                if (p.last) {
-#pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        v[k] *= pre.scale;
-                    put4_16<true>(to + i * 4 * p.ld, v, left);
-                } else
-                    *reinterpret_cast<float4 *>(sum + i * 4 * p.lds) = make_float4(v[0], v[1], v[2], v[3]);
-            }, staged);
-        }
+        pre.scale = p.scale.get();
+        read_sum(p, x, chunk, pre);
     }
-    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre, const CUtensorMap *map)
+    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre, const EpiMaps &maps)
     {
         if (p.sum) {
-            finish_tile<WeightEpi>(p, x, pre);
-        } else if (p.mapped) {
-            auto scaled = [&](int, float(&v)[32]) {
+#pragma unroll 1
+            for (int c = x.part; c < x.chunks; c += kParts) {
+                const int col = x.group_col(c), left = x.N - col, rows = x.M - x.group_row(0);
+                uint16_t *to = p.out + x.group_row(0) * p.ld + col;
+                float *sum = p.sum + x.group_row(0) * p.lds + col;
+                x.across(c, [&](int i, float(&v)[4]) {
+                    if (i * 4 >= rows || left <= 0)
+                        return;
+                    if (!p.first) {
+                        v[0] += pre.o[i].x;
+                        v[1] += pre.o[i].y;
+                        v[2] += pre.o[i].z;
+                        v[3] += pre.o[i].w;
+                    }
+                    if (p.last) {
 #pragma unroll
-                for (int i = 0; i < 32; i++)
-                    v[i] *= pre.scale;
-            };
+                        for (int k = 0; k < 4; k++)
+                            v[k] *= pre.scale;
+                        put4_16<true>(to + i * 4 * p.ld, v, left);
+                    } else
+                        *reinterpret_cast<float4 *>(sum + i * 4 * p.lds) = make_float4(v[0], v[1], v[2], v[3]);
+                });
+                read_sum(p, x, c + kParts, pre);
+            }
+        } else if (p.mapped) {
 #pragma unroll 1
             for (int u = x.part; u < x.units(); u += kParts)
-                x.emit_map<true>(map, u, scaled);
+                x.emit_map<true>(maps.m, u, [&](int h, float(&v)[32]) {
+                    x.load_sum(u * 2 + h, v);
+#pragma unroll
+                    for (int i = 0; i < 32; i++)
+                        v[i] *= pre.scale;
+                });
         } else {
             // a lane per column: every 32-byte sector is written in one go
             const int n = x.M - (x.row - x.lane);
@@ -711,9 +744,12 @@ fsdp_status launch_linear_cross_entropy(const LossArgs &a, void *workspace, int 
         const Operand ox{x, a.cols, ceil_to(rows, 64), q.ldx, 0};
         const Operand ow{w, a.cols, a.vocab, ldw, 0};
         const Operand oe{q.e, q.lde, ceil_to(rows, 64), q.lde, 0};
-        const LogitsEpi::Params le{grad, q.stats, q.stat_pieces, q.target + row0, q.tlogit + row0};
-        if ((st = product<false, false, LogitsEpi>(sh, ox, ow, true, le, dev, s, "linear_cross_entropy (logits)",
-                                                   grad ? &oe : nullptr)) != FSDP_OK)
+        const LogitsParams le{grad, q.stats, q.stat_pieces, q.target + row0, q.tlogit + row0};
+        const char *what = "linear_cross_entropy (logits)";
+        const Operand *out = grad ? &oe : nullptr;
+        st = a.cols > kLongCols ? product<false, false, LogitsEpi<true>>(sh, ox, ow, true, le, dev, s, what, out)
+                                : product<false, false, LogitsEpi<false>>(sh, ox, ow, true, le, dev, s, what, out);
+        if (st != FSDP_OK)
             return st;
 
         RowsParams rp{};

@@ -3,8 +3,7 @@
 //
 //   start    one pass over the input: the norm's partial sums; for the Muon
 //            step also the fold of the R ranks' gradients and the momentum
-//   scale    x = u / (||u||_F + eps) in fp16, for the products; the fp32 u
-//            is scaled where it is read next, in the first step's epilogue
+//   scale    x = u / (||u||_F + eps), as hi + lo (below)
 //   steps x  S = x x^T (or x^T x: the smaller side), P = b S + c S^2 - d I and
 //            x = (a + d) x + P x, three products on the tensor cores. S and P are
 //            symmetric: only the squares on and above the diagonal are
@@ -12,11 +11,18 @@
 //   the last product's epilogue writes the result, or updates the master
 //
 // Numbers: the operands are fp16 (all are at most about 5 in size; 2^-11
-// each), sums are fp32, and x itself is carried in fp32, so that the linear
-// term is never rounded: with x kept in fp16 alone, a 512 x 512 gradient of
+// each), sums are fp32, and x itself is carried to 22 bits, so that the linear
+// term is hardly rounded: with x kept in fp16 alone, a 512 x 512 gradient of
 // rank 16 under 1 % noise comes out 4e-2 off (its small directions grow by a
 // per step, and the rounding with them). P is shifted along its diagonal
 // (shift_of): 4e-4 to 7e-4 off for that gradient, 8e-4 for a Gaussian one.
+//
+// x is kept as two fp16 matrices, hi = fp16(x), which is the products' operand
+// as well, and lo = fp16(2048 (x - hi)). Beside fp32 it saves a fifth of the
+// last product's traffic, and both move by bulk copies through the warps'
+// stages, so that no thread loads or stores them: that epilogue was bound by
+// shared memory and L1, which the MMAs' operands use as well (48 x 512 x 512:
+// 365 us with the fp32 x, 324 so; a Muon step of 14336 x 4096 3,032 and 3,001).
 #include "fsdp_muon.cuh"
 
 namespace fsdp {
@@ -28,7 +34,7 @@ struct StartParams {
     int m, n, groups;       // groups of 8 columns per row
     int64_t ldx;            // stride of x
     int vec;                // every row of every input starts on 16 bytes
-    float *x32;             // [batch][m][ldx]: u
+    float *x32;             // [batch][m][ldx]: the Muon step's u
     float *partial;         // [batch][kMaxParts]
     // newton_schulz
     const void *g;
@@ -119,7 +125,8 @@ __global__ void __launch_bounds__(kStartThreads) start_kernel(const __grid_const
         } else {
             load8(p.g, z * p.g_stride + r * p.ldg + c, left, p.bf16, u);
         }
-        store8(x + r * p.ldx + c, 8, u);
+        if (kMuon)
+            store8(x + r * p.ldx + c, 8, u);
 #pragma unroll
         for (int k = 0; k < 8; k++)
             sq += u[k] * u[k];
@@ -129,9 +136,32 @@ __global__ void __launch_bounds__(kStartThreads) start_kernel(const __grid_const
         p.partial[z * kMaxParts + blockIdx.x] = sq;
 }
 
-// x16 = u / (||u||_F + eps); inv[z]: that factor.
-__global__ void __launch_bounds__(kStartThreads) scale_kernel(const float *x32, uint16_t *x16, const float *partial,
-                                                              int parts, float eps, int64_t count, float *inv_out)
+// Where u is: fp32 or bf16 rows.
+struct Source {
+    const void *p;
+    int64_t ld, stride;
+    int bf16;
+};
+
+// Two values as hi + lo / 2048, each pair in one word.
+constexpr float kLoScale = 2048.0f;
+__device__ __forceinline__ uint32_t high(float a, float b) { return pack_f16(a, b); }
+__device__ __forceinline__ uint32_t low(uint32_t hi, float a, float b)
+{
+    const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    return pack_f16((a - h.x) * kLoScale, (b - h.y) * kLoScale);
+}
+__device__ __forceinline__ float2 both(uint32_t hi, uint32_t lo)
+{
+    const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    const float2 l = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+    return make_float2(fmaf(l.x, 1.0f / kLoScale, h.x), fmaf(l.y, 1.0f / kLoScale, h.y));
+}
+
+// x = u / (||u||_F + eps); inv[z]: that factor.
+__global__ void __launch_bounds__(kStartThreads) scale_kernel(const Source u, uint16_t *hi, uint16_t *lo,
+                                                              const float *partial, int parts, float eps, int m, int n,
+                                                              int groups, float *inv_out)
 {
     __shared__ float sh[kStartThreads / 32];
     launch_wait();
@@ -144,18 +174,23 @@ __global__ void __launch_bounds__(kStartThreads) scale_kernel(const float *x32, 
     const float inv = 1.0f / (sqrtf(sq) + eps);
     if (blockIdx.x == 0 && threadIdx.x == 0)
         inv_out[z] = inv;
-    const float *src = x32 + z * count;
-    uint16_t *dst = x16 + z * count;
-    const int64_t step = (int64_t)gridDim.x * kStartThreads * 8;
-    for (int64_t i = ((int64_t)blockIdx.x * kStartThreads + threadIdx.x) * 8; i < count; i += step) {
+    const int64_t total = (int64_t)m * groups;
+    hi += z * total * 8;
+    lo += z * total * 8;
+    for (int64_t i = (int64_t)blockIdx.x * kStartThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kStartThreads) {
+        const int r = (int)((uint64_t)i < 0x80000000u ? (uint32_t)i / (uint32_t)groups : i / groups);
+        const int c = (int)(i - (int64_t)r * groups) * 8;
         float v[8];
-        load8(src, i, 8, false, v);
-        uint4 u;
-        uint32_t *w = reinterpret_cast<uint32_t *>(&u);
+        load8(u.p, z * u.stride + r * u.ld + c, n - c, u.bf16, v);
+        uint4 h, l;
+        uint32_t *hw = reinterpret_cast<uint32_t *>(&h), *lw = reinterpret_cast<uint32_t *>(&l);
 #pragma unroll
-        for (int k = 0; k < 4; k++)
-            w[k] = pack_f16(v[2 * k] * inv, v[2 * k + 1] * inv);
-        *reinterpret_cast<uint4 *>(dst + i) = u;
+        for (int k = 0; k < 4; k++) {
+            hw[k] = high(v[2 * k] * inv, v[2 * k + 1] * inv);
+            lw[k] = low(hw[k], v[2 * k] * inv, v[2 * k + 1] * inv);
+        }
+        *reinterpret_cast<uint4 *>(hi + i * 8) = h;
+        *reinterpret_cast<uint4 *>(lo + i * 8) = l;
     }
 }
 
@@ -163,8 +198,7 @@ __global__ void __launch_bounds__(kStartThreads) scale_kernel(const float *x32, 
 // multiplied. Strides are multiples of 16, so groups of 8 and pairs of rows
 // stay inside a padded row.
 template <bool kPoly>
-struct SquareEpi {
-    static constexpr int kLeastTN = 64;
+struct SquareEpi : EpiDefaults {
     struct Params {
         uint16_t *out;
         const uint16_t *from;  // S
@@ -191,7 +225,11 @@ struct SquareEpi {
             if (i * 4 < rows && in)
                 pre.s[kPoly ? i : 0] = *reinterpret_cast<const uint4 *>(from + i * 4 * p.ld);
     }
-    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre, const CUtensorMap *map)
+    static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int unit, Pre &pre, const EpiMaps &)
+    {
+        fetch(p, x, unit, pre);
+    }
+    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre, const EpiMaps &maps)
     {
         uint16_t *out = p.out + x.z * p.stride;
 #pragma unroll 1
@@ -211,6 +249,7 @@ struct SquareEpi {
                     fetch(p, x, u + kParts, pre);
             }
             auto finish = [&](int h, float(&v)[32]) {
+                x.load_sum(u * 2 + h, v);
                 if (kPoly) {
 #pragma unroll
                     for (int j = 0; j < 16; j++) {
@@ -248,7 +287,7 @@ struct SquareEpi {
                         *reinterpret_cast<uint32_t *>(across + j * p.ld) = pair;
                 }
             };
-            x.emit_map<false>(map, u, finish);
+            x.emit_map<false>(maps.m, u, finish);
         }
     }
 };
@@ -293,20 +332,17 @@ __global__ void __launch_bounds__(256) join_square_kernel(const float *parts, co
     }
 }
 
-// x = (a + d) x + (P x), x the fp32 one. What becomes of it:
-//   kKeep    fp32 in place, and the next step's fp16 operand
+// x = (a + d) x + (P x). What becomes of it:
+//   kKeep    the next step's hi and lo
 //   kOut     the result, in bf16
 //   kMaster  w = w decay - lr x, and the bf16 parameter
+// Maps: hi, lo, and (kKeep) the next hi; lo is updated in place.
 enum class Then { kKeep, kOut, kMaster };
 
 struct StepParams {
-    float *x32;
-    const float *inv;  // the first step's factor of x32, per matrix; NULL: 1
-    int64_t ld, stride;
     float a, b, c;
     const float *trace;
     int groups, k;
-    uint16_t *x16;
     uint16_t *out;
     int64_t ldo, out_stride, n;
     float decay, lr;
@@ -315,82 +351,121 @@ struct StepParams {
 };
 
 template <Then kThen>
-struct StepEpi {
-    static constexpr int kLeastTN = 64;
-    static constexpr bool kAhead = kThen != Then::kMaster;  // registers: it has twice the reads
+struct StepEpi : EpiDefaults {
+    static constexpr int kStages = 2;
     using Params = StepParams;
-    static constexpr bool kMaster = kThen == Then::kMaster;
-    struct Pre;
-    static __device__ __forceinline__ void carry(const Pre &from, Pre &to) { to.a = from.a; }
     struct Pre {
         float a;
-        float4 x[8];
     };
-    static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int chunk, Pre &pre)
+    static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int unit, Pre &pre, const EpiMaps &maps)
     {
-        const int rows = x.M - x.group_row(0), left = x.N - x.group_col(chunk);
-        if (chunk == x.part) {
-            pre.a = p.a + shift_of(p.trace + x.z * p.groups, p.k, p.b, p.c, x.lane);
-            if (p.inv)
-                pre.a *= p.inv[x.z];
-        }
-        const float *from = p.x32 + x.z * p.stride + x.group_row(0) * p.ld + x.group_col(chunk);
-#pragma unroll
-        for (int i = 0; i < 8; i++)
-            if (i * 4 < rows && left > 0)
-                pre.x[i] = *reinterpret_cast<const float4 *>(from + i * 4 * p.ld);
+        pre.a = p.a + shift_of(p.trace + x.z * p.groups, p.k, p.b, p.c, x.lane);
+        if (unit < x.units())
+            x.load_units(&maps.m[0], &maps.m[1], unit);
     }
-    template <class G>
-    static __device__ __forceinline__ void chunk(const Params &p, const Slot &x, int c, Pre &pre, G staged)
+    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre, const EpiMaps &maps)
     {
-        const int rows = x.M - x.group_row(0), col = x.group_col(c), left = x.N - col;
-        const int64_t at = x.z * p.stride + x.group_row(0) * p.ld + col;
-        const int64_t to = x.group_row(0) * (kThen == Then::kOut ? p.ldo : p.n) + col;
-        float mine[32];
-        // the master's elements are read once the accumulator's registers are free
-        float w[kMaster ? 8 : 1][4];
-        auto read_master = [&] {
-            staged();
-            if (kMaster) {
+        const int rows = x.M - x.group_row(0);
+#pragma unroll 1
+        for (int u = x.part; u < x.units(); u += kParts) {
+            if (u > x.part)
+                x.load_units(&maps.m[0], &maps.m[1], u);
+            if (!x.units_loaded())
+                return;
+            // The thread's own row of the unit. Where the first stage is
+            // needed for what leaves, hi is taken out of it before.
+            uint4 hi[8];
+            if (kThen != Then::kKeep) {
 #pragma unroll
                 for (int i = 0; i < 8; i++)
-                    if (i * 4 < rows && left > 0)
-                        get4_f32(p.master[x.z] + to + i * 4 * p.n, w[kMaster ? i : 0], left);
+                    hi[i] = *x.piece(x.lane, i, 0);
+                __syncwarp();
             }
-        };
-        x.across<false>(c, mine, [&](int i, float(&v)[4]) {
-            if (i * 4 >= rows || left <= 0)
-                return;
-            v[0] = fmaf(pre.a, pre.x[i].x, v[0]);
-            v[1] = fmaf(pre.a, pre.x[i].y, v[1]);
-            v[2] = fmaf(pre.a, pre.x[i].z, v[2]);
-            v[3] = fmaf(pre.a, pre.x[i].w, v[3]);
+            auto finish = [&](int h, float(&v)[32]) {
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const uint4 a = kThen != Then::kKeep ? hi[h * 4 + i] : *x.piece(x.lane, h * 4 + i, 0);
+                    const uint4 b = *x.piece(x.lane, h * 4 + i, 1);
+                    const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        const float2 old = both(aw[k], bw[k]);
+                        v[8 * i + 2 * k] = fmaf(pre.a, old.x, v[8 * i + 2 * k]);
+                        v[8 * i + 2 * k + 1] = fmaf(pre.a, old.y, v[8 * i + 2 * k + 1]);
+                    }
+                }
+            };
             if (kThen == Then::kKeep) {
-                *reinterpret_cast<float4 *>(p.x32 + at + i * 4 * p.ld) = make_float4(v[0], v[1], v[2], v[3]);
-                *reinterpret_cast<uint2 *>(p.x16 + at + i * 4 * p.ld) = four_16<false>(v);
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    float v[32];
+                    x.load(u * 2 + h, v);
+                    finish(h, v);
+#pragma unroll
+                    for (int g = 0; g < 4; g++) {
+                        uint32_t a[4], b[4];
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            a[i] = high(v[8 * g + 2 * i], v[8 * g + 2 * i + 1]);
+                            b[i] = low(a[i], v[8 * g + 2 * i], v[8 * g + 2 * i + 1]);
+                        }
+                        *x.piece(x.lane, h * 4 + g, 0) = make_uint4(a[0], a[1], a[2], a[3]);
+                        *x.piece(x.lane, h * 4 + g, 1) = make_uint4(b[0], b[1], b[2], b[3]);
+                    }
+                }
+                x.store_units(&maps.m[2], &maps.m[1], u);
             } else if (kThen == Then::kOut) {
-                put4_16<true>(p.out + x.z * p.out_stride + to + i * 4 * p.ldo, v, left);
+                const int left = x.N - x.unit_col(u);
+                uint16_t *to = p.out + x.z * p.out_stride + x.group_row(0) * p.ldo + x.unit_col(u);
+                const bool whole = rows_of_16(p.out, p.ldo | p.out_stride);
+                x.emit16<true>(u, finish, [&](int i, const uint4 &e) {
+                    if (i * 4 >= rows)
+                        return;
+                    if (whole) {
+                        put8_16(to + i * 4 * p.ldo, e, left);
+                    } else {
+                        const uint16_t *q = reinterpret_cast<const uint16_t *>(&e);
+#pragma unroll
+                        for (int k = 0; k < 8; k++)
+                            if (k < left)
+                                to[i * 4 * p.ldo + k] = q[k];
+                    }
+                });
             } else {
 #pragma unroll
-                for (int k = 0; k < 4; k++)
-                    v[k] = fmaf(-p.lr, v[k], w[kMaster ? i : 0][k] * p.decay);
-                put4_f32(p.master[x.z] + to + i * 4 * p.n, v, left);
-                if (p.param[x.z])
-                    put4_16<true>(p.param[x.z] + to + i * 4 * p.n, v, left);
+                for (int h = 0; h < 2; h++) {
+                    const int left = x.N - x.group_col(u * 2 + h);
+                    const int64_t to = x.group_row(0) * p.n + x.group_col(u * 2 + h);
+                    float mine[32], w[8][4];
+                    x.load(u * 2 + h, mine);
+                    finish(h, mine);
+                    auto read_master = [&] {
+#pragma unroll
+                        for (int i = 0; i < 8; i++)
+                            if (i * 4 < rows && left > 0)
+                                get4_f32(p.master[x.z] + to + i * 4 * p.n, w[i], left);
+                    };
+                    x.spread(mine, [&](int i, float(&v)[4]) {
+                        if (i * 4 >= rows || left <= 0)
+                            return;
+#pragma unroll
+                        for (int k = 0; k < 4; k++)
+                            v[k] = fmaf(-p.lr, v[k], w[i][k] * p.decay);
+                        put4_f32(p.master[x.z] + to + i * 4 * p.n, v, left);
+                        if (p.param[x.z])
+                            put4_16<true>(p.param[x.z] + to + i * 4 * p.n, v, left);
+                    }, read_master);
+                }
             }
-        }, read_master);
-    }
-    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre, const CUtensorMap *)
-    {
-        finish_tile<StepEpi>(p, x, pre);
+        }
     }
 };
 
 // steps = 0: the scaled input is the result.
 struct FinishParams {
-    const float *x32, *inv;
-    int m, n, groups;
-    int64_t ld;
+    Source u;
+    const float *inv;
+    int m, n;
     uint16_t *out;
     int64_t ldo, out_stride;
     float decay, lr;
@@ -403,11 +478,12 @@ __global__ void __launch_bounds__(kStartThreads) finish_kernel(const __grid_cons
     launch_wait();
     launch_next();
     const int z = blockIdx.y;
-    const float *x = p.x32 + (int64_t)z * p.m * p.ld;
     for (int64_t i = (int64_t)blockIdx.x * kStartThreads + threadIdx.x; i < (int64_t)p.m * p.n;
          i += (int64_t)gridDim.x * kStartThreads) {
         const int64_t r = i / p.n, c = i - r * p.n;
-        const float v = x[r * p.ld + c] * p.inv[z];
+        const int64_t at = z * p.u.stride + r * p.u.ld + c;
+        const float v = (p.u.bf16 ? bf16_at(static_cast<const uint16_t *>(p.u.p) + at)
+                                  : static_cast<const float *>(p.u.p)[at]) * p.inv[z];
         if (kMuon) {
             const float w = fmaf(-p.lr, v, p.master[z][i] * p.decay);
             p.master[z][i] = w;
@@ -421,7 +497,10 @@ __global__ void __launch_bounds__(kStartThreads) finish_kernel(const __grid_cons
 
 }  // namespace
 
-int64_t schulz_workspace(int64_t batch, int64_t m, int64_t n) { return schulz_plan(batch, m, n, nullptr).bytes; }
+int64_t schulz_workspace(int64_t batch, int64_t m, int64_t n, bool muon)
+{
+    return schulz_plan(batch, m, n, muon, nullptr).bytes;
+}
 
 fsdp_status launch_newton_schulz(const SchulzArgs &a, void *workspace, int dev, void *stream)
 {
@@ -431,7 +510,7 @@ fsdp_status launch_newton_schulz(const SchulzArgs &a, void *workspace, int dev, 
     const int64_t team = team_clocks(a, dev);
     if (team >= 0 && team < product_clocks(a, sms))
         return launch_team(a, workspace, dev, stream);
-    const SchulzPlan q = schulz_plan(a.batch, a.m, a.n, workspace);
+    const SchulzPlan q = schulz_plan(a.batch, a.m, a.n, muon, workspace);
     const int batch = (int)a.batch, m = (int)a.m, n = (int)a.n;
     fsdp_status st;
 
@@ -472,17 +551,18 @@ fsdp_status launch_newton_schulz(const SchulzArgs &a, void *workspace, int dev, 
     }
     if (st != FSDP_OK)
         return st;
-    if ((st = launch("newton_schulz (scale)", scale_kernel, grid, kStartThreads, 0, s, 1, q.x32, q.x16[0], q.partial,
-                     parts, a.eps, a.m * q.ldx, q.inv)) != FSDP_OK)
+    const Source u = muon ? Source{q.x32, q.ldx, a.m * q.ldx, 0}
+                          : Source{a.g, a.ldg, a.g_stride, a.dtype == FSDP_BF16};
+    if ((st = launch("newton_schulz (scale)", scale_kernel, grid, kStartThreads, 0, s, 1, u, q.x16[0], q.lo, q.partial,
+                     parts, a.eps, m, n, sp.groups, q.inv)) != FSDP_OK)
         return st;
 
     if (a.steps == 0) {
         FinishParams fp{};
-        fp.x32 = q.x32;
+        fp.u = u;
         fp.inv = q.inv;
         fp.m = m;
         fp.n = n;
-        fp.ld = q.ldx;
         fp.out = static_cast<uint16_t *>(a.out);
         fp.ldo = a.ldo;
         fp.out_stride = a.out_stride;
@@ -499,9 +579,6 @@ fsdp_status launch_newton_schulz(const SchulzArgs &a, void *workspace, int dev, 
     const bool wide = a.m <= a.n;
     const int64_t xs = a.m * q.ldx, ks = q.k * q.ldk;
     StepParams ep{};
-    ep.x32 = q.x32;
-    ep.ld = q.ldx;
-    ep.stride = xs;
     ep.a = a.a, ep.b = a.b, ep.c = a.c;
     ep.trace = q.trace;
     ep.groups = (int)q.groups;
@@ -548,13 +625,12 @@ fsdp_status launch_newton_schulz(const SchulzArgs &a, void *workspace, int dev, 
         up.K = (int)q.k;
         up.batch = batch;
         up.epi_bytes = kStepBytes;
-        ep.inv = step == 0 ? q.inv : nullptr;
-        ep.x16 = q.x16[(step + 1) % 2];
+        const Operand lo{q.lo, a.n, a.m, q.ldx, xs}, next{q.x16[(step + 1) % 2], a.n, a.m, q.ldx, xs};
         auto update = [&](auto epi) {
             using E = decltype(epi);
             // wide: P x, x with its columns adjacent; tall: x P, P symmetric
-            return wide ? product<false, true, E>(up, poly, x, false, ep, dev, s, "newton_schulz (x)")
-                        : product<false, false, E>(up, x, poly, false, ep, dev, s, "newton_schulz (x)");
+            return wide ? product<false, true, E>(up, poly, x, false, ep, dev, s, "newton_schulz (x)", &x, &lo, &next)
+                        : product<false, false, E>(up, x, poly, false, ep, dev, s, "newton_schulz (x)", &x, &lo, &next);
         };
         st = step + 1 < a.steps ? update(StepEpi<Then::kKeep>{})
              : muon             ? update(StepEpi<Then::kMaster>{})

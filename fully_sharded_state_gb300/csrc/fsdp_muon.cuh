@@ -126,11 +126,11 @@ struct SchulzPlan {
     int *splits_used;
     float *parts;
     unsigned *arrived;  // of each team
-    uint16_t *x16[2], *s, *p;
+    uint16_t *x16[2], *lo, *s, *p;
     int64_t bytes;
 };
 
-inline SchulzPlan schulz_plan(int64_t batch, int64_t m, int64_t n, void *base)
+inline SchulzPlan schulz_plan(int64_t batch, int64_t m, int64_t n, bool muon, void *base)
 {
     SchulzPlan q{};
     q.k = m < n ? m : n;
@@ -142,7 +142,9 @@ inline SchulzPlan schulz_plan(int64_t batch, int64_t m, int64_t n, void *base)
     q.groups = (q.k + 31) / 32;
     q.trace = c.take<float>(batch * q.groups);
     q.arrived = c.take<unsigned>(kMaxParts);
-    q.x32 = c.take<float>(batch * m * q.ldx);
+    if (muon)
+        q.x32 = c.take<float>(batch * m * q.ldx);
+    q.lo = c.take<uint16_t>(batch * m * q.ldx);
     q.x16[0] = c.take<uint16_t>(batch * m * q.ldx);
     q.x16[1] = c.take<uint16_t>(batch * m * q.ldx);
     q.splits = square_splits(q.k, m < n ? n : m, batch);
@@ -158,7 +160,7 @@ inline SchulzPlan schulz_plan(int64_t batch, int64_t m, int64_t n, void *base)
 // The product S (or P) of k x k matrices over K: one triangle and its mirror
 // image, or the whole square. The mirror image is scattered stores, 7 bytes'
 // time per element against 3 (S), 9 against 4 (P): it pays where K is long.
-constexpr int kStepBytes = 10;
+constexpr int kStepBytes = 5;
 inline Shape square_shape(int64_t k, int64_t K, int64_t batch, int sms, bool poly)
 {
     Shape whole{}, half{};

@@ -377,7 +377,7 @@ fsdp_status fsdp_newton_schulz_workspace(int64_t batch, int64_t m, int64_t n, in
     fsdp_status st = check_schulz(fn, batch, m, n);
     if (st != FSDP_OK)
         return st;
-    *bytes = schulz_workspace(batch, m, n);
+    *bytes = schulz_workspace(batch, m, n, false);
     return FSDP_OK;
 }
 
@@ -398,7 +398,7 @@ fsdp_status fsdp_newton_schulz(int64_t batch, int64_t m, int64_t n, const void *
         Buffers buf(fn);
         buf.matrix("g", g, m, n, ldg, esize(dtype), false, batch, batch_stride);
         buf.matrix("out", out, m, n, ldo, 2, true, batch, out_batch_stride);
-        buf.workspace(workspace, workspace_bytes, schulz_workspace(batch, m, n));
+        buf.workspace(workspace, workspace_bytes, schulz_workspace(batch, m, n, false));
         if ((st = buf.done()) != FSDP_OK)
             return st;
         SchulzArgs s{};
@@ -412,7 +412,14 @@ fsdp_status fsdp_newton_schulz(int64_t batch, int64_t m, int64_t n, const void *
 
 fsdp_status fsdp_muon_workspace(int n_mats, int64_t m, int64_t n, int64_t *bytes)
 {
-    return fsdp_newton_schulz_workspace(n_mats, m, n, bytes);
+    const char *fn = "fsdp_muon_workspace";
+    if (bytes == nullptr)
+        return set_error(FSDP_EINVAL, "%s: bytes is NULL", fn);
+    fsdp_status st = check_schulz(fn, n_mats, m, n);
+    if (st != FSDP_OK)
+        return st;
+    *bytes = schulz_workspace(n_mats, m, n, true);
+    return FSDP_OK;
 }
 
 fsdp_status fsdp_muon(int n_mats, int64_t m, int64_t n, int R, const void *const *grads, fsdp_dtype grad_dtype,
@@ -450,7 +457,7 @@ fsdp_status fsdp_muon(int n_mats, int64_t m, int64_t n, int R, const void *const
             if (param_out)
                 b.matrix("param_out", param_out[i], m, n, n, 2, true, 1, 0, i);
         }
-        b.workspace(workspace, workspace_bytes, schulz_workspace(n_mats, m, n));
+        b.workspace(workspace, workspace_bytes, schulz_workspace(n_mats, m, n, true));
         if ((st = b.done()) != FSDP_OK)
             return st;
         SchulzArgs s{};

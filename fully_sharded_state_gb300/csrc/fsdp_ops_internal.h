@@ -106,7 +106,7 @@ struct SchulzArgs {
     float mu, decay, lr;  // lr includes update_scale
     int nesterov;
 };
-int64_t schulz_workspace(int64_t batch, int64_t m, int64_t n);
+int64_t schulz_workspace(int64_t batch, int64_t m, int64_t n, bool muon);  // bytes
 fsdp_status launch_newton_schulz(const SchulzArgs &a, void *workspace, int dev, void *stream);
 
 }  // namespace fsdp

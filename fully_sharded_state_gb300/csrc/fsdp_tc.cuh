@@ -265,6 +265,12 @@ struct Shape {
     int dyn_is_k;
 };
 
+// Tensor maps of an epilogue's own inputs and outputs, boxes of 64 x 32.
+constexpr int kEpiMaps = 3;
+struct EpiMaps {
+    CUtensorMap m[kEpiMaps];
+};
+
 struct Work {
     int z, split;
     int row, col;     // first row and column of the (pair's) tile
@@ -393,8 +399,11 @@ struct Slot {
     int part, chunks;
     __device__ __forceinline__ int units() const { return (chunks + 1) / 2; }
     uint32_t tmem;
-    unsigned char *stage;  // the warp's 4 KB: 32 rows of 128 bytes
+    unsigned char *stage;  // the warp's 4 KB (or two of them): 32 rows of 128 bytes
     int lane;
+    uint64_t *bar;              // of the warp's own loads (LoadUnits)
+    mutable uint32_t bar_phase;
+    mutable bool failed;        // a wait on it was given up
     bool mirror;  // sym: also store the transposed element
     bool empty;   // K was empty (only a dynamic one can be): the accumulator
                   // holds nothing, the sum is 0
@@ -408,9 +417,9 @@ struct Slot {
     // 16-byte piece c (0..7) of line r (0..31) of the stage. Pieces of a line
     // are permuted by its number: eight lanes on one piece of eight lines, and
     // eight lanes on the pieces of one line, both touch every bank once.
-    __device__ __forceinline__ uint4 *piece(int r, int c) const
+    __device__ __forceinline__ uint4 *piece(int r, int c, int which = 0) const
     {
-        return reinterpret_cast<uint4 *>(stage + r * 128 + ((c ^ (r & 7)) << 4));
+        return reinterpret_cast<uint4 *>(stage + which * 4096 + r * 128 + ((c ^ (r & 7)) << 4));
     }
 
     // Group i (0..7) of this lane in a chunk: 4 adjacent columns of a row, the
@@ -466,10 +475,9 @@ struct Slot {
     }
 
     // Takes the threads' own rows of a chunk to the lanes by groups and calls
-    // f(i, v) for each of this lane's 8. What f leaves in v is back in `mine`
-    // after it, where kBack is set.
-    // `staged` is called when `mine` is in the stage and its registers are free.
-    template <bool kBack, class F, class G>
+    // f(i, v) for each of this lane's 8. `staged` is called when `mine` is in
+    // the stage and its registers are free.
+    template <class F, class G>
     __device__ __forceinline__ void spread(float (&mine)[32], F f, G staged) const
     {
         put_stage(mine);
@@ -479,24 +487,20 @@ struct Slot {
             const uint4 u = *group(i);
             float v[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
             f(i, v);
-            if (kBack)
-                *group(i) = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                                       __float_as_uint(v[3]));
         }
         __syncwarp();
-        if (kBack)
-            get_stage(mine);
     }
-    template <bool kBack, class F>
+    template <class F>
     __device__ __forceinline__ void spread(float (&mine)[32], F f) const
     {
-        spread<kBack>(mine, f, [] {});
+        spread(mine, f, [] {});
     }
-    template <bool kBack, class F, class G>
-    __device__ __forceinline__ void across(int chunk, float (&mine)[32], F f, G staged) const
+    template <class F>
+    __device__ __forceinline__ void across(int chunk, F f) const
     {
+        float mine[32];
         load_sum(chunk, mine);
-        spread<kBack>(mine, f, staged);
+        spread(mine, f);
     }
     // A unit as 16-bit numbers, for results that need nothing from memory by
     // groups: op(h, v) works on the thread's own row of chunk h (0, 1) of the
@@ -531,17 +535,49 @@ struct Slot {
             store_read_wait();
         __syncwarp();
     }
+    // A unit of each of two tensor maps into the warp's two stages (rows and
+    // columns past a map are zeros), and the wait for them.
+    __device__ __forceinline__ void load_units(const CUtensorMap *a, const CUtensorMap *b, int unit) const
+    {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        stage_free();
+        if (lane == 0) {
+            bar_expect(bar, 2 * 4096);
+            tma_load<1>(stage, a, col + unit * 64, row, z, bar);
+            tma_load<1>(stage + 4096, b, col + unit * 64, row, z, bar);
+        }
+        __syncwarp();
+    }
+    __device__ __forceinline__ bool units_loaded() const
+    {
+        if (!warp_wait(bar, bar_phase))
+            failed = true;
+        bar_phase ^= 1;
+        return !failed;
+    }
+    // And back out of them.
+    __device__ __forceinline__ void store_units(const CUtensorMap *a, const CUtensorMap *b, int unit) const
+    {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0 && row < M) {
+            tma_store(a, stage, col + unit * 64, row, z);
+            tma_store(b, stage + 4096, col + unit * 64, row, z);
+        }
+        __syncwarp();
+    }
+
     // A unit as 16-bit numbers to its place in the output's tensor map, whose
-    // swizzle is the stage's: no thread reads it back or stores it. Rows and
+    // swizzle is the stage's: no thread reads it back or stores it. get(h, v)
+    // makes the thread's own row of chunk h (0, 1) of the unit. Rows and
     // columns past the map are dropped; a tile's columns are whole units.
-    template <bool kBf16, class Op>
-    __device__ __forceinline__ void emit_map(const CUtensorMap *map, int unit, Op op) const
+    template <bool kBf16, class Get>
+    __device__ __forceinline__ void emit_map(const CUtensorMap *map, int unit, Get get) const
     {
 #pragma unroll
         for (int h = 0; h < 2; h++) {
             float v[32];
-            load_sum(unit * 2 + h, v);
-            op(h, v);
+            get(h, v);
             if (h == 0)
                 stage_free();
 #pragma unroll
@@ -576,56 +612,37 @@ struct Slot {
 
 // An epilogue E has
 //   Params, kLeastTN   its arguments; the narrowest tile it takes
-//   Pre                what it reads from memory for one chunk, in registers
-//   fetch(p, x, chunk, pre)   starts those reads
-//   chunk(p, x, chunk, pre, staged)   finishes a chunk with them; calls
-//                      staged() once the accumulator's registers are free
-//   carry(from, to)    copies what all chunks of a tile share
-// The first chunk's reads are started before the accumulator is waited for,
-// and with kAhead each chunk's while the one before it is finished: with reads and
-// stores in turn, their latency made up most of a short product.
-template <class E>
-__device__ __forceinline__ void finish_tile(const typename E::Params &p, const Slot &x, typename E::Pre &a)
-{
-    typename E::Pre b;
-    E::carry(a, b);
-#pragma unroll 1
-    for (int c = x.part; c < x.chunks; c += 2 * kParts) {
-        const int d = c + kParts, e = d + kParts;
-        if (E::kAhead) {
-            E::chunk(p, x, c, a, [&] {
-                if (d < x.chunks)
-                    E::fetch(p, x, d, b);
-            });
-            if (d < x.chunks)
-                E::chunk(p, x, d, b, [&] {
-                    if (e < x.chunks)
-                        E::fetch(p, x, e, a);
-                });
-        } else {
-            E::chunk(p, x, c, a, [] {});
-            if (d < x.chunks) {
-                E::fetch(p, x, d, a);
-                E::chunk(p, x, d, a, [] {});
-            }
-            if (e < x.chunks)
-                E::fetch(p, x, e, a);
-        }
-    }
-}
+//   kStages            4 KB stages of a warp
+//   Pre                what it reads from memory for a chunk or unit, in registers
+//   fetch(p, x, part, pre, maps)   starts the first such reads, before the
+//                      accumulator is waited for
+//   run(p, x, pre, maps)   finishes the tile
+//   kPromote           0, or: the sums over K are taken in parts of so many
+//                      blocks, each part by add(x, pre) to registers; run
+//                      finds them there
+// The tensor cores cut their sums off where fp32 would round them, always
+// toward zero, so that the error of a long sum grows with its length and does
+// not average out; a sum of parts in registers is as exact as a part's.
+struct EpiDefaults {
+    static constexpr int kLeastTN = 64, kStages = 1, kPromote = 0;
+};
+// Registers of a thread of warps 0 to 3 and of the epilogue, where the latter
+// holds sums: as many together as the launch has (kLaunchRegs of 65,536 / 384).
+constexpr int kLaunchRegs = 168, kFewRegs = 72, kManyRegs = 216;
+static_assert(kFewRegs * 4 + kManyRegs * kEpiWarps <= kLaunchRegs * (4 + kEpiWarps), "registers of a block");
 struct NoPre {
 };
 
-template <int kCtas, int TN>
+template <int kCtas, int TN, int kEpiStages = 1>
 struct Ring {
     static constexpr int kRowsB = TN / kCtas;
     static constexpr int kBytesA = kTM * kBK * 2;
     static constexpr int kBytesB = kRowsB * kBK * 2;
     static constexpr int kStageBytes = kBytesA + kBytesB;
-    static constexpr int kFit = 192 * 1024 / kStageBytes;
+    static constexpr int kFit = (kEpiStages == 1 ? 192 : 160) * 1024 / kStageBytes;
     static constexpr int kStages = kFit < 8 ? kFit : 8;
-    static constexpr int kBarriers = 2 * kStages + 4;
-    static constexpr int kEpiBytes = kEpiWarps * 4096;
+    static constexpr int kBarriers = 2 * kStages + 4 + kEpiWarps;
+    static constexpr int kEpiBytes = kEpiWarps * kEpiStages * 4096;
     // 1024 bytes for the swizzle's alignment, the epilogue's stages, the
     // barriers and the TMEM address
     static constexpr int kSmem = 1024 + kStages * kStageBytes + kEpiBytes + kBarriers * 8 + 16;
@@ -635,9 +652,9 @@ struct Ring {
 template <int kCtas, int TN, bool kAMN, bool kBMN, class Epi>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                   const __grid_constant__ CUtensorMap map_out, const __grid_constant__ Shape s, const __grid_constant__ typename Epi::Params ep)
+                   const __grid_constant__ EpiMaps maps, const __grid_constant__ Shape s, const __grid_constant__ typename Epi::Params ep)
 {
-    using R = Ring<kCtas, TN>;
+    using R = Ring<kCtas, TN, Epi::kStages>;
     extern __shared__ unsigned char raw[];
     // the same offset in both CTAs of a pair: dynamic shared memory starts at
     // one address in every CTA
@@ -647,7 +664,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *empty = full + R::kStages;
     uint64_t *acc_full = empty + R::kStages;
     uint64_t *acc_empty = acc_full + 2;
-    uint32_t *tmem_at = reinterpret_cast<uint32_t *>(acc_empty + 2);
+    uint64_t *epi_bar = acc_empty + 2;
+    uint32_t *tmem_at = reinterpret_cast<uint32_t *>(epi_bar + kEpiWarps);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = kCtas == 2 ? cluster_rank() : 0;
@@ -667,6 +685,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar_init(acc_full + i, 1);
             bar_init(acc_empty + i, kEpiWarps * kCtas);
         }
+        for (int i = 0; i < kEpiWarps; i++)
+            bar_init(epi_bar + i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     fence_before();
@@ -684,67 +704,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int rows_b = s.tn / kCtas;  // of B in this CTA
     const uint32_t stage_bytes = R::kBytesA + (kBMN ? (rows_b + 63) / 64 * 8192 : rows_b * 128);
 
-    if (warp == 0) {
-        int stage = 0;
-        uint32_t phase = 0;
-        for (uint32_t t = first; ok && t < tiles.total; t += step) {
-            const Work w = tiles.at(s, t);
-            const int row = w.row + (int)rank * kTM, col = w.col + (int)rank * rows_b;
-            for (int kb = 0; kb < w.nkb; kb++) {
-                if (!(ok = warp_wait(empty + stage, phase ^ 1)))
-                    break;
-                if (elect_one()) {
-                    if (rank == 0)
-                        bar_expect(full + stage, stage_bytes * kCtas);
-                    unsigned char *a = ring + stage * R::kStageBytes, *b = a + R::kBytesA;
-                    const int k = (w.kb + kb) * kBK;
-                    if (kAMN) {
-#pragma unroll
-                        for (int i = 0; i < kTM / 64; i++)
-                            tma_load<kCtas>(a + i * 8192, &map_a, row + i * 64, k, w.z, full + stage);
-                    } else {
-                        tma_load<kCtas>(a, &map_a, k, row, w.z, full + stage);
-                    }
-                    if (kBMN) {
-#pragma unroll
-                        for (int i = 0; i < R::kRowsB / 64; i++)
-                            if (i * 64 < rows_b)
-                                tma_load<kCtas>(b + i * 8192, &map_b, col + i * 64, k, w.z, full + stage);
-                    } else {
-                        tma_load<kCtas>(b, &map_b, k, col, w.z, full + stage);
-                    }
-                }
-                __syncwarp();
-                if (++stage == R::kStages) {
-                    stage = 0;
-                    phase ^= 1;
-                }
-            }
-        }
-        if (!ok)
-            let_copies_land();
-    } else if (warp == 1) {
-        if (rank == 0) {
-            int stage = 0, acc = 0;
-            uint32_t phase = 0, acc_phase = 0;
+    if (warp < 4) {
+        if (Epi::kPromote > 0)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+        if (warp == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
             for (uint32_t t = first; ok && t < tiles.total; t += step) {
                 const Work w = tiles.at(s, t);
-                if (!(ok = warp_wait(acc_empty + acc, acc_phase ^ 1)))
-                    break;
-                fence_after();
-                const uint32_t d = tmem + acc * TN;
+                const int row = w.row + (int)rank * kTM, col = w.col + (int)rank * rows_b;
                 for (int kb = 0; kb < w.nkb; kb++) {
-                    if (!(ok = warp_wait(full + stage, phase)))
+                    if (!(ok = warp_wait(empty + stage, phase ^ 1)))
                         break;
-                    fence_after();
-                    const uint32_t a = saddr(ring + stage * R::kStageBytes);
-                    const uint64_t da = operand_desc(a, kAMN), db = operand_desc(a + R::kBytesA, kBMN);
                     if (elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < kBK / 16; k++)
-                            mma_f16<kCtas>(d, da + k * k_step(kAMN), db + k * k_step(kBMN), s.idesc,
-                                           kb > 0 || k > 0);
-                        mma_commit<kCtas>(empty + stage);
+                        if (rank == 0)
+                            bar_expect(full + stage, stage_bytes * kCtas);
+                        unsigned char *a = ring + stage * R::kStageBytes, *b = a + R::kBytesA;
+                        const int k = (w.kb + kb) * kBK;
+                        if (kAMN) {
+    #pragma unroll
+                            for (int i = 0; i < kTM / 64; i++)
+                                tma_load<kCtas>(a + i * 8192, &map_a, row + i * 64, k, w.z, full + stage);
+                        } else {
+                            tma_load<kCtas>(a, &map_a, k, row, w.z, full + stage);
+                        }
+                        if (kBMN) {
+    #pragma unroll
+                            for (int i = 0; i < R::kRowsB / 64; i++)
+                                if (i * 64 < rows_b)
+                                    tma_load<kCtas>(b + i * 8192, &map_b, col + i * 64, k, w.z, full + stage);
+                        } else {
+                            tma_load<kCtas>(b, &map_b, k, col, w.z, full + stage);
+                        }
                     }
                     __syncwarp();
                     if (++stage == R::kStages) {
@@ -752,18 +743,67 @@ __global__ void __launch_bounds__(kThreads, 1)
                         phase ^= 1;
                     }
                 }
-                if (elect_one())
-                    mma_commit<kCtas>(acc_full + acc);
-                __syncwarp();
-                if (++acc == 2) {
-                    acc = 0;
-                    acc_phase ^= 1;
+            }
+            if (!ok)
+                let_copies_land();
+        } else if (warp == 1) {
+            if (rank == 0) {
+                int stage = 0, acc = 0;
+                uint32_t phase = 0, acc_phase = 0;
+                for (uint32_t t = first; ok && t < tiles.total; t += step) {
+                    const Work w = tiles.at(s, t);
+                    if (!(ok = warp_wait(acc_empty + acc, acc_phase ^ 1)))
+                        break;
+                    fence_after();
+                    int part = 0;  // K blocks of the sum so far
+                    for (int kb = 0; kb < w.nkb; kb++, part++) {
+                        if (Epi::kPromote > 0 && part == Epi::kPromote) {
+                            if (elect_one())
+                                mma_commit<kCtas>(acc_full + acc);
+                            __syncwarp();
+                            part = 0;
+                            if (++acc == 2) {
+                                acc = 0;
+                                acc_phase ^= 1;
+                            }
+                            if (!(ok = warp_wait(acc_empty + acc, acc_phase ^ 1)))
+                                break;
+                            fence_after();
+                        }
+                        const uint32_t d = tmem + acc * TN;
+                        if (!(ok = warp_wait(full + stage, phase)))
+                            break;
+                        fence_after();
+                        const uint32_t a = saddr(ring + stage * R::kStageBytes);
+                        const uint64_t da = operand_desc(a, kAMN), db = operand_desc(a + R::kBytesA, kBMN);
+                        if (elect_one()) {
+    #pragma unroll
+                            for (int k = 0; k < kBK / 16; k++)
+                                mma_f16<kCtas>(d, da + k * k_step(kAMN), db + k * k_step(kBMN), s.idesc,
+                                               part > 0 || k > 0);
+                            mma_commit<kCtas>(empty + stage);
+                        }
+                        __syncwarp();
+                        if (++stage == R::kStages) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
+                    }
+                    if (elect_one())
+                        mma_commit<kCtas>(acc_full + acc);
+                    __syncwarp();
+                    if (++acc == 2) {
+                        acc = 0;
+                        acc_phase ^= 1;
+                    }
                 }
             }
         }
-    } else if (warp >= 4) {
+    } else {
+        if (Epi::kPromote > 0)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
         int acc = 0;
-        uint32_t acc_phase = 0;
+        uint32_t acc_phase = 0, bar_phase = 0;
         const int quarter = warp % 4, part = (warp - 4) / 4;
         for (uint32_t t = first; t < tiles.total; t += step) {
             const Work w = tiles.at(s, t);
@@ -778,29 +818,48 @@ __global__ void __launch_bounds__(kThreads, 1)
             x.part = part;
             x.chunks = (x.N - w.col + 31) / 32;
             x.lane = lane;
-            x.stage = epi + (warp - 4) * 4096;
-            x.tmem = tmem + acc * TN + ((uint32_t)(quarter * 32) << 16);
+            x.stage = epi + (warp - 4) * Epi::kStages * 4096;
+            x.bar = epi_bar + (warp - 4);
+            x.bar_phase = bar_phase;
+            x.failed = false;
             x.mirror = s.sym && w.row / T::kSquare != w.col / T::kSquare;
             x.empty = w.nkb == 0;
             typename Epi::Pre pre;
-            Epi::fetch(ep, x, part, pre);
-            ok = bar_wait(acc_full + acc, acc_phase);
-            ok = __all_sync(0xffffffffu, ok);
+            Epi::fetch(ep, x, part, pre, maps);
+            int left = w.nkb;
+            do {
+                ok = bar_wait(acc_full + acc, acc_phase);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
+                    break;
+                fence_after();
+                x.tmem = tmem + acc * TN + ((uint32_t)(quarter * 32) << 16);
+                if constexpr (Epi::kPromote > 0)
+                    Epi::add(x, pre);
+                else
+                    Epi::run(ep, x, pre, maps);
+                fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive_at(acc_empty + acc, 0);
+                if (++acc == 2) {
+                    acc = 0;
+                    acc_phase ^= 1;
+                }
+                left -= Epi::kPromote;
+            } while (Epi::kPromote > 0 && left > 0);
+            if constexpr (Epi::kPromote > 0)
+                if (ok)
+                    Epi::run(ep, x, pre, maps);
+            bar_phase = x.bar_phase;
+            ok = ok && !x.failed;
             if (!ok)
                 break;
-            fence_after();
-            Epi::run(ep, x, pre, &map_out);
-            fence_before();
-            __syncwarp();
-            if (lane == 0)
-                bar_arrive_at(acc_empty + acc, 0);
-            if (++acc == 2) {
-                acc = 0;
-                acc_phase ^= 1;
-            }
         }
         if (lane == 0)
             store_wait();
+        if (!ok)
+            let_copies_land();
     }
     if (!ok && lane == 0)
         atomicAdd(&g_wait_timeouts, 1ull);
@@ -866,9 +925,9 @@ inline fsdp_status make_map(CUtensorMap *map, const Operand &o, int batch, int b
 
 template <int kCtas, int TN, bool kAMN, bool kBMN, class Epi>
 fsdp_status product_as(Shape s, const Operand &a, const Operand &b, bool bf16, const typename Epi::Params &ep,
-                       const Operand *out, int64_t tiles, int dev, cudaStream_t stream, const char *what)
+                       const Operand *const *own, int64_t tiles, int dev, cudaStream_t stream, const char *what)
 {
-    using R = Ring<kCtas, TN>;
+    using R = Ring<kCtas, TN, Epi::kStages>;
     auto kernel = product_kernel<kCtas, TN, kAMN, kBMN, Epi>;
     static std::atomic<uint64_t> ready{0};  // devices (of the first 64) whose attribute is set
     const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
@@ -877,14 +936,19 @@ fsdp_status product_as(Shape s, const Operand &a, const Operand &b, bool bf16, c
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmem);
         if (e != cudaSuccess)
             return set_error(FSDP_ECUDA, "%s: cudaFuncSetAttribute: %s", what, cudaGetErrorString(e));
+        cudaFuncAttributes attr;
+        if (Epi::kPromote > 0 && (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess || attr.numRegs < kLaunchRegs))
+            return set_error(FSDP_ECUDA, "%s: built with too few registers", what);
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    CUtensorMap ma, mb, mo{};
+    CUtensorMap ma, mb;
+    EpiMaps mo{};
     fsdp_status st = make_map(&ma, a, s.batch, kAMN ? kBK : kTM, bf16);
     if (st == FSDP_OK)
         st = make_map(&mb, b, s.batch, kBMN ? kBK : s.tn / kCtas, bf16);
-    if (st == FSDP_OK && out)
-        st = make_map(&mo, *out, s.batch, 32, bf16);
+    for (int i = 0; own && i < kEpiMaps && own[i]; i++)
+        if (st == FSDP_OK)
+            st = make_map(&mo.m[i], *own[i], s.batch, 32, bf16);
     if (st != FSDP_OK)
         return st;
     s.idesc = instruction(kTM * kCtas, s.tn, bf16, kAMN, kBMN);
@@ -946,14 +1010,16 @@ inline Form best_form(const Shape &s, int64_t sms, int least_tn)
 }
 
 // Launches D = A B^T. `s` needs M, N, K, batch, epi_bytes, sym, dyn* and, for
-// split sums, splits; the rest is filled in here. `out`: the output, where the
-// epilogue stores through its tensor map (16-bit, of the operands' type).
+// split sums, splits; the rest is filled in here. own0..2: what the epilogue
+// reads and stores through tensor maps (16-bit, of the operands' type).
 template <bool kAMN, bool kBMN, class Epi>
 fsdp_status product(Shape s, const Operand &a, const Operand &b, bool bf16, const typename Epi::Params &ep,
-                    int dev, cudaStream_t stream, const char *what, const Operand *out = nullptr)
+                    int dev, cudaStream_t stream, const char *what, const Operand *own0 = nullptr,
+                    const Operand *own1 = nullptr, const Operand *own2 = nullptr)
 {
+    const Operand *const own[kEpiMaps] = {own0, own1, own2};
     s.group = s.group > 0 ? s.group : 8;
-    s.whole_units = out != nullptr;
+    s.whole_units = own0 != nullptr;
     const Form best = best_form(s, device_sms(dev), Epi::kLeastTN);
     s.tn = best.columns;
     if (best.tiles < 1)
@@ -961,13 +1027,13 @@ fsdp_status product(Shape s, const Operand &a, const Operand &b, bool bf16, cons
     if (best.tiles >= (int64_t)1 << 31)
         return set_error(FSDP_ERANGE, "%s: %lld tiles", what, (long long)best.tiles);
     if (best.ctas == 2)
-        return product_as<2, 256, kAMN, kBMN, Epi>(s, a, b, bf16, ep, out, best.tiles, dev, stream, what);
+        return product_as<2, 256, kAMN, kBMN, Epi>(s, a, b, bf16, ep, own, best.tiles, dev, stream, what);
     if (best.tn == 256)
-        return product_as<1, 256, kAMN, kBMN, Epi>(s, a, b, bf16, ep, out, best.tiles, dev, stream, what);
+        return product_as<1, 256, kAMN, kBMN, Epi>(s, a, b, bf16, ep, own, best.tiles, dev, stream, what);
     if constexpr (Epi::kLeastTN <= 64) {
         if (best.tn == 128)
-            return product_as<1, 128, kAMN, kBMN, Epi>(s, a, b, bf16, ep, out, best.tiles, dev, stream, what);
-        return product_as<1, 64, kAMN, kBMN, Epi>(s, a, b, bf16, ep, out, best.tiles, dev, stream, what);
+            return product_as<1, 128, kAMN, kBMN, Epi>(s, a, b, bf16, ep, own, best.tiles, dev, stream, what);
+        return product_as<1, 64, kAMN, kBMN, Epi>(s, a, b, bf16, ep, own, best.tiles, dev, stream, what);
     }
     return FSDP_OK;
 }
@@ -1044,31 +1110,25 @@ __device__ __forceinline__ void put4_f32(float *p, const float (&v)[4], int n)
 }
 
 // Partial sums of split products, fp32.
-struct PartEpi {
-    static constexpr int kLeastTN = 64;
-    static constexpr bool kAhead = false;
+struct PartEpi : EpiDefaults {
     struct Params {
         float *out;  // [batch][splits][M][ld], M as the device's counts leave it, ld a multiple of 8
         int64_t ld;
     };
     using Pre = NoPre;
-    static __device__ __forceinline__ void carry(const Pre &, Pre &) {}
-    static __device__ __forceinline__ void fetch(const Params &, const Slot &, int, Pre &) {}
-    template <class G>
-    static __device__ __forceinline__ void chunk(const Params &p, const Slot &x, int c, Pre &, G staged)
+    static __device__ __forceinline__ void fetch(const Params &, const Slot &, int, Pre &, const EpiMaps &) {}
+    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &, const EpiMaps &)
     {
-        float mine[32];
         const int rows = x.M - x.group_row(0);
-        const bool in = x.group_col(c) < x.N;
-        float *to = p.out + (((int64_t)x.z * x.splits + x.split) * x.M + x.group_row(0)) * p.ld + x.group_col(c);
-        x.across<false>(c, mine, [&](int i, float(&v)[4]) {
-            if (i * 4 < rows && in)
-                *reinterpret_cast<float4 *>(to + i * 4 * p.ld) = make_float4(v[0], v[1], v[2], v[3]);
-        }, staged);
-    }
-    static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre, const CUtensorMap *)
-    {
-        finish_tile<PartEpi>(p, x, pre);
+        float *row = p.out + (((int64_t)x.z * x.splits + x.split) * x.M + x.group_row(0)) * p.ld;
+#pragma unroll 1
+        for (int c = x.part; c < x.chunks; c += kParts) {
+            const int col = x.group_col(c);
+            x.across(c, [&](int i, float(&v)[4]) {
+                if (i * 4 < rows && col < x.N)
+                    *reinterpret_cast<float4 *>(row + i * 4 * p.ld + col) = make_float4(v[0], v[1], v[2], v[3]);
+            });
+        }
     }
 };
 

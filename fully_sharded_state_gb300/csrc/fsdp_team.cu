@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
             auto keep = [&](uint16_t *x16, int c, float(&mine)[32]) {  // the fp16 x
                 const int left = q.n - x.group_col(c);
                 uint16_t *to = x16 + z * q.xs + x.group_row(0) * q.ldx + x.group_col(c);
-                x.spread<false>(mine, [&](int i, float(&v)[4]) {
+                x.spread(mine, [&](int i, float(&v)[4]) {
                     if (i * 4 < rows && left > 0)
                         *reinterpret_cast<uint2 *>(to + i * 4 * q.ldx) = four_16<false>(v);
                 });
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
                             }
                             uint16_t *to = out + y.group_row(0) * q.ldk + y.group_col(c);
                             const bool in = y.group_col(c) < q.k;
-                            y.spread<false>(mine, [&](int i, float(&v)[4]) {
+                            y.spread(mine, [&](int i, float(&v)[4]) {
                                 if (i * 4 >= yrows || !in)
                                     return;
                                 if (which == 1) {
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
                                 continue;
                             }
                             const int col = x.group_col(c), left = q.n - col;
-                            x.spread<false>(mine, [&](int i, float(&v)[4]) {
+                            x.spread(mine, [&](int i, float(&v)[4]) {
                                 if (i * 4 >= rows || left <= 0)
                                     return;
                                 const int64_t row = x.group_row(0) + i * 4;
@@ -533,8 +533,8 @@ fsdp_status launch_team(const SchulzArgs &a, void *workspace, int dev, void *str
 {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const TeamForm f = team_form(a, device_sms(dev));
-    const SchulzPlan q = schulz_plan(a.batch, a.m, a.n, workspace);
     const bool muon = a.grads != nullptr;
+    const SchulzPlan q = schulz_plan(a.batch, a.m, a.n, muon, workspace);
     TeamParams p{};
     p.m = (int)a.m;
     p.n = (int)a.n;

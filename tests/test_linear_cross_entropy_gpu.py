@@ -76,6 +76,37 @@ def test_pieces_of_the_rows(cuda_lib, n, d, v, piece, masked):
     _check(h, w, t, linear_cross_entropy_grad(h, w, t, ignore_index=IGNORE, piece_rows=piece))
 
 
+@pytest.mark.parametrize("n,d,v,pad", [(16, 1024, 100, 0), (16, 1025, 100, 0), (5, 2056, 300, 8), (16, 4100, 129, 0), (130, 8192, 40, 0)])
+def test_long_rows(cuda_lib, n, d, v, pad):
+    """Above 1024 columns the sums are of parts of 512. A part is 32 steps of
+    16 products; each cuts the running sum, and the products aligned with it,
+    to 24 bits: off by at most twice 2^-23 of the largest of them. Joining the
+    parts rounds by 2^-24 of the running sum each."""
+    h, w, t = _make(n, d, v, d, pad)
+    got = linear_cross_entropy_grad(h, w, t, ignore_index=IGNORE)
+    _check(h, w, t, got)
+    part = 512 if d > 1024 else d
+    worst = torch.zeros(n, dtype=torch.float64, device="cuda")
+    for r in range(n):
+        z = h[r].double()[None] * w.double()  # [v, d]
+        run, off = torch.zeros(v, dtype=torch.float64, device="cuda"), torch.zeros(v, dtype=torch.float64, device="cuda")
+        for k in range(0, d, part):
+            q = z[:, k:k + part].cumsum(1).abs()
+            largest = torch.maximum(q.max(1).values, z[:, k:k + part].abs().max(1).values)
+            off += -(-min(part, d - k) // 16) * 2.0 ** -22 * largest
+            run += z[:, k:k + part].sum(1)
+            off += 2.0 ** -24 * run.abs()
+        worst[r] = off.max()
+    wrows = ref.linear_cross_entropy(h, w, t, IGNORE, True, 1.0)[0]
+    err = (got[1].double() - wrows).abs()
+    # one z, and the log-sum-exp, a mean of them; 8 units for the logarithm,
+    # the exponentials and the last sums
+    assert (err <= 2 * worst + 8 * ref.F32_U * (1 + wrows.abs())).all(), (err / worst).max()
+    loss, rows = linear_cross_entropy(h, w, t, ignore_index=IGNORE)
+    assert torch.equal(loss, got[0]) and torch.equal(rows, got[1])
+    assert ops_wait_timeouts() == 0
+
+
 @pytest.mark.parametrize("scale", [1.0, 1024.0, -0.25])
 def test_sum_and_scale(cuda_lib, scale):
     h, w, t = _make(150, 80, 600, 11, 0, 0.2)
