@@ -199,54 +199,40 @@ __global__ void __launch_bounds__(kStartThreads) scale_kernel(const Source u, ui
 // stay inside a padded row.
 template <bool kPoly>
 struct SquareEpi : EpiDefaults {
+    static constexpr int kStages = kPoly ? 2 : 1;
     struct Params {
         uint16_t *out;
-        const uint16_t *from;  // S
         int64_t ld, stride;
         float b, c;
         float *trace;          // [batch][groups], of S
         int groups;
     };
     struct Pre {
-        uint4 s[kPoly ? 8 : 1];  // this lane's groups of a unit of S
         float shift;
     };
-    static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int unit, Pre &pre)
+    static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int unit, Pre &pre, const EpiMaps &maps)
     {
         if (!kPoly)
             return;
-        if (unit == x.part)
-            pre.shift = shift_of(p.trace + x.z * p.groups, x.M, p.b, p.c, x.lane);
-        const int rows = x.M - x.group_row(0);
-        const uint16_t *from = p.from + x.z * p.stride + x.group_row(0) * p.ld + x.unit_col(unit);
-        const bool in = x.unit_col(unit) < x.N;
-#pragma unroll
-        for (int i = 0; i < 8; i++)
-            if (i * 4 < rows && in)
-                pre.s[kPoly ? i : 0] = *reinterpret_cast<const uint4 *>(from + i * 4 * p.ld);
-    }
-    static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int unit, Pre &pre, const EpiMaps &)
-    {
-        fetch(p, x, unit, pre);
+        pre.shift = shift_of(p.trace + x.z * p.groups, x.M, p.b, p.c, x.lane);
+        if (unit < x.units())
+            x.load_units(&maps.m[1], 1, 1, 0, unit);
     }
     static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre, const EpiMaps &maps)
     {
         uint16_t *out = p.out + x.z * p.stride;
 #pragma unroll 1
         for (int u = x.part; u < x.units(); u += kParts) {
-            uint4 own[kPoly ? 8 : 1];  // the thread's own row of the unit
+            uint4 own[kPoly ? 8 : 1];  // the thread's own row of the unit of S
             if (kPoly) {
-                x.stage_free();
+                if (!x.units_loaded(0))
+                    return;
 #pragma unroll
                 for (int i = 0; i < 8; i++)
-                    *x.group(i) = pre.s[kPoly ? i : 0];
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 8; i++)
-                    own[kPoly ? i : 0] = *x.piece(x.lane, i);
+                    own[kPoly ? i : 0] = *x.piece(x.lane, i, 1);
                 __syncwarp();
                 if (u + kParts < x.units())
-                    fetch(p, x, u + kParts, pre);
+                    x.load_units(&maps.m[1], 1, 1, 0, u + kParts);
             }
             auto finish = [&](int h, float(&v)[32]) {
                 x.load_sum(u * 2 + h, v);
@@ -350,9 +336,14 @@ struct StepParams {
     uint16_t *param[kMuonMaxMats];
 };
 
-template <Then kThen>
+//
+// kSlots: units of hi and lo that a warp has under way. Two take 64 KB from
+// the operands' ring, which a long K needs: taken where the epilogue is the
+// longer part, up to kShortK.
+constexpr int kShortK = 1024;
+template <Then kThen, int kSlots = 1>
 struct StepEpi : EpiDefaults {
-    static constexpr int kStages = 2;
+    static constexpr int kStages = 2 * kSlots;
     using Params = StepParams;
     struct Pre {
         float a;
@@ -360,17 +351,23 @@ struct StepEpi : EpiDefaults {
     static __device__ __forceinline__ void fetch(const Params &p, const Slot &x, int unit, Pre &pre, const EpiMaps &maps)
     {
         pre.a = p.a + shift_of(p.trace + x.z * p.groups, p.k, p.b, p.c, x.lane);
-        if (unit < x.units())
-            x.load_units(&maps.m[0], &maps.m[1], unit);
+        x.stage_free();
+#pragma unroll
+        for (int i = 0; i < kSlots; i++)
+            if (unit + i * kParts < x.units())
+                x.load_units(maps.m, 2, 2 * i, i, unit + i * kParts);
     }
     static __device__ __forceinline__ void run(const Params &p, const Slot &x, Pre &pre, const EpiMaps &maps)
     {
         const int rows = x.M - x.group_row(0);
 #pragma unroll 1
         for (int u = x.part; u < x.units(); u += kParts) {
-            if (u > x.part)
-                x.load_units(&maps.m[0], &maps.m[1], u);
-            if (!x.units_loaded())
+            const int i = (u - x.part) / kParts, slot = i % kSlots;
+            if (i >= kSlots) {
+                x.stage_free();
+                x.load_units(maps.m, 2, 2 * slot, slot, u);
+            }
+            if (!x.units_loaded(slot))
                 return;
             // The thread's own row of the unit. Where the first stage is
             // needed for what leaves, hi is taken out of it before.
@@ -384,8 +381,8 @@ struct StepEpi : EpiDefaults {
             auto finish = [&](int h, float(&v)[32]) {
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    const uint4 a = kThen != Then::kKeep ? hi[h * 4 + i] : *x.piece(x.lane, h * 4 + i, 0);
-                    const uint4 b = *x.piece(x.lane, h * 4 + i, 1);
+                    const uint4 a = kThen != Then::kKeep ? hi[h * 4 + i] : *x.piece(x.lane, h * 4 + i, 2 * slot);
+                    const uint4 b = *x.piece(x.lane, h * 4 + i, 2 * slot + 1);
                     const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
                     for (int k = 0; k < 4; k++) {
@@ -409,11 +406,11 @@ struct StepEpi : EpiDefaults {
                             a[i] = high(v[8 * g + 2 * i], v[8 * g + 2 * i + 1]);
                             b[i] = low(a[i], v[8 * g + 2 * i], v[8 * g + 2 * i + 1]);
                         }
-                        *x.piece(x.lane, h * 4 + g, 0) = make_uint4(a[0], a[1], a[2], a[3]);
-                        *x.piece(x.lane, h * 4 + g, 1) = make_uint4(b[0], b[1], b[2], b[3]);
+                        *x.piece(x.lane, h * 4 + g, 2 * slot) = make_uint4(a[0], a[1], a[2], a[3]);
+                        *x.piece(x.lane, h * 4 + g, 2 * slot + 1) = make_uint4(b[0], b[1], b[2], b[3]);
                     }
                 }
-                x.store_units(&maps.m[2], &maps.m[1], u);
+                x.store_units(&maps.m[2], &maps.m[1], 2 * slot, u);
             } else if (kThen == Then::kOut) {
                 const int left = x.N - x.unit_col(u);
                 uint16_t *to = p.out + x.z * p.out_stride + x.group_row(0) * p.ldo + x.unit_col(u);
@@ -597,8 +594,8 @@ fsdp_status launch_newton_schulz(const SchulzArgs &a, void *workspace, int dev, 
         const Operand x{q.x16[step % 2], a.n, a.m, q.ldx, xs};
         const Operand gram{q.s, q.k, q.k, q.ldk, ks}, poly{q.p, q.k, q.k, q.ldk, ks};
         Shape sq = square_shape(q.k, wide ? n : m, batch, sms, false);
-        const typename SquareEpi<false>::Params e1{q.s, nullptr, q.ldk, ks, 0.0f, 0.0f, q.trace, (int)q.groups};
-        const typename SquareEpi<true>::Params e2{q.p, q.s, q.ldk, ks, a.b, a.c, q.trace, (int)q.groups};
+        const typename SquareEpi<false>::Params e1{q.s, q.ldk, ks, 0.0f, 0.0f, q.trace, (int)q.groups};
+        const typename SquareEpi<true>::Params e2{q.p, q.ldk, ks, a.b, a.c, q.trace, (int)q.groups};
         if (q.splits > 1) {
             sq.sym = sq.square = 0;
             sq.splits = q.splits;
@@ -617,7 +614,7 @@ fsdp_status launch_newton_schulz(const SchulzArgs &a, void *workspace, int dev, 
             return st;
         sq = square_shape(q.k, q.k, batch, sms, true);
         if ((st = product<false, false, SquareEpi<true>>(sq, gram, gram, false, e2, dev, s, "newton_schulz (P)",
-                                                         &poly)) != FSDP_OK)
+                                                         &poly, &gram)) != FSDP_OK)
             return st;
         Shape up{};
         up.M = m;
@@ -632,7 +629,7 @@ fsdp_status launch_newton_schulz(const SchulzArgs &a, void *workspace, int dev, 
             return wide ? product<false, true, E>(up, poly, x, false, ep, dev, s, "newton_schulz (x)", &x, &lo, &next)
                         : product<false, false, E>(up, x, poly, false, ep, dev, s, "newton_schulz (x)", &x, &lo, &next);
         };
-        st = step + 1 < a.steps ? update(StepEpi<Then::kKeep>{})
+        st = step + 1 < a.steps ? (q.k <= kShortK ? update(StepEpi<Then::kKeep, 2>{}) : update(StepEpi<Then::kKeep>{}))
              : muon             ? update(StepEpi<Then::kMaster>{})
                                 : update(StepEpi<Then::kOut>{});
         if (st != FSDP_OK)

@@ -399,11 +399,11 @@ struct Slot {
     int part, chunks;
     __device__ __forceinline__ int units() const { return (chunks + 1) / 2; }
     uint32_t tmem;
-    unsigned char *stage;  // the warp's 4 KB (or two of them): 32 rows of 128 bytes
+    unsigned char *stage;  // the warp's stages of 4 KB: 32 rows of 128 bytes
     int lane;
-    uint64_t *bar;              // of the warp's own loads (LoadUnits)
-    mutable uint32_t bar_phase;
-    mutable bool failed;        // a wait on it was given up
+    uint64_t *bar;              // two, of the warp's own loads
+    mutable uint32_t bar_phase; // a bit of each
+    mutable bool failed;        // a wait on one was given up
     bool mirror;  // sym: also store the transposed element
     bool empty;   // K was empty (only a dynamic one can be): the accumulator
                   // holds nothing, the sum is 0
@@ -535,34 +535,35 @@ struct Slot {
             store_read_wait();
         __syncwarp();
     }
-    // A unit of each of two tensor maps into the warp's two stages (rows and
-    // columns past a map are zeros), and the wait for them.
-    __device__ __forceinline__ void load_units(const CUtensorMap *a, const CUtensorMap *b, int unit) const
+    // A unit of each of n tensor maps into the warp's stages from `at` on (rows
+    // and columns past a map are zeros), and the wait for them; bar i. The
+    // stages are free before (stage_free, where stores leave from them).
+    __device__ __forceinline__ void load_units(const CUtensorMap *maps, int n, int at, int i, int unit) const
     {
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        stage_free();
+        __syncwarp();
         if (lane == 0) {
-            bar_expect(bar, 2 * 4096);
-            tma_load<1>(stage, a, col + unit * 64, row, z, bar);
-            tma_load<1>(stage + 4096, b, col + unit * 64, row, z, bar);
+            bar_expect(bar + i, n * 4096);
+            for (int k = 0; k < n; k++)
+                tma_load<1>(stage + (at + k) * 4096, maps + k, col + unit * 64, row, z, bar + i);
         }
         __syncwarp();
     }
-    __device__ __forceinline__ bool units_loaded() const
+    __device__ __forceinline__ bool units_loaded(int i) const
     {
-        if (!warp_wait(bar, bar_phase))
+        if (!warp_wait(bar + i, bar_phase >> i & 1))
             failed = true;
-        bar_phase ^= 1;
+        bar_phase ^= 1u << i;
         return !failed;
     }
-    // And back out of them.
-    __device__ __forceinline__ void store_units(const CUtensorMap *a, const CUtensorMap *b, int unit) const
+    // And back out of two of them.
+    __device__ __forceinline__ void store_units(const CUtensorMap *a, const CUtensorMap *b, int at, int unit) const
     {
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0 && row < M) {
-            tma_store(a, stage, col + unit * 64, row, z);
-            tma_store(b, stage + 4096, col + unit * 64, row, z);
+            tma_store(a, stage + at * 4096, col + unit * 64, row, z);
+            tma_store(b, stage + (at + 1) * 4096, col + unit * 64, row, z);
         }
         __syncwarp();
     }
@@ -639,10 +640,10 @@ struct Ring {
     static constexpr int kBytesA = kTM * kBK * 2;
     static constexpr int kBytesB = kRowsB * kBK * 2;
     static constexpr int kStageBytes = kBytesA + kBytesB;
-    static constexpr int kFit = (kEpiStages == 1 ? 192 : 160) * 1024 / kStageBytes;
-    static constexpr int kStages = kFit < 8 ? kFit : 8;
-    static constexpr int kBarriers = 2 * kStages + 4 + kEpiWarps;
     static constexpr int kEpiBytes = kEpiWarps * kEpiStages * 4096;
+    static constexpr int kFit = (225 * 1024 + 512 - kEpiBytes) / kStageBytes;
+    static constexpr int kStages = kFit < 8 ? kFit : 8;
+    static constexpr int kBarriers = 2 * kStages + 4 + 2 * kEpiWarps;
     // 1024 bytes for the swizzle's alignment, the epilogue's stages, the
     // barriers and the TMEM address
     static constexpr int kSmem = 1024 + kStages * kStageBytes + kEpiBytes + kBarriers * 8 + 16;
@@ -665,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *acc_full = empty + R::kStages;
     uint64_t *acc_empty = acc_full + 2;
     uint64_t *epi_bar = acc_empty + 2;
-    uint32_t *tmem_at = reinterpret_cast<uint32_t *>(epi_bar + kEpiWarps);
+    uint32_t *tmem_at = reinterpret_cast<uint32_t *>(epi_bar + 2 * kEpiWarps);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = kCtas == 2 ? cluster_rank() : 0;
@@ -685,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar_init(acc_full + i, 1);
             bar_init(acc_empty + i, kEpiWarps * kCtas);
         }
-        for (int i = 0; i < kEpiWarps; i++)
+        for (int i = 0; i < 2 * kEpiWarps; i++)
             bar_init(epi_bar + i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -819,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             x.chunks = (x.N - w.col + 31) / 32;
             x.lane = lane;
             x.stage = epi + (warp - 4) * Epi::kStages * 4096;
-            x.bar = epi_bar + (warp - 4);
+            x.bar = epi_bar + 2 * (warp - 4);
             x.bar_phase = bar_phase;
             x.failed = false;
             x.mirror = s.sym && w.row / T::kSquare != w.col / T::kSquare;
