@@ -22,7 +22,15 @@
 // last product's traffic, and both move by bulk copies through the warps'
 // stages, so that no thread loads or stores them: that epilogue was bound by
 // shared memory and L1, which the MMAs' operands use as well (48 x 512 x 512:
-// 365 us with the fp32 x, 324 so; a Muon step of 14336 x 4096 3,032 and 3,001).
+// 365 us with the fp32 x, 324 so).
+//
+// What bounds it. Small matrices: the epilogues. Five steps of 48 x 512 x 512
+// are 303 us, of which the tensor cores are busy for a third; each epilogue
+// waits for its first unit and its accumulator in turn, and 192 tiles are 2.5
+// waves of the 76 CTA pairs. Few small matrices: latency, see the team kernel.
+// Large ones: the tensor cores. A Muon step of 14336 x 4096 over 8 ranks is
+// 3.0 ms, 4.0 TFLOP and a first pass of 1.8 GB: 1,330 TFLOP/s in all, at the
+// clock that the power limit leaves.
 #include "fsdp_muon.cuh"
 
 namespace fsdp {
@@ -339,8 +347,9 @@ struct StepParams {
 //
 // kSlots: units of hi and lo that a warp has under way. Two take 64 KB from
 // the operands' ring, which a long K needs: taken where the epilogue is the
-// longer part, up to kShortK.
-constexpr int kShortK = 1024;
+// longer part. One and two: 48 x 512 x 512 316 and 307 us, 16 x 768 x 768 273
+// and 265, 16 x 1024 x 1024 473 and 495, 4096 x 14336 2,612 and 2,867.
+constexpr int kShortK = 768;
 template <Then kThen, int kSlots = 1>
 struct StepEpi : EpiDefaults {
     static constexpr int kStages = 2 * kSlots;

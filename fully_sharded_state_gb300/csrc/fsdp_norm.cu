@@ -8,6 +8,9 @@
 // the mean are formed per warp, in two steps over the registers, and the
 // warps' joined by their counts: fp32 precision under a large mean, where
 // sum(x^2) - mean^2 would lose it.
+//
+// 16384 x 4096 bf16: forward 50.4 us, 5.3 TB/s (0.79 of a plain copy's rate);
+// backward 76.8 us, 5.2 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -14,13 +14,18 @@
 //             the next tile is being multiplied. (Sixteen were no faster: an
 //             epilogue is bound by the 128 bytes a clock of shared memory and
 //             L1, which the MMAs' operands use as well.) What they read and
-//             write in memory
-//             goes through 4 KB of shared memory per warp, so that lanes
+//             write in memory goes through 4 KB of shared memory per warp,
+//             by bulk copies where rows start on 16 bytes, else so that lanes
 //             touch whole lines of a row; with each lane on a row of its own,
 //             a 512 x 512 update spent 17 us per tile on its accesses
 // The grid is persistent. An operand may be stored with K adjacent
 // (row-major [rows, K]) or with its rows adjacent ([K, rows], "MN-major"),
 // which the descriptors express; nothing is transposed in memory.
+//
+// Measured (2048 x 4096 x 32768, bf16, each alone): 1,880 TFLOP/s with the
+// loss's exponentials as epilogue, 1,812 and 1,968 for its two gradients; the
+// tensor pipe is active for 91 to 97 % of the time. Back to back for longer
+// the power limit holds all three at 1,620 to 1,720 (8192 x 4096 x 65536).
 //
 // Every wait is bounded (kWaitNs); a role that gives up leaves its loop, and
 // the block counts itself.
@@ -653,7 +658,8 @@ struct Ring {
 template <int kCtas, int TN, bool kAMN, bool kBMN, class Epi>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                   const __grid_constant__ EpiMaps maps, const __grid_constant__ Shape s, const __grid_constant__ typename Epi::Params ep)
+                   const __grid_constant__ EpiMaps maps, const __grid_constant__ Shape s,
+                   const __grid_constant__ typename Epi::Params ep)
 {
     using R = Ring<kCtas, TN, Epi::kStages>;
     extern __shared__ unsigned char raw[];

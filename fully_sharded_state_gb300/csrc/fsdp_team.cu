@@ -15,6 +15,11 @@
 //   per matrix: read the gradients (and the momentum), sum of squares -- meet
 //               -- scale, x16 -- meet -- (S -- meet -- P -- meet -- x -- meet)
 //               x steps; the last x goes out instead
+//
+// 4 x 512 x 512, a Muon step over 4 ranks: 88 us (when first written 95,
+// and 104 with a kernel for each product). It is bound by latency: a product is about 0.7 us of waiting for the
+// meeting, 0.5 until its first operands are there, 1.7 to 2.2 of products,
+// 0.7 of epilogue and 0.6 of meeting, 15 times.
 #include "fsdp_muon.cuh"
 
 namespace fsdp {
