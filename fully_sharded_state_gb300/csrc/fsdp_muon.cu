@@ -423,20 +423,20 @@ struct StepEpi : EpiDefaults {
             } else if (kThen == Then::kOut) {
                 const int left = x.N - x.unit_col(u);
                 uint16_t *to = p.out + x.z * p.out_stride + x.group_row(0) * p.ldo + x.unit_col(u);
-                const bool whole = rows_of_16(p.out, p.ldo | p.out_stride);
-                x.emit16<true>(u, finish, [&](int i, const uint4 &e) {
-                    if (i * 4 >= rows)
-                        return;
-                    if (whole) {
-                        put8_16(to + i * 4 * p.ldo, e, left);
-                    } else {
-                        const uint16_t *q = reinterpret_cast<const uint16_t *>(&e);
-#pragma unroll
-                        for (int k = 0; k < 8; k++)
-                            if (k < left)
-                                to[i * 4 * p.ldo + k] = q[k];
-                    }
-                });
+                auto result = [&](int h, float(&v)[32]) {
+                    x.load(u * 2 + h, v);
+                    finish(h, v);
+                };
+                if (rows_of_16(p.out, p.ldo | p.out_stride))
+                    x.emit16<true>(u, finish, [&](int i, const uint4 &e) {
+                        if (i * 4 < rows)
+                            put8_16(to + i * 4 * p.ldo, e, left);
+                    });
+                else
+                    x.emit_rows<true>(u, result, [&](int r) {
+                        const int64_t row = x.row - x.lane + r;
+                        return row < x.M ? p.out + x.z * p.out_stride + row * p.ldo + x.col + u * 64 : nullptr;
+                    });
             } else {
 #pragma unroll
                 for (int h = 0; h < 2; h++) {

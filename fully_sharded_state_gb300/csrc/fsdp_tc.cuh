@@ -395,6 +395,22 @@ __device__ __forceinline__ uint32_t two(float lo, float hi)
     return kBf16 ? pack_bf16(lo, hi) : pack_f16(lo, hi);
 }
 
+// 8 of the 16-bit elements of a and b, from number `from` (0 to 7) on.
+__device__ __forceinline__ uint4 eight_from(const uint4 &a, const uint4 &b, int from)
+{
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 6; i++)
+        w[i] = from & 4 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; i++)
+        w[i] = from & 2 ? w[i + 1] : w[i];
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+        w[i] = from & 1 ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // What an epilogue thread is given: its row, the tile's first column, and
 // where they are in tensor memory. The tile's columns are taken in chunks of
 // 32, or units of two chunks: warp `part` of the kParts that share a row takes
@@ -454,20 +470,6 @@ struct Slot {
         __syncwarp();
     }
     __device__ __forceinline__ uint4 *group(int i) const { return piece(i * 4 + lane / 8, lane % 8); }
-
-    // Calls f(r, v) for every row of a chunk, v the value of this lane's
-    // column: for rows that do not start on whole groups.
-    template <class F>
-    __device__ __forceinline__ void by_rows(int chunk, F f) const
-    {
-        float mine[32];
-        load_sum(chunk, mine);
-        put_stage(mine);
-#pragma unroll 8
-        for (int r = 0; r < 32; r++)
-            f(r, reinterpret_cast<const float *>(piece(r, lane / 4))[lane % 4]);
-        __syncwarp();
-    }
 
     __device__ __forceinline__ void load_sum(int chunk, float (&mine)[32]) const
     {
@@ -530,6 +532,50 @@ struct Slot {
 #pragma unroll
         for (int i = 0; i < 8; i++)
             f(i, *group(i));
+        __syncwarp();
+    }
+
+    // A unit as 16-bit numbers to rows that may start anywhere: to(r) is where
+    // the unit's first column of row r (0..31) goes, or NULL. Eight lanes have
+    // a row: its whole 16-byte pieces, each cut out of two of the stage's, and
+    // the 8 elements before and after them one each.
+    template <bool kBf16, class Get, class To>
+    __device__ __forceinline__ void emit_rows(int unit, Get get, To to) const
+    {
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            float v[32];
+            get(h, v);
+#pragma unroll
+            for (int g = 0; g < 4; g++)
+                *piece(lane, h * 4 + g) = make_uint4(
+                    two<kBf16>(v[8 * g], v[8 * g + 1]), two<kBf16>(v[8 * g + 2], v[8 * g + 3]),
+                    two<kBf16>(v[8 * g + 4], v[8 * g + 5]), two<kBf16>(v[8 * g + 6], v[8 * g + 7]));
+        }
+        __syncwarp();
+        const int left = N - (col + unit * 64), k = lane % 8;
+#pragma unroll 2
+        for (int i = 0; i < 8; i++) {
+            const int r = i * 4 + lane / 8;
+            uint16_t *p = to(r);
+            auto element = [&](int e) { return reinterpret_cast<const uint16_t *>(piece(r, e / 8))[e % 8]; };
+            if (p == nullptr)
+                continue;
+            const int off = (int)(reinterpret_cast<uintptr_t>(p) & 15) / 2;  // elements past a 16-byte boundary
+            if (left >= 64) {
+                if (off == 0) {
+                    *reinterpret_cast<uint4 *>(p + k * 8) = *piece(r, k);
+                } else {
+                    if (k > 0)
+                        *reinterpret_cast<uint4 *>(p + k * 8 - off) = eight_from(*piece(r, k - 1), *piece(r, k), 8 - off);
+                    const int e = k < 8 - off ? k : 56 + k;
+                    p[e] = element(e);
+                }
+            } else {
+                for (int e = k; e < left; e += 8)
+                    p[e] = element(e);
+            }
+        }
         __syncwarp();
     }
 
