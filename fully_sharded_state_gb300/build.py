@@ -25,7 +25,7 @@ LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libfsdp_shard.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = ["fsdp_kernels.cu", "fsdp_norm.cu", "fsdp_loss.cu", "fsdp_muon.cu", "fsdp_team.cu",
+SOURCES = ["fsdp_kernels.cu", "fsdp_norm.cu", "fsdp_loss.cu", "fsdp_muon.cu", "fsdp_team.cu", "fsdp_thin.cu",
            "fsdp_capi.cpp",
            "fsdp_ops_capi.cpp"]
 HEADERS = [os.path.join(CSRC, h) for h in ("fsdp_internal.h", "fsdp_ops_internal.h", "fsdp_tc.cuh",

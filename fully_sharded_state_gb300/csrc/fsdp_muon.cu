@@ -1,5 +1,6 @@
 // fsdp_muon.cu -- Newton-Schulz orthogonalisation and the Muon step, for
-// sm_103a.
+// sm_103a, with a kernel per product; fsdp_team.cu and fsdp_thin.cu have the
+// forms for few small and for thin matrices.
 //
 //   start    one pass over the input: the norm's partial sums; for the Muon
 //            step also the fold of the R ranks' gradients and the momentum
@@ -513,8 +514,15 @@ fsdp_status launch_newton_schulz(const SchulzArgs &a, void *workspace, int dev, 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool muon = a.grads != nullptr;
     const int sms = device_sms(dev);
-    const int64_t team = team_clocks(a, dev);
-    if (team >= 0 && team < product_clocks(a, sms))
+    const int64_t thin = thin_clocks(a, sms), team = team_clocks(a, dev), products = product_clocks(a, sms);
+    const int64_t other = team >= 0 && team < products ? team : products;
+    // preferred up to twice the other's estimate, for the sake of fp32: with
+    // few rows, fp16 operands leave a nearly low-rank result 8e-3 off (5 x
+    // 30011). Measured, that is a third slower at most (8 x 8192 transposed,
+    // 139 us against 110)
+    if (thin >= 0 && thin < 2 * other)
+        return launch_thin(a, workspace, dev, stream);
+    if (other == team)
         return launch_team(a, workspace, dev, stream);
     const SchulzPlan q = schulz_plan(a.batch, a.m, a.n, muon, workspace);
     const int batch = (int)a.batch, m = (int)a.m, n = (int)a.n;

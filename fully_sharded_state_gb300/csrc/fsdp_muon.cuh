@@ -1,5 +1,5 @@
-// fsdp_muon.cuh -- what the two forms of the Newton-Schulz iteration share
-// (fsdp_muon.cu, fsdp_team.cu): the workspace and the reading of gradients.
+// fsdp_muon.cuh -- what the forms of the Newton-Schulz iteration share
+// (fsdp_muon.cu, fsdp_team.cu, fsdp_thin.cu): the workspace and the reading of gradients.
 #pragma once
 
 #include "fsdp_tc.cuh"
@@ -10,6 +10,9 @@ namespace fsdp {
 // clocks, or -1 where the matrices do not fit it.
 int64_t team_clocks(const SchulzArgs &a, int dev);
 fsdp_status launch_team(const SchulzArgs &a, void *workspace, int dev, void *stream);
+// One block per matrix, in fp32, for thin ones (fsdp_thin.cu). Likewise.
+int64_t thin_clocks(const SchulzArgs &a, int sms);
+fsdp_status launch_thin(const SchulzArgs &a, void *workspace, int dev, void *stream);
 
 namespace {
 

@@ -68,6 +68,45 @@ def test_long_sums(cuda_lib, batch, m, n):
     assert torch.equal(newton_schulz(g), out)
 
 
+@pytest.mark.parametrize("batch,k,l", [(1, 1, 1), (3, 1, 97), (28, 2, 2), (200, 4, 4), (100, 8, 8), (50, 16, 16),
+                                       (45, 2, 1939), (8, 9, 2485), (3, 25, 504), (2, 31, 33), (2, 32, 32),
+                                       (1, 32, 700), (2, 5, 30011)])
+@pytest.mark.parametrize("tall", [False, True])
+def test_thin_matrices(cuda_lib, batch, k, l, tall):
+    """fp32 throughout: the 64-bit form with every product rounded to fp32
+    (CPU, 300 square Gaussian matrices each of 4 to 32 rows, and rank 1 and 2
+    under noise) is 7e-4 off in norm at most; the result's bf16 rounding is
+    2^-8 of each element at most."""
+    g = _gauss((batch, l, k) if tall else (batch, k, l), k + l)
+    if k > 4:
+        g[0] = (_gauss((l, 2), 1, 1.0) @ _gauss((2, k), 2, 1.0) if tall else _gauss((k, 2), 1, 1.0) @ _gauss((2, l), 2, 1.0)) + 10 * g[0]
+    out = newton_schulz(g)
+    for i in range(batch):
+        exact = ref.newton_schulz(g[i])
+        assert (out[i].double() - exact).norm() <= (ref.BF16_U + 1e-3) * exact.norm(), i
+    assert torch.equal(newton_schulz(g), out)
+    wide = torch.zeros(batch, g.shape[1] + 1, g.shape[2] + 3, device="cuda", dtype=torch.bfloat16)
+    newton_schulz(g, out=wide[:, :-1, 1:-2])
+    assert torch.equal(wide[:, :-1, 1:-2], out)
+    wide[:, :-1, 1:-2] = 0
+    assert not wide.any()
+
+
+@pytest.mark.parametrize("m,n", [(3, 50), (50, 3), (16, 1600), (12, 4001), (4001, 12), (1, 40000)])
+def test_thin_muon_step(cuda_lib, m, n):
+    """As test_muon_step, with the bound of test_thin_matrices on the update."""
+    grads, master, mom, params = _state(3, m, n, 3, torch.bfloat16, 7 + m)
+    old_w, old_m = [w.clone() for w in master], [x.clone() for x in mom]
+    muon_step(grads, master, mom, params, MuonHP(lr=0.02, momentum=0.9, weight_decay=0.1))
+    for i in range(3):
+        w, x, u = ref.muon(grads[i], old_w[i], old_m[i], 0.02, 0.9, 0.1, max(1.0, m / n) ** 0.5, True)
+        size = sum(q.double().abs() for q in grads[i]) / 3 + old_m[i].double().abs()
+        assert ((mom[i].double() - x).abs() <= 7 * 2 * ref.F32_U * size).all()
+        err = (master[i].double() - w).norm()
+        assert err <= 1e-3 * u.norm() + 4 * ref.F32_U * (w.norm() + u.norm())
+        assert torch.equal(params[i], master[i].bfloat16())
+
+
 def test_nearly_low_rank(cuda_lib):
     g = _gauss((512, 16), 1, 1.0) @ _gauss((16, 768), 2, 1.0) + 0.01 * _gauss((512, 768), 3, 1.0)
     _check(newton_schulz(g), g)
