@@ -393,8 +393,10 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
 // 4096 bf16 took 107 us.
 //
 // bf16 rows are bound by instructions as much as by HBM. Two elements share
-// each fp32 one (Pair), xhat is one multiply-add, and xhat and dy gamma stay in
-// registers for dx, which is two more.
+// each fp32 one (Pair), and xhat and dy gamma stay in registers for dx. x - mean
+// and dy gamma - mean(dy gamma) are formed first, as one multiply-add less would
+// not: a row of one value, or of one column, has xhat = 0 and dx = 0, where
+// x rstd - mean rstd leaves a rounding times rstd, up to 1 / sqrt(eps).
 template <typename T, bool kFull, bool kStaged, int TPR, int NV>
 __global__ void __launch_bounds__(backward_block<TPR>(), backward_block<TPR>() > 256 ? 1 : 2)
     norm_backward_kernel(const BackwardParams p)
@@ -489,13 +491,13 @@ __global__ void __launch_bounds__(backward_block<TPR>(), backward_block<TPR>() >
         }
         // xhat and dy gamma of a chunk; past the row's end dy and gamma are 0,
         // and so is all that xhat enters
-        const Pair scale(rstd), shift(-mean * rstd);
+        const Pair scale(rstd), shift(-mean);
         auto widen = [&](int q, Pair(&xhat)[V / 2], Pair(&gg)[V / 2], Pair(&g)[V / 2]) {
             cx[q].pairs(xhat);
             cy[q].pairs(g);
 #pragma unroll
             for (int i = 0; i < V / 2; i++) {
-                xhat[i] = fma2(xhat[i], scale, shift);
+                xhat[i] = (xhat[i] + shift) * scale;
                 gg[i] = g[i] * gamma[q][i];
             }
         };
@@ -549,7 +551,7 @@ __global__ void __launch_bounds__(backward_block<TPR>(), backward_block<TPR>() >
         if (!live)
             continue;
         // dx = rstd (dy gamma - mean(dy gamma) - xhat mean(dy gamma xhat))
-        const Pair ca(-a * inv * rstd), cb(-b * inv * rstd);
+        const Pair ca(-a * inv), cb(-b * inv);
         T *dx = static_cast<T *>(p.dx) + r * p.lddx;
 #pragma unroll
         for (int q = 0; q < NV; q++) {
@@ -566,7 +568,7 @@ __global__ void __launch_bounds__(backward_block<TPR>(), backward_block<TPR>() >
             }
 #pragma unroll
             for (int i = 0; i < V / 2; i++)
-                fma2(gg[i], scale, fma2(xhat[i], cb, ca)).get(out[2 * i], out[2 * i + 1]);
+                (fma2(xhat[i], cb, gg[i] + ca) * scale).get(out[2 * i], out[2 * i + 1]);
             store_chunk<T, kFull, TPR>(dx, q, t, p.cols, out);
         }
     }

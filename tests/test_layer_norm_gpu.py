@@ -147,3 +147,27 @@ def test_gradients_against_differences(cuda_lib):
         want = (grad.double() * d.double()).sum().item()
         scale = (grad.double() * d.double()).norm().item()
         assert abs(diff - want) <= 2e-3 * scale + 1e-3, (at, diff, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,cols", [(4, 1), (300, 1), (5, 64), (7, 513), (3, 2048), (2, 11127), (2, 20001)])
+def test_rows_of_one_value(cuda_lib, rows, cols, dtype):
+    """xhat is 0 in every element, and so dgamma, and with one column dx:
+    differences of equal numbers, which are exact."""
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    value = (torch.randn(rows, 1, device="cuda", generator=g) * 2 + 0.3).to(dtype)
+    x = value.expand(rows, cols).contiguous()
+    dy = torch.randn(rows, cols, device="cuda", generator=g).to(dtype)
+    gamma = (1 + 0.1 * torch.randn(cols, device="cuda", generator=g)).to(dtype)
+    mean, rstd = value.float()[:, 0].contiguous(), torch.full((rows,), 1e-5, device="cuda").rsqrt()
+    dx, dgamma, dbeta = layer_norm_backward(dy, x, gamma, mean, rstd)
+    assert not dgamma.any()
+    if cols == 1:
+        assert not dx.any()
+    want = dy.double() * gamma.double()
+    want = (want - want.mean(1, keepdim=True)) * rstd.double()[:, None]
+    size = (dy.double() * gamma.double()).abs()
+    # g rounded, its mean of up to 20,001 terms in a tree, one difference, one product, the result's rounding
+    unit = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24
+    bound = (64 * 2.0 ** -24 * (size + size.mean(1, keepdim=True))) * rstd.double()[:, None] + unit * want.abs() + 1e-30
+    assert ((dx.double() - want).abs() <= bound).all()
