@@ -22,9 +22,9 @@
 // (row-major [rows, K]) or with its rows adjacent ([K, rows], "MN-major"),
 // which the descriptors express; nothing is transposed in memory.
 //
-// Measured (2048 x 4096 x 32768, bf16, each alone): 1,880 TFLOP/s with the
-// loss's exponentials as epilogue, 1,812 and 1,968 for its two gradients; the
-// tensor pipe is active for 91 to 97 % of the time. Back to back for longer
+// Measured (2048 x 4096 x 32768, bf16, each alone): 1,840 to 1,880 TFLOP/s
+// with the loss's exponentials as epilogue, 1,780 to 1,810 and 1,950 to 1,970
+// for its two gradients; the tensor pipe is active for 91 to 97 % of the time. Back to back for longer
 // the power limit holds all three at 1,620 to 1,720 (8192 x 4096 x 65536).
 //
 // Every wait is bounded (kWaitNs); a role that gives up leaves its loop, and
