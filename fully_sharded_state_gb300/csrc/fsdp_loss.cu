@@ -20,7 +20,7 @@
 // 6 * rows * cols * vocab flops for a step: nothing is computed twice. Many
 // rows are bound by the tensor cores, at the clock that the power limit
 // leaves: 8192 x 4096 x 65536 in 7.8 to 8.3 ms (from one board to another),
-// 1,590 to 1,690 TFLOP/s. Few rows are bound by reading the weight and by four
+// 1,590 to 1,690 TFLOP/s. Few rows are bound by reading the weight and by six
 // kernels' starts and ends: 256 x 512 x 32000 in 59 us, of which the products'
 // flops are 13; the loss alone of one row in 25 us of the caller's time.
 // Weights and gradients whose rows do not start on 16 bytes cost a copy each
