@@ -364,6 +364,14 @@ __device__ __forceinline__ float reduce_sum(float v, float *sh)
     return v;
 }
 
+// What a piece's exponentials count for in a row with the reference `ref`. A
+// piece of -inf alone counts for nothing: its exponentials, about 0, are 0, and
+// exp(0 - ref) times 0 would be NaN where ref is below -88.
+__device__ __forceinline__ float piece_factor(float top, float ref)
+{
+    return top == -CUDART_INF_F ? 0.0f : expf(top - ref);
+}
+
 // Two exponentials as fp16 -> two elements of G as bf16; t: which of them is
 // the target's, if any.
 __device__ __forceinline__ uint32_t two_of_g(uint32_t e, float f, int t)
@@ -412,8 +420,7 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowsParams p)
         float sum = 0.0f;
         for (int i = threadIdx.x; i < p.pieces; i += 256) {
             const float2 q = st[i];
-            // a piece without a finite maximum has its exponentials about 0
-            sum += q.y * expf((q.x == -CUDART_INF_F ? 0.0f : q.x) - ref);
+            sum += q.y * piece_factor(q.x, ref);  // a NaN in q.y stays one
         }
         sum = reduce_sum(sum, sh);
         if (threadIdx.x == 0 && blockIdx.y == 0)
@@ -423,8 +430,7 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowsParams p)
         const int t = p.target[r];
         const float inv = 1.0f / sum;
         auto turn = [&](uint4 u, int c) {
-            const float q = st[c / kPieceCols].x;
-            const float f = expf((q == -CUDART_INF_F ? 0.0f : q) - ref) * inv;
+            const float f = piece_factor(st[c / kPieceCols].x, ref) * inv;
             u.x = two_of_g(u.x, f, t - c);
             u.y = two_of_g(u.y, f, t - c - 2);
             u.z = two_of_g(u.z, f, t - c - 4);
