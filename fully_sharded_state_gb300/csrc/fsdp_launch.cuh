@@ -22,6 +22,8 @@ template <class... Params, class... Args>
 fsdp_status launch(const char *what, void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
                    cudaStream_t stream, int cluster, const Args &...args)
 {
+    if (Record *r = current_record())
+        return r->add("%s: %u x %u blocks of %d", what, grid.x, grid.y, threads);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);

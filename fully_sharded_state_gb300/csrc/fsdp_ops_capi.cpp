@@ -2,6 +2,9 @@
 // training-step operators (fsdp_ops.h). Host code only.
 #include <algorithm>
 #include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <cstring>
 #include <exception>
 #include <limits>
 #include <mutex>
@@ -18,8 +21,28 @@ cudaError_t loss_wait_timeouts(unsigned long long *n);
 cudaError_t muon_wait_timeouts(unsigned long long *n);
 cudaError_t team_wait_timeouts(unsigned long long *n);
 
+Record *&current_record()
+{
+    static thread_local Record *r = nullptr;
+    return r;
+}
+
+fsdp_status Record::add(const char *fmt, ...)
+{
+    char line[256];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(line, sizeof line, fmt, ap);
+    va_end(ap);
+    text += line;
+    text += '\n';
+    return FSDP_OK;
+}
+
 int device_sms(int dev)
 {
+    if (const Record *r = current_record())
+        return r->sms;
     static std::mutex mu;
     static std::unordered_map<int, int> known;
     std::lock_guard<std::mutex> lk(mu);
@@ -226,6 +249,29 @@ fsdp_status check_iteration(const char *fn, int steps, double eps, double a, dou
     if (!(std::isfinite(eps) && eps >= 0) || !std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c))
         return set_error(FSDP_EINVAL, "%s: bad eps or coefficients", fn);
     return FSDP_OK;
+}
+
+// Runs f with a record set and hands the text out.
+template <class F>
+fsdp_status recorded(const char *fn, int sms, char *text, int64_t bytes, F f)
+{
+    if (sms < 1 || text == nullptr || bytes < 1)
+        return set_error(FSDP_EINVAL, "%s: bad sms or text", fn);
+    struct Set {
+        explicit Set(Record *r) { current_record() = r; }
+        ~Set() { current_record() = nullptr; }
+    };
+    Record r{sms, {}};
+    fsdp_status st;
+    {
+        const Set set(&r);
+        st = f();
+    }
+    if (st == FSDP_OK && (int64_t)r.text.size() >= bytes)
+        return set_error(FSDP_EINVAL, "%s: the text has %lld bytes", fn, (long long)r.text.size() + 1);
+    if (st == FSDP_OK)
+        memcpy(text, r.text.c_str(), r.text.size() + 1);
+    return st;
 }
 
 }  // namespace
@@ -498,6 +544,48 @@ fsdp_status fsdp_ops_wait_timeouts(int device, uint64_t *count)
         return set_error(FSDP_ECUDA, "%s: %s", fn, cudaGetErrorString(err));
     *count = n[0] + n[1] + n[2] + n[3];
     return FSDP_OK;
+}
+
+// Pointers are looked at for their alignment alone.
+fsdp_status fsdp_ops_plan_newton_schulz(int64_t batch, int64_t m, int64_t n, int ranks, int steps, int sms, char *text,
+                                        int64_t bytes)
+{
+    const char *fn = "fsdp_ops_plan_newton_schulz";
+    return guarded(fn, [&]() -> fsdp_status {
+        fsdp_status st = check_schulz(fn, batch, m, n);
+        if (st != FSDP_OK || (st = check_iteration(fn, steps, 1e-7, 0, 0, 0)) != FSDP_OK)
+            return st;
+        if (batch < 1 || ranks < 0 || (ranks > 0 && (batch > kMuonMaxMats || batch * ranks > kMuonMaxGrads)))
+            return set_error(FSDP_EINVAL, "%s: bad batch or ranks", fn);
+        SchulzArgs s{};
+        s.batch = batch, s.m = m, s.n = n, s.steps = steps;
+        s.a = 3.4445f, s.b = -4.7750f, s.c = 2.0315f;
+        s.ldg = s.ldo = n, s.g_stride = s.out_stride = m * n;
+        const std::vector<const void *> grads((size_t)(ranks > 0 ? batch * ranks : 1));
+        const std::vector<float *> state((size_t)batch);
+        if (ranks > 0)
+            s.grads = grads.data(), s.momentum = s.master = state.data(), s.R = ranks;
+        return recorded(fn, sms, text, bytes, [&] { return launch_newton_schulz(s, nullptr, 0, nullptr); });
+    });
+}
+
+fsdp_status fsdp_ops_plan_linear_cross_entropy(int64_t rows, int64_t cols, int64_t vocab, int with_gradients, int aligned,
+                                               int64_t piece_rows, int sms, char *text, int64_t bytes)
+{
+    const char *fn = "fsdp_ops_plan_linear_cross_entropy";
+    return guarded(fn, [&]() -> fsdp_status {
+        fsdp_status st = check_loss(fn, rows, cols, vocab, piece_rows);
+        if (st != FSDP_OK)
+            return st;
+        if (rows < 1)
+            return set_error(FSDP_EINVAL, "%s: no rows", fn);
+        LossArgs a{};
+        a.rows = rows, a.cols = cols, a.vocab = vocab, a.piece_rows = piece_rows;
+        a.ldh = a.ldw = a.lddh = a.lddw = aligned ? ceil_to(cols, 8) : cols | 1;
+        if (with_gradients)
+            a.dhidden = a.dweight = reinterpret_cast<void *>(uintptr_t(256));
+        return recorded(fn, sms, text, bytes, [&] { return launch_linear_cross_entropy(a, nullptr, 0, nullptr); });
+    });
 }
 
 }  // extern "C"

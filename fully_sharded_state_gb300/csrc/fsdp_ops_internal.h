@@ -4,11 +4,22 @@
 #pragma once
 
 #include <cstdint>
+#include <string>
 
 #include "fsdp_internal.h"
 #include "fsdp_ops.h"
 
 namespace fsdp {
+
+// What a call would launch, one line per launch, written instead of launched
+// where a thread has one set: the tests ask so which kernels a call takes, on
+// the host and for any number of multiprocessors.
+struct Record {
+    int sms;
+    std::string text;
+    fsdp_status add(const char *fmt, ...) __attribute__((format(printf, 2, 3)));
+};
+Record *&current_record();  // this thread's, or NULL
 
 // Multiprocessors of `dev`, read once per device.
 int device_sms(int dev);
@@ -108,5 +119,15 @@ struct SchulzArgs {
 };
 int64_t schulz_workspace(int64_t batch, int64_t m, int64_t n, bool muon);  // bytes
 fsdp_status launch_newton_schulz(const SchulzArgs &a, void *workspace, int dev, void *stream);
+
+// The launches of a call of these sizes on `sms` multiprocessors, as text (at
+// most `bytes` of it, its end included). ranks > 0: a Muon step. aligned: the
+// caller's matrices start on 16 bytes and so do their rows.
+extern "C" {
+fsdp_status fsdp_ops_plan_newton_schulz(int64_t batch, int64_t m, int64_t n, int ranks, int steps, int sms, char *text,
+                                        int64_t bytes);
+fsdp_status fsdp_ops_plan_linear_cross_entropy(int64_t rows, int64_t cols, int64_t vocab, int with_gradients, int aligned,
+                                               int64_t piece_rows, int sms, char *text, int64_t bytes);
+}
 
 }  // namespace fsdp

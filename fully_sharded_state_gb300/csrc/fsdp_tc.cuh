@@ -258,7 +258,7 @@ struct Shape {
     int splits;       // parts of K, each its own tile (its results are partial
                       // sums): at most so many, chosen by Tiles on the device
     int *splits_out;  // where the number is left, or NULL
-    int tn;           // columns of a tile, a multiple of 16, at most TN
+    int tn;           // columns of a tile, at most TN; a multiple of 16, of 32 for a pair of CTAs
     int whole_units;  // tiles' columns are multiples of 64
     int epi_bytes;    // what the epilogue moves per element, for the choice of the tile
     int sym;          // only the squares on and above the diagonal (M = N)
@@ -981,6 +981,11 @@ fsdp_status product_as(Shape s, const Operand &a, const Operand &b, bool bf16, c
                        const Operand *const *own, int64_t tiles, int dev, cudaStream_t stream, const char *what)
 {
     using R = Ring<kCtas, TN, Epi::kStages>;
+    if (s.tn < 1 || s.tn > TN || s.tn % (16 * kCtas) != 0)
+        return set_error(FSDP_EUNSUPPORTED, "%s: tiles of %d columns", what, s.tn);
+    if (Record *r = current_record())
+        return r->add("%s: product ctas %d tile %d columns %d tiles %lld sym %d splits %d stages %d parts %d", what, kCtas, TN,
+                      s.tn, (long long)tiles, s.sym, s.splits, Epi::kStages, Epi::kPromote);
     auto kernel = product_kernel<kCtas, TN, kAMN, kBMN, Epi>;
     static std::atomic<uint64_t> ready{0};  // devices (of the first 64) whose attribute is set
     const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
@@ -1049,7 +1054,9 @@ inline Form best_form(const Shape &s, int64_t sms, int least_tn)
         if (f[1] < least_tn)
             continue;
         const int64_t across = (s.N + f[1] - 1) / f[1];
-        const int columns = s.square || least_tn == 256 ? f[1] : (int)ceil_to((s.N + across - 1) / across, s.whole_units ? 64 : 16);
+        // N of an MMA goes in steps of 16 with the 128 rows of one CTA, of 32 with the 256 of a pair
+        const int step = s.whole_units ? 64 : 16 * f[0];
+        const int columns = s.square || least_tn == 256 ? f[1] : (int)ceil_to((s.N + across - 1) / across, step);
         Form g{f[0], f[1], columns, count_tiles(s, kTM * f[0], f[1]), 0};
         const int64_t slots = sms / g.ctas < 1 ? 1 : sms / g.ctas, waves = (g.tiles + slots - 1) / slots;
         const int64_t mma = nk * block_clocks(g.ctas, columns), epi = 1000 + kTM * columns * s.epi_bytes / 35;

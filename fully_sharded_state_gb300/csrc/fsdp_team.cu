@@ -586,6 +586,9 @@ fsdp_status launch_team(const SchulzArgs &a, void *workspace, int dev, void *str
         low = reinterpret_cast<uintptr_t>(a.g) | (uintptr_t)((a.ldg | a.g_stride) * (p.bf16 ? 2 : 4));
     }
     p.vec = (low & 7u) == 0;
+    if (Record *r = current_record())
+        return r->add("%s: team tile %d size %d teams %d rounds %d", muon ? "muon" : "newton_schulz", f.tn, f.tiles, f.teams,
+                      (p.batch + f.teams - 1) / f.teams);
     CUtensorMap maps[4];
     const Operand ops[4] = {{q.x16[0], a.n, a.m, q.ldx, p.xs},
                             {q.x16[1], a.n, a.m, q.ldx, p.xs},

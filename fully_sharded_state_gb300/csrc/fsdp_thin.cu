@@ -348,7 +348,7 @@ fsdp_status launch_thin(const SchulzArgs &a, void *workspace, int dev, void *str
     }
     auto kernel = muon ? thin_kernel<true> : thin_kernel<false>;
     const size_t smem = (size_t)rows * p.pitch * sizeof(float);
-    if (smem > 16 * 1024) {  // with the 31 KB of its own, past what needs no leave
+    if (smem > 16 * 1024 && !current_record()) {  // with the 31 KB of its own, past what needs no leave
         const cudaError_t err =
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kThinFloats * (int)sizeof(float));
         if (err != cudaSuccess)
