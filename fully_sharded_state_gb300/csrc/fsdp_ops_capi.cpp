@@ -54,8 +54,10 @@ int device_sms(int dev)
 
 namespace {
 
-// Sizes whose coordinates the tensor maps and kernels hold in 32 bits.
-constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1024;
+// Sizes whose coordinates the tensor maps and kernels hold in 32 bits, with
+// room for what a loop's last step reaches past them (the loss's pass over the
+// rows: four steps of 2048 columns, and segments rounded up by 8 columns each).
+constexpr int64_t kMaxDim = (int64_t(1) << 31) - (1 << 16);
 constexpr int64_t kMaxElems = int64_t(1) << 40;
 
 int64_t esize(fsdp_dtype d) { return d == FSDP_BF16 ? 2 : 4; }

@@ -331,7 +331,7 @@ struct Tiles {
             const int per = (blocks + n - 1) / n;
             n = (blocks + per - 1) / per;
             const int waves = (base * n + slots - 1) / slots;
-            const float t = (float)waves * (float)(per * per_block + 4000) + (float)n * join;
+            const float t = (float)waves * (float)((int64_t)per * per_block + 4000) + (float)n * join;
             if (w == 1 || t < best) {
                 best = t;
                 chosen = n;

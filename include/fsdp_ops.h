@@ -13,6 +13,8 @@
  * fsdp_last_error these calls share):
  *  - Matrices are row-major with a row stride in elements (ld >= columns);
  *    the elements of a row are adjacent.
+ *  - Rows, columns and vocabulary are at most 2^31 - 65536 each, and matrices
+ *    have at most 2^40 elements (FSDP_ERANGE above).
  *  - Pointers need the alignment of their element only; 16-byte aligned
  *    bases and strides take the vector and tensor-copy paths directly, others
  *    go through scalar accesses or one packing copy.
