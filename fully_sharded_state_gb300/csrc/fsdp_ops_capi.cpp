@@ -59,6 +59,9 @@ namespace {
 // rows: four steps of 2048 columns, and segments rounded up by 8 columns each).
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - (1 << 16);
 constexpr int64_t kMaxElems = int64_t(1) << 40;
+// Elements from the first to the last of a matrix, gaps included: with the
+// batch's (65,535 strides of at most kMaxElems) their bytes stay in int64.
+constexpr int64_t kMaxRange = int64_t(1) << 56;
 
 int64_t esize(fsdp_dtype d) { return d == FSDP_BF16 ? 2 : 4; }
 bool known(fsdp_dtype d) { return d == FSDP_F32 || d == FSDP_BF16; }
@@ -81,6 +84,8 @@ class Buffers {
             fail(FSDP_EALIGN, what, index, "is not aligned to its element");
         else if (ld < cols || ld > kMaxElems)
             fail(FSDP_EINVAL, what, index, "has a row stride below its columns");
+        else if (rows - 1 > kMaxRange / ld)
+            fail(FSDP_ERANGE, what, index, "has a range that is too large");
         else if (batch > 1 && (stride < (rows - 1) * ld + cols || stride > kMaxElems))
             fail(FSDP_EINVAL, what, index, "has a batch stride below its matrices");
         else {

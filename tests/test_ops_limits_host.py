@@ -42,3 +42,29 @@ def test_every_size_has_the_limit(lib, query, sizes):
         assert getattr(lib, query)(*at(MOST), ctypes.byref(n)) == capi.FSDP_OK
         assert getattr(lib, query)(*at(MOST + 1), ctypes.byref(n)) == capi.FSDP_ERANGE
         assert b"too large" in lib.fsdp_last_error()
+
+
+BASE, MB = 1 << 40, 1 << 20
+
+
+def at(k):
+    return BASE + k * 64 * MB
+
+
+@pytest.mark.parametrize("rows,ld", [(1 << 24, 1 << 40), (1 << 25, 1 << 39), ((1 << 30) + 1, (1 << 34) + 64), (MOST, 1 << 40)])
+@pytest.mark.parametrize("which", ["x", "y"])
+def test_row_strides_whose_ranges_wrap(lib, rows, ld, which):
+    """rows * ld elements past 2^63 would come out as a small or negative range,
+    which nothing overlaps."""
+    ldx, ldy = (ld, 64) if which == "x" else (64, ld)
+    # the other matrix is small enough to be named after this one
+    args = [rows, 64, at(0), ldx, 1, at(1 << 20), None, 1, 1e-5, at(1 << 21), ldy, None, None, None]
+    assert lib.fsdp_layer_norm(*args) == capi.FSDP_ERANGE
+    assert f"{which} ".encode() in lib.fsdp_last_error() and b"too large" in lib.fsdp_last_error()
+
+
+def test_batch_strides_whose_ranges_wrap(lib):
+    rows, ld = 1 << 24, 1 << 40
+    st = lib.fsdp_newton_schulz(2, rows, 8, at(0), ld, 8 * rows, 1, at(1), 8, 8 * rows, 5, 1e-7, 3.0, -4.0, 2.0, at(2), 64 * MB,
+                                None)
+    assert st == capi.FSDP_ERANGE and b"g " in lib.fsdp_last_error()
