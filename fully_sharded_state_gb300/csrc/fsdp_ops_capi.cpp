@@ -66,6 +66,10 @@ constexpr int64_t kMaxRange = int64_t(1) << 56;
 int64_t esize(fsdp_dtype d) { return d == FSDP_BF16 ? 2 : 4; }
 bool known(fsdp_dtype d) { return d == FSDP_F32 || d == FSDP_BF16; }
 
+// Whether fp32, in which the kernels take the numbers, holds v: finite, and 0
+// only for 0.
+bool in_f32(double v) { return std::isfinite((float)v) && ((float)v != 0.0f || v == 0.0); }
+
 // One call's buffers: each is checked as it is named, the rest in done().
 class Buffers {
   public:
@@ -253,7 +257,7 @@ fsdp_status check_iteration(const char *fn, int steps, double eps, double a, dou
 {
     if (steps < 0 || steps > 64)
         return set_error(FSDP_EINVAL, "%s: steps = %d outside [0, 64]", fn, steps);
-    if (!(std::isfinite(eps) && eps >= 0) || !std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c))
+    if (!(in_f32(eps) && eps >= 0) || !std::isfinite((float)a) || !std::isfinite((float)b) || !std::isfinite((float)c))
         return set_error(FSDP_EINVAL, "%s: bad eps or coefficients", fn);
     return FSDP_OK;
 }
@@ -297,8 +301,8 @@ fsdp_status fsdp_layer_norm(int64_t rows, int64_t cols, const void *x, int64_t l
         fsdp_status st = check_norm(fn, rows, cols, dtype, param_dtype);
         if (st != FSDP_OK)
             return st;
-        if (!(std::isfinite(eps) && eps > 0))
-            return set_error(FSDP_EINVAL, "%s: eps = %g, must be above 0", fn, eps);
+        if (!(in_f32(eps) && eps > 0))
+            return set_error(FSDP_EINVAL, "%s: eps = %g, must be above 0 and an fp32 number", fn, eps);
         if ((mean == nullptr) != (rstd == nullptr))
             return set_error(FSDP_EINVAL, "%s: mean and rstd are given together", fn);
         if (rows == 0)
@@ -494,8 +498,10 @@ fsdp_status fsdp_muon(int n_mats, int64_t m, int64_t n, int R, const void *const
             return set_error(FSDP_EINVAL, "%s: hp is NULL", fn);
         if ((st = check_iteration(fn, hp->steps, hp->eps, hp->a, hp->b, hp->c)) != FSDP_OK)
             return st;
-        if (!(std::isfinite(hp->lr) && hp->lr >= 0) || !(hp->momentum >= 0 && hp->momentum < 1) ||
-            !std::isfinite(hp->weight_decay) || !(std::isfinite(hp->update_scale) && hp->update_scale > 0))
+        if (!(std::isfinite(hp->lr) && hp->lr >= 0) || !(hp->momentum >= 0 && (float)hp->momentum < 1) ||
+            !std::isfinite(hp->weight_decay) || !(std::isfinite(hp->update_scale) && hp->update_scale > 0) ||
+            !std::isfinite((float)(hp->lr * hp->update_scale)) ||
+            !std::isfinite((float)(1.0 - hp->lr * hp->weight_decay)))
             return set_error(FSDP_EINVAL, "%s: bad hyper-parameters", fn);
         if (!known(grad_dtype))
             return set_error(FSDP_EUNSUPPORTED, "%s: unsupported dtype", fn);

@@ -15,6 +15,8 @@
  *    the elements of a row are adjacent.
  *  - Rows, columns and vocabulary are at most 2^31 - 65536 each, and matrices
  *    have at most 2^40 elements (FSDP_ERANGE above).
+ *  - Numbers are doubles that the kernels take as fp32: one that fp32 cannot
+ *    hold (infinite in it, or an eps that is 0 in it) is FSDP_EINVAL.
  *  - Pointers need the alignment of their element only; 16-byte aligned
  *    bases and strides take the vector and tensor-copy paths directly, others
  *    go through scalar accesses or one packing copy.
