@@ -667,18 +667,17 @@ Plan plan_of(const LossArgs &a, bool grad, void *base, bool with_weight)
 {
     Plan q{};
     q.lde = ceil_to(a.vocab, 64);  // whole lines
+    q.stat_pieces = (int)((a.vocab + kPieceCols - 1) / kPieceCols);
     int64_t piece = a.piece_rows;
     if (piece <= 0) {
-        piece = (int64_t(1) << 31) / (2 * q.lde);
+        // 2 GiB of what is kept of a piece's rows: the exponentials, or without gradients the statistics
+        piece = (int64_t(1) << 31) / (grad ? 2 * q.lde : (int64_t)sizeof(float2) * q.stat_pieces);
         piece = piece / 256 * 256;
     }
-    if (!grad)
-        piece = a.rows;  // nothing of a piece's size is kept
     piece = ceil_to(piece < 1 ? 1 : piece, 64);
     q.piece = piece < a.rows ? piece : a.rows;
     q.pieces = a.rows ? (a.rows + q.piece - 1) / q.piece : 0;
     q.ldx = ceil_to(a.cols, 16);
-    q.stat_pieces = (int)((a.vocab + kPieceCols - 1) / kPieceCols);
     // dhidden sums over the vocabulary. Where its 256-row tiles are few, the
     // sum may be cut in parts (Tiles::choose_splits), which are then joined.
     const int64_t tiles = (q.piece + 255) / 256 * ((a.cols + 255) / 256);

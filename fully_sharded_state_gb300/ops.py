@@ -209,11 +209,14 @@ def _loss_call(hidden, weight, targets, ignore_index, reduction, grad, grad_scal
     return loss, row_loss, dhidden, dweight
 
 
-def linear_cross_entropy(hidden, weight, targets, ignore_index: int = -100, reduction: str = "mean", stream=None):
+def linear_cross_entropy(hidden, weight, targets, ignore_index: int = -100, reduction: str = "mean", stream=None,
+                         piece_rows: int = 0):
     """Cross entropy of ``hidden`` [rows, cols] @ ``weight`` [vocab, cols]^T
     against ``targets`` (int64), without the logits: (loss, row_loss), fp32.
-    Rows whose target is ``ignore_index`` count for nothing."""
-    return _loss_call(hidden, weight, targets, ignore_index, reduction, False, 1.0, None, None, 0, stream)[:2]
+    Rows whose target is ``ignore_index`` count for nothing. ``piece_rows`` as
+    in ``linear_cross_entropy_grad``."""
+    return _loss_call(hidden, weight, targets, ignore_index, reduction, False, 1.0, None, None, int(piece_rows),
+                      stream)[:2]
 
 
 def linear_cross_entropy_grad(hidden, weight, targets, ignore_index: int = -100, reduction: str = "mean",

@@ -88,8 +88,9 @@ typedef enum { FSDP_MEAN = 0, FSDP_SUM = 1 } fsdp_reduction;
  * be a view of a unit's gradient buffer. loss [1], row_loss [rows]: fp32.
  * G is rounded to bf16 for its two products, which is where the gradients'
  * error comes from (2^-8 per element of G at most, beside their own rounding).
- * The rows are taken in pieces of piece_rows (0: as many as keep a piece's
- * 16-bit exponentials at 2 GiB); within a piece the softmax is formed from
+ * The rows are taken in pieces of piece_rows, rounded up to 64 (0: as many as
+ * keep a piece's 16-bit exponentials, or without gradients its statistics of 8
+ * bytes per 128 words, at 2 GiB); within a piece the softmax is formed from
  * tiles of the vocabulary, each with its own maximum and sum. */
 fsdp_status fsdp_linear_cross_entropy(int64_t rows, int64_t cols, int64_t vocab,
                                       const void *hidden, int64_t ldh, const void *weight,

@@ -68,3 +68,20 @@ def test_batch_strides_whose_ranges_wrap(lib):
     st = lib.fsdp_newton_schulz(2, rows, 8, at(0), ld, 8 * rows, 1, at(1), 8, 8 * rows, 5, 1e-7, 3.0, -4.0, 2.0, at(2), 64 * MB,
                                 None)
     assert st == capi.FSDP_ERANGE and b"g " in lib.fsdp_last_error()
+
+
+def test_the_loss_alone_keeps_to_its_pieces(lib):
+    """What it keeps of a row, 8 bytes per 128 words, is bounded as the
+    exponentials are: by 2 GiB, or by piece_rows."""
+    n = ctypes.c_int64(0)
+
+    def ask(rows, piece, grad=0, cols=64, vocab=200000):
+        assert lib.fsdp_linear_cross_entropy_workspace(rows, cols, vocab, grad, 1, piece, ctypes.byref(n)) == capi.FSDP_OK
+        return n.value
+
+    own = lambda rows: rows * (64 * 2 + 4 + 4 + 4) + 4096  # noqa: E731  # hidden's copy, source, target, its logit
+    for rows in (1 << 18, 1 << 20, 1 << 22):
+        assert ask(rows, 0) <= (1 << 31) + own(rows)
+        assert ask(rows, 1024) <= 1024 * 1563 * 8 + own(rows)
+    assert ask(100, 0) <= 100 * 1563 * 8 + own(128)
+    assert ask(1 << 18, 1024) < ask(1 << 18, 4096) < ask(1 << 18, 0)
