@@ -5,7 +5,8 @@ outputs can be views of a unit's full gradient buffers; ``newton_schulz`` and
 ``muon_step``, the matrix-aware update that uses them. Each function checks
 its tensors, allocates its outputs and workspace with torch on the stream
 that the kernels run on, and makes one call of the CUDA library (C ABI in
-``include/fsdp_ops.h``, where the formulas are). Nothing synchronises.
+``include/fsdp_ops.h``, where the formulas are); ``muon_step`` makes one per
+shape, after all of its checks. Nothing synchronises.
 
 Tensors are CUDA tensors of one device whose rows' elements are adjacent
 (``stride(-1) == 1``); rows may be further apart. ``stream`` defaults to the
@@ -330,13 +331,39 @@ def muon_step(grads, master, momentum, params, hp: MuonHP, stream=None) -> None:
             ma = (_vp * k)(*[ptr(master[i], m, n, torch.float32, "master", i) for i in part])
             po = None if params is None else (_vp * k)(*[ptr(params[i], m, n, torch.bfloat16, "params", i)
                                                          for i in part])
-            calls.append((k, m, n, R, g, _DT[dt], mo, ma, po))
+            calls.append((part, m, n, R, g, dt, mo, ma, po))
+    if len(calls) > 1:
+        _apart(calls)  # one call sees to its own
+    # the workspace before the first launch, too; the calls follow one another in it
     handle, ctx = _on(stream, dev)
-    for k, m, n, R, g, dt, mo, ma, po in calls:
-        with ctx:
-            ws, nws = _workspace("fsdp_muon_workspace", k, m, n, device=dev)
+    nws = max(_workspace_bytes("fsdp_muon_workspace", len(part), m, n) for part, m, n, *_ in calls)
+    with ctx:
+        ws = torch.empty(nws or 1, dtype=torch.uint8, device=dev)
+    for part, m, n, R, g, dt, mo, ma, po in calls:
         c = hp._c(m, n)
-        capi._check(lib.fsdp_muon(k, m, n, R, g, dt, mo, ma, po, ctypes.byref(c), ws.data_ptr(), nws, handle))
+        capi._check(lib.fsdp_muon(len(part), m, n, R, g, _DT[dt], mo, ma, po, ctypes.byref(c), ws.data_ptr(), nws, handle))
+
+
+def _apart(calls):
+    """Refuses a matrix that is written and shares memory with another one, over
+    all calls of a step: what each call checks of its own matrices."""
+    spans = []
+    for part, m, n, R, g, dt, mo, ma, po in calls:
+        numel = m * n
+        spans += [(p, p + numel * dt.itemsize, False, "grads", part[j // R], j % R) for j, p in enumerate(g)]
+        for name, pointers, size in (("momentum", mo, 4), ("master", ma, 4), ("params", po or (), 2)):
+            spans += [(p, p + numel * size, True, name, part[j], None) for j, p in enumerate(pointers)]
+    spans.sort()
+    name = lambda s: f"{s[3]}[{s[4]}]" + ("" if s[5] is None else f"[{s[5]}]")  # noqa: E731
+    furthest = written = (0, 0)  # of all before, and of those that are written
+    for s in spans:
+        hit = furthest if s[2] else written
+        if s[0] < hit[1]:
+            _refuse(f"{name(s)} overlaps {name(hit)}")
+        if s[1] > furthest[1]:
+            furthest = s
+        if s[2] and s[1] > written[1]:
+            written = s
 
 
 def ops_wait_timeouts(device=None) -> int:
