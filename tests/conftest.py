@@ -27,3 +27,16 @@ def cuda_lib():
     from fully_sharded_state_gb300 import build, capi
     build.build()
     return capi.load()
+
+
+# modules whose GPU tests run the operators' kernels
+_OPERATORS = ("test_layer_norm", "test_linear_cross_entropy", "test_muon", "test_ops_path")
+
+
+@pytest.fixture(autouse=True)
+def no_wait_given_up(request):
+    """After every GPU test of the operators: no block gave up a wait."""
+    yield
+    if "gpu" in request.keywords and request.module.__name__.startswith(_OPERATORS) and "cuda_lib" in request.fixturenames:
+        from fully_sharded_state_gb300 import ops_wait_timeouts
+        assert ops_wait_timeouts() == 0
