@@ -111,13 +111,18 @@ __device__ __forceinline__ float diagonal_sum(const float (&v)[32], int lane)
 
 // S sums over the matrix's longer side. Where even its smallest tiles (128 x
 // 64) leave two thirds of the multiprocessors idle and that side is long, the
-// sum may be cut in parts (Tiles::choose_splits): 8 Muon steps of 7 x 13053,
-// with 8 tiles of 204 K blocks for each S, took 345 us whole and take 171 in
-// parts; 6 matrices of 3823 x 271, with 90 tiles, 226 whole and 262 in parts.
+// sum is cut in parts (Tiles::choose_splits). What that saves grows with the
+// longer side l, what joining the parts costs with the shorter one, k, so a sum
+// is cut from l = 56 k on. Five steps, in parts and whole, us: 8 x 13 x 6000 136
+// and 197, 4 x 24 x 14000 160 and 331, 1 x 128 x 14000 208 and 317, 1 x 400 x 40000
+// 532 and 890; below the bound 1 x 300 x 6001 292 and 201, 4 x 256 x 3000 240 and
+// 166. Over 332 shapes the worst that the rule does is a quarter (2 x 14000 x 300,
+// 349 in parts, which it does not take, and 433).
+constexpr int kSplitRatio = 56;
 inline int square_splits(int64_t k, int64_t l, int64_t batch)
 {
     const int64_t tiles = (k + 127) / 128 * ((k + 63) / 64) * batch, blocks = (l + kBK - 1) / kBK;
-    return tiles <= kSplitSms / 3 && blocks >= 32 ? (int)(blocks / 4) : 1;
+    return tiles <= kSplitSms / 3 && blocks >= 32 && l >= kSplitRatio * k ? (int)(blocks / 4) : 1;
 }
 
 // The workspace of one call.

@@ -32,7 +32,7 @@ CASES = [
     (400, 50, 60, 0),
     # a kernel per product: S in parts
     (8, 2606, 14, 0), (7, 2928, 12, 2), (6, 13, 2886, 0), (8, 14, 2493, 2), (20, 1810, 20, 2), (4, 137, 2820, 3),
-    (2, 2996, 210, 2),
+    (2, 2996, 210, 2), (2, 132, 7500, 0), (1, 7600, 133, 3), (2, 140, 8000, 2), (3, 9000, 135, 0),
     # S whole, squares and their mirror images, rows that start on 16 bytes and rows that do not
     (105, 159, 85, 0), (53, 270, 67, 3), (51, 137, 304, 0), (378, 67, 78, 0), (40, 206, 257, 2), (51, 316, 149, 0),
     (2, 811, 1297, 2), (40, 429, 209, 0), (2, 1335, 805, 0), (1, 2792, 841, 0), (5, 1053, 908, 3), (1, 859, 2942, 0),

@@ -46,3 +46,18 @@ def test_a_step_of_each_form():
     assert team["kind"] == "team" and team["what"] == "muon" and team["rounds"] == 1
     plan = ops_plan.newton_schulz(48, 512, 512, steps=2)
     assert [p["what"].split(" ", 1)[1] for p in plan] == ["(start)", "(scale)"] + ["(S)", "(P)", "(x)"] * 2
+
+
+def _in_parts(*case):
+    return any("S, parts" in p["what"] for p in ops_plan.newton_schulz(*case))
+
+
+def test_sums_are_cut_where_that_is_shorter():
+    """Times of five steps, in parts and whole, us: 1 x 300 x 6001 292 and 201,
+    4 x 256 x 3000 240 and 166, 1 x 400 x 6000 366 and 223, 8 x 160 x 2048 168 and
+    139; 8 x 33 x 14000 189 and 356, 1 x 128 x 14000 224 and 314, 1 x 400 x 40000 532
+    and 890."""
+    for case in ((1, 300, 6001), (1, 6001, 300), (4, 256, 3000), (4, 3000, 256), (1, 400, 6000), (8, 160, 2048), (8, 2048, 160)):
+        assert not _in_parts(*case), case
+    for case in ((20, 33, 6000), (8, 33, 14000), (1, 33, 40000), (1, 64, 14000), (1, 128, 14000), (1, 400, 40000), (1, 40000, 400)):
+        assert _in_parts(*case), case
