@@ -330,13 +330,15 @@ fsdp_status fsdp_layer_norm(int64_t rows, int64_t cols, const void *x, int64_t l
 fsdp_status fsdp_layer_norm_backward_workspace(int64_t rows, int64_t cols, int64_t *bytes)
 {
     const char *fn = "fsdp_layer_norm_backward_workspace";
-    if (bytes == nullptr)
-        return set_error(FSDP_EINVAL, "%s: bytes is NULL", fn);
-    fsdp_status st = check_norm(fn, rows, cols, FSDP_F32, FSDP_F32);
-    if (st != FSDP_OK)
-        return st;
-    *bytes = norm_backward_workspace(rows, cols);
-    return FSDP_OK;
+    return guarded(fn, [&]() -> fsdp_status {
+        if (bytes == nullptr)
+            return set_error(FSDP_EINVAL, "%s: bytes is NULL", fn);
+        fsdp_status st = check_norm(fn, rows, cols, FSDP_F32, FSDP_F32);
+        if (st != FSDP_OK)
+            return st;
+        *bytes = norm_backward_workspace(rows, cols);
+        return FSDP_OK;
+    });
 }
 
 fsdp_status fsdp_layer_norm_backward(int64_t rows, int64_t cols, const void *dy, int64_t lddy, const void *x,
@@ -375,15 +377,17 @@ fsdp_status fsdp_linear_cross_entropy_workspace(int64_t rows, int64_t cols, int6
                                                 int aligned_weight, int64_t piece_rows, int64_t *bytes)
 {
     const char *fn = "fsdp_linear_cross_entropy_workspace";
-    if (bytes == nullptr)
-        return set_error(FSDP_EINVAL, "%s: bytes is NULL", fn);
-    fsdp_status st = check_loss(fn, rows, cols, vocab, piece_rows);
-    if (st != FSDP_OK)
-        return st;
-    LossArgs a{};
-    a.rows = rows, a.cols = cols, a.vocab = vocab, a.piece_rows = piece_rows;
-    *bytes = loss_workspace(a, with_gradients != 0, aligned_weight != 0);
-    return FSDP_OK;
+    return guarded(fn, [&]() -> fsdp_status {
+        if (bytes == nullptr)
+            return set_error(FSDP_EINVAL, "%s: bytes is NULL", fn);
+        fsdp_status st = check_loss(fn, rows, cols, vocab, piece_rows);
+        if (st != FSDP_OK)
+            return st;
+        LossArgs a{};
+        a.rows = rows, a.cols = cols, a.vocab = vocab, a.piece_rows = piece_rows;
+        *bytes = loss_workspace(a, with_gradients != 0, aligned_weight != 0);
+        return FSDP_OK;
+    });
 }
 
 fsdp_status fsdp_linear_cross_entropy(int64_t rows, int64_t cols, int64_t vocab, const void *hidden, int64_t ldh,
@@ -429,13 +433,15 @@ fsdp_status fsdp_linear_cross_entropy(int64_t rows, int64_t cols, int64_t vocab,
 fsdp_status fsdp_newton_schulz_workspace(int64_t batch, int64_t m, int64_t n, int64_t *bytes)
 {
     const char *fn = "fsdp_newton_schulz_workspace";
-    if (bytes == nullptr)
-        return set_error(FSDP_EINVAL, "%s: bytes is NULL", fn);
-    fsdp_status st = check_schulz(fn, batch, m, n);
-    if (st != FSDP_OK)
-        return st;
-    *bytes = schulz_workspace(batch, m, n, false);
-    return FSDP_OK;
+    return guarded(fn, [&]() -> fsdp_status {
+        if (bytes == nullptr)
+            return set_error(FSDP_EINVAL, "%s: bytes is NULL", fn);
+        fsdp_status st = check_schulz(fn, batch, m, n);
+        if (st != FSDP_OK)
+            return st;
+        *bytes = schulz_workspace(batch, m, n, false);
+        return FSDP_OK;
+    });
 }
 
 fsdp_status fsdp_newton_schulz(int64_t batch, int64_t m, int64_t n, const void *g, int64_t ldg, int64_t batch_stride,
@@ -470,13 +476,15 @@ fsdp_status fsdp_newton_schulz(int64_t batch, int64_t m, int64_t n, const void *
 fsdp_status fsdp_muon_workspace(int n_mats, int64_t m, int64_t n, int64_t *bytes)
 {
     const char *fn = "fsdp_muon_workspace";
-    if (bytes == nullptr)
-        return set_error(FSDP_EINVAL, "%s: bytes is NULL", fn);
-    fsdp_status st = check_schulz(fn, n_mats, m, n);
-    if (st != FSDP_OK)
-        return st;
-    *bytes = schulz_workspace(n_mats, m, n, true);
-    return FSDP_OK;
+    return guarded(fn, [&]() -> fsdp_status {
+        if (bytes == nullptr)
+            return set_error(FSDP_EINVAL, "%s: bytes is NULL", fn);
+        fsdp_status st = check_schulz(fn, n_mats, m, n);
+        if (st != FSDP_OK)
+            return st;
+        *bytes = schulz_workspace(n_mats, m, n, true);
+        return FSDP_OK;
+    });
 }
 
 fsdp_status fsdp_muon(int n_mats, int64_t m, int64_t n, int R, const void *const *grads, fsdp_dtype grad_dtype,
@@ -533,30 +541,32 @@ fsdp_status fsdp_muon(int n_mats, int64_t m, int64_t n, int R, const void *const
 fsdp_status fsdp_ops_wait_timeouts(int device, uint64_t *count)
 {
     const char *fn = "fsdp_ops_wait_timeouts";
-    if (count == nullptr || device < 0)
-        return set_error(FSDP_EINVAL, "%s: count is NULL or device < 0", fn);
-    int prev = -1;
-    cudaError_t err = cudaGetDevice(&prev);
-    if (err != cudaSuccess)
-        return set_error(FSDP_ECUDA, "%s: cudaGetDevice: %s", fn, cudaGetErrorString(err));
-    if (prev != device && (err = cudaSetDevice(device)) != cudaSuccess)
-        return set_error(FSDP_ECUDA, "%s: cudaSetDevice(%d): %s", fn, device, cudaGetErrorString(err));
-    unsigned long long n[4] = {0, 0, 0, 0};
-    err = cudaDeviceSynchronize();
-    if (err == cudaSuccess)
-        err = norm_wait_timeouts(&n[0]);
-    if (err == cudaSuccess)
-        err = loss_wait_timeouts(&n[1]);
-    if (err == cudaSuccess)
-        err = muon_wait_timeouts(&n[2]);
-    if (err == cudaSuccess)
-        err = team_wait_timeouts(&n[3]);
-    if (prev != device)
-        cudaSetDevice(prev);
-    if (err != cudaSuccess)
-        return set_error(FSDP_ECUDA, "%s: %s", fn, cudaGetErrorString(err));
-    *count = n[0] + n[1] + n[2] + n[3];
-    return FSDP_OK;
+    return guarded(fn, [&]() -> fsdp_status {
+        if (count == nullptr || device < 0)
+            return set_error(FSDP_EINVAL, "%s: count is NULL or device < 0", fn);
+        int prev = -1;
+        cudaError_t err = cudaGetDevice(&prev);
+        if (err != cudaSuccess)
+            return set_error(FSDP_ECUDA, "%s: cudaGetDevice: %s", fn, cudaGetErrorString(err));
+        if (prev != device && (err = cudaSetDevice(device)) != cudaSuccess)
+            return set_error(FSDP_ECUDA, "%s: cudaSetDevice(%d): %s", fn, device, cudaGetErrorString(err));
+        unsigned long long n[4] = {0, 0, 0, 0};
+        err = cudaDeviceSynchronize();
+        if (err == cudaSuccess)
+            err = norm_wait_timeouts(&n[0]);
+        if (err == cudaSuccess)
+            err = loss_wait_timeouts(&n[1]);
+        if (err == cudaSuccess)
+            err = muon_wait_timeouts(&n[2]);
+        if (err == cudaSuccess)
+            err = team_wait_timeouts(&n[3]);
+        if (prev != device)
+            cudaSetDevice(prev);
+        if (err != cudaSuccess)
+            return set_error(FSDP_ECUDA, "%s: %s", fn, cudaGetErrorString(err));
+        *count = n[0] + n[1] + n[2] + n[3];
+        return FSDP_OK;
+    });
 }
 
 // Pointers are looked at for their alignment alone.

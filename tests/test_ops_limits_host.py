@@ -85,3 +85,19 @@ def test_the_loss_alone_keeps_to_its_pieces(lib):
         assert ask(rows, 1024) <= 1024 * 1563 * 8 + own(rows)
     assert ask(100, 0) <= 100 * 1563 * 8 + own(128)
     assert ask(1 << 18, 1024) < ask(1 << 18, 4096) < ask(1 << 18, 0)
+
+
+def test_every_entry_of_the_operators_is_guarded():
+    """What an entry calls may throw (set_error keeps a string): each runs its
+    body where exceptions are caught."""
+    import os
+    import re
+
+    source = open(os.path.join(build.CSRC, "fsdp_ops_capi.cpp")).read()
+    body = source[source.index('extern "C" {'):]
+    entries = re.split(r"^fsdp_status (?=fsdp_)", body, flags=re.M)[1:]
+    assert len(entries) >= 10
+    for e in entries:
+        name = e[:e.index("(")]
+        first = e[e.index("{") + 1:].split(";")[1].strip()
+        assert first.startswith("return guarded(fn, [&]()"), name
