@@ -24,7 +24,7 @@
 // kernels' starts and ends: 256 x 512 x 32000 in 59 us, of which the products'
 // flops are 13; the loss alone of one row in 25 us of the caller's time.
 // Weights and gradients whose rows do not start on 16 bytes cost a copy each
-// way: 1001 x 513 x 50021 with a third of the rows ignored 201 us, about 25 of
+// way: 1001 x 513 x 50021 with a third of the rows ignored 200 us, about 25 of
 // them the weight's copy and 10 the gradient's cut pieces.
 #include <math_constants.h>
 

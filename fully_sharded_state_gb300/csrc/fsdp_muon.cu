@@ -22,16 +22,16 @@
 // as well, and lo = fp16(2048 (x - hi)). Beside fp32 it saves a fifth of the
 // last product's traffic, and both move by bulk copies through the warps'
 // stages, so that no thread loads or stores them: that epilogue was bound by
-// shared memory and L1, which the MMAs' operands use as well (48 x 512 x 512:
-// 365 us with the fp32 x, 324 so).
+// shared memory and L1, which the MMAs' operands use as well (the change took
+// 48 x 512 x 512 from 365 to 324 us).
 //
 // What bounds it. Small matrices: the epilogues. Five steps of 48 x 512 x 512
-// are 303 us, of which the tensor cores are busy for a third; each epilogue
+// are 302 to 310 us, of which the tensor cores are busy for a third; each epilogue
 // waits for its first unit and its accumulator in turn, and 192 tiles are 2.5
 // waves of the 76 CTA pairs. Few small matrices: latency, see the team kernel.
 // Large ones: the tensor cores. A Muon step of 14336 x 4096 over 8 ranks is
-// 3.0 ms, 4.0 TFLOP and a first pass of 1.8 GB: 1,330 TFLOP/s in all, at the
-// clock that the power limit leaves.
+// 3.0 to 3.1 ms, 4.0 TFLOP and a first pass of 1.8 GB: 1,290 to 1,310 TFLOP/s in
+// all, at the clock that the power limit leaves.
 #include "fsdp_muon.cuh"
 
 namespace fsdp {
@@ -348,8 +348,8 @@ struct StepParams {
 //
 // kSlots: units of hi and lo that a warp has under way. Two take 64 KB from
 // the operands' ring, which a long K needs: taken where the epilogue is the
-// longer part. One and two: 48 x 512 x 512 316 and 307 us, 16 x 768 x 768 273
-// and 265, 16 x 1024 x 1024 473 and 495, 4096 x 14336 2,612 and 2,867.
+// longer part. One and two: 48 x 512 x 512 312 and 304 us, 16 x 768 x 768 267
+// and 261, 16 x 1024 x 1024 472 and 494, 4096 x 14336 2,480 and 2,785.
 constexpr int kShortK = 768;
 template <Then kThen, int kSlots = 1>
 struct StepEpi : EpiDefaults {
@@ -518,8 +518,9 @@ fsdp_status launch_newton_schulz(const SchulzArgs &a, void *workspace, int dev, 
     const int64_t other = team >= 0 && team < products ? team : products;
     // preferred up to twice the other's estimate, for the sake of fp32: with
     // few rows, fp16 operands leave a nearly low-rank result 8e-3 off (5 x
-    // 30011). Measured, that is a third slower at most (8 x 8192 transposed,
-    // 139 us against 110)
+    // 30011). Where the other is shorter, that costs up to 1.8 times its time
+    // (us, here and there: 2 x 6000 x 13 198 and 110, 8 x 24 x 2048 148 and 97,
+    // 2 x 8 x 14000 172 and 129)
     if (thin >= 0 && thin < 2 * other)
         return launch_thin(a, workspace, dev, stream);
     if (other == team)

@@ -30,8 +30,11 @@
  *    bytes that the operator's _workspace query returns, 256-byte aligned.
  *    It may be reused as soon as the call's work on the stream is done, and
  *    holds nothing that a later call needs.
- *  - Sums, statistics and products accumulate in fp32 or wider, in an order
- *    that depends on the sizes alone: the same inputs give the same bits.
+ *  - Sums, statistics and products accumulate in fp32 or wider. Their order is
+ *    fixed by the sizes, by whether rows start on 16 bytes, by the device's
+ *    number of multiprocessors and, for the loss, by the number of rows that
+ *    count: the same call gives the same bits every time. The same values in
+ *    buffers of another alignment may be summed in another order.
  *  - No kernel traps. The matrix kernels wait on their own copies and on the
  *    tensor core; a wait that lasts ~2 s is given up, the block counts itself
  *    (fsdp_ops_wait_timeouts) and its outputs are invalid.
@@ -110,9 +113,15 @@ fsdp_status fsdp_linear_cross_entropy_workspace(int64_t rows, int64_t cols, int6
  *   x = g / (||g||_F + eps);  `steps` times:
  *     S = x x^T (m <= n) or x^T x;  P = b S + c S^2;  x = a x + P x (or x P)
  *   out = x
- * g: bf16 or fp32; out [batch, m, n]: bf16. The products' operands are fp16,
- * their sums fp32, and x itself is carried in fp32. steps in [0, 64].
- * ||g||_F has to be below 1.8e19 (its square is an fp32 number). */
+ * g: bf16 or fp32; out [batch, m, n]: bf16. steps in [0, 64].
+ * The sizes and the device choose one of three forms. For a shorter side of at
+ * most 32 there is one of fp32 throughout. In the others the products' operands
+ * x, S and P are fp16, their sums fp32, and x is carried from step to step in
+ * fp32 (few small matrices) or as two fp16 numbers, which is 22 bits, or 2^-36
+ * where that is more (many or large ones). Coefficients with which an element
+ * of x, S or P passes 65504 give infinities there.
+ * ||g||_F has to be below 1.8e19, and below 1e-19 it counts as 0 beside eps (its
+ * square is an fp32 number). */
 fsdp_status fsdp_newton_schulz(int64_t batch, int64_t m, int64_t n, const void *g, int64_t ldg,
                                int64_t batch_stride, fsdp_dtype dtype, void *out, int64_t ldo,
                                int64_t out_batch_stride, int steps, double eps, double a, double b,
