@@ -287,7 +287,8 @@ __device__ __forceinline__ PolicyRow policy_row(const TuneParams &p, float now, 
     const Two l = difference(old, now);
     r.cut = a > 0.0f ? above(l, p.log_high) : a < 0.0f && above(p.log_low, l);
     if (a != 0.0f) {
-        const float e = expf(l.hi), ratio = l.lo == 0.0f ? e : fmaf(e, l.lo, e);
+        // what rounding l left; an infinite e has none of it (inf - inf where it is below 0)
+        const float e = expf(l.hi), ratio = e < CUDART_INF_F ? fmaf(e, l.lo, e) : e;
         r.term = -(r.cut ? (a > 0.0f ? p.high : p.low) : ratio) * a;
         r.slope = r.cut ? 0.0f : ratio * a;
     }

@@ -1,0 +1,37 @@
+"""The policy loss where exp leaves fp32: rows whose log ratio or whose distance
+from the reference model passes 88.7, or is infinite.
+
+Tolerances, in units of 2^-24 (half a step): exp is good to 2 steps, of which a
+far row takes two (8 units); the factors between them, the ratio's remainder and
+the share of a row are a rounding each (6), and a lane's sum of 8 rows 8 more.
+The distance from the reference model is rounded before its exponential is taken,
+which is |d| units of that."""
+import pytest
+import torch
+
+from ops_reference import F32_U
+from fully_sharded_state_gb300 import policy_loss
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+ROWS = [64, 20000]  # one block; chunks
+
+
+def _rand(rows, seed, lo=0.0, hi=1.0):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.rand(rows, device="cuda", generator=gen) * (hi - lo) + lo
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+def test_ratios_that_overflow_with_a_remainder(cuda_lib, rows, sign):
+    """old - now is not an fp32 number, and off it to either side."""
+    now, old = _rand(rows, 1), _rand(rows, 2, 95.0, 140.0)
+    rest = (old.double() - now.double()) - (old - now).double()
+    assert (rest < 0).any() and (rest > 0).any()
+    loss, weights, _, clipped = policy_loss(now, old, torch.full_like(now, sign))
+    if sign < 0:
+        assert loss.item() == INF and (weights == -INF).all() and clipped.item() == 0
+    else:
+        assert abs(loss.item() + 1.2) < 1e-5 and (weights == 0).all() and clipped.item() == 1
