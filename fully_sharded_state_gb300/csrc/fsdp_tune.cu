@@ -295,8 +295,10 @@ __device__ __forceinline__ PolicyRow policy_row(const TuneParams &p, float now, 
     if (p.ref) {
         const float d = now - ref, g = expm1f(d);
         r.kl = kl_of(d, g);
-        r.term = fmaf(p.kl_coef, r.kl, r.term);
-        r.slope = fmaf(p.kl_coef, g, r.slope);
+        if (p.kl_coef != 0.0f) {  // else the KL is only watched: 0 times an infinite one is no part of the loss
+            r.term = fmaf(p.kl_coef, r.kl, r.term);
+            r.slope = fmaf(p.kl_coef, g, r.slope);
+        }
     }
     return r;
 }

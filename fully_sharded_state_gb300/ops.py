@@ -438,7 +438,8 @@ def policy_loss(row_loss, old_row_loss, advantages, offsets=None, ref_row_loss=N
     ``reduction``: the mean over rows, their "sum", or "sequence", the mean over
     sequences of their means. ``mask`` (bool): the rows that count.
     ``row_weights`` is the gradient with respect to ``row_loss``; kl and clipped
-    are the KL estimate's mean and the share of clipped rows."""
+    are the KL estimate's mean and the share of clipped rows. With ``kl_coef`` 0
+    a reference is watched by ``kl`` alone."""
     lib = capi.load()
     rows, dev, (pq, pr), po, pm = _tuning_inputs(
         row_loss, (("old_row_loss", old_row_loss), ("ref_row_loss", ref_row_loss)), offsets, mask)

@@ -209,12 +209,13 @@ typedef enum { FSDP_POLICY_MEAN = 0, FSDP_POLICY_SUM = 1, FSDP_POLICY_SEQUENCE =
  * l = old_row_loss - row_loss, A its advantage and d = row_loss - ref_row_loss:
  *   term = -min(exp(l) A, clip(exp(l), 1 - clip_low, 1 + clip_high) A)
  *          + kl_coef (exp(d) - 1 - d)
- * (A = 0: the KL term alone; ref_row_loss NULL: without it; a ratio at a
- * border is not clipped, on which side one is being decided without l's
- * rounding). loss is the terms' mean over the rows that count, their sum, or
- * the mean over the sequences with such rows of their means. sequences and
- * offsets [sequences + 1] int64 may be 0 and NULL: then all rows are one's,
- * and the last reduction is refused. advantages: [rows], or [sequences] where
+ * (A = 0: the KL term alone; ref_row_loss NULL or kl_coef 0: without it,
+ * infinite or not; a ratio at a border is not clipped, on which side one is
+ * being decided without l's rounding). loss is the terms' mean over the rows
+ * that count, their sum, or the mean over the sequences with such rows of their
+ * means. sequences and offsets [sequences + 1] int64 may be 0 and NULL: then
+ * all rows are one's, and the last reduction is refused. advantages: [rows], or
+ * [sequences] where
  * by_sequence is not 0. kl, clipped [1], fp32: the mean of exp(d) - 1 - d and
  * the share of clipped rows, both over the rows that count. */
 fsdp_status fsdp_policy_loss(int64_t rows, int64_t sequences, const float *row_loss,

@@ -35,3 +35,18 @@ def test_ratios_that_overflow_with_a_remainder(cuda_lib, rows, sign):
         assert loss.item() == INF and (weights == -INF).all() and clipped.item() == 0
     else:
         assert abs(loss.item() + 1.2) < 1e-5 and (weights == 0).all() and clipped.item() == 1
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("far", [99.5, INF])
+def test_without_a_coefficient_the_reference_changes_neither_loss_nor_weights(cuda_lib, rows, far):
+    now, old, ref = _rand(rows, 3, 0.0, 4.0), _rand(rows, 4, 0.0, 4.0), _rand(rows, 5, 0.0, 4.0)
+    now[5::7] = far
+    a = _rand(rows, 6, -1.0, 1.0)
+    offsets = torch.tensor([0, rows // 3, rows], device="cuda")
+    for reduction in ("mean", "sum", "sequence"):
+        alone = policy_loss(now, old, a, offsets=offsets, reduction=reduction)
+        watched = policy_loss(now, old, a, offsets=offsets, reduction=reduction, ref_row_loss=ref)
+        assert alone[0].isfinite() and alone[1].isfinite().all()
+        assert torch.equal(alone[0], watched[0]) and torch.equal(alone[1], watched[1])
+        assert torch.equal(alone[3], watched[3]) and not watched[2].isfinite()
