@@ -265,7 +265,7 @@ __device__ __forceinline__ Pair pair_of(const TuneParams &p, Two sg, Two sp, int
 __device__ __forceinline__ float kl_of(float d, float expm1_d)
 {
     if (fabsf(d) >= 0.25f)
-        return expm1_d - d;
+        return expm1_d < CUDART_INF_F ? expm1_d - d : expm1_d;  // d may be infinite too
     float s = 1.0f / 40320.0f;
     s = fmaf(s, d, 1.0f / 5040.0f);
     s = fmaf(s, d, 1.0f / 720.0f);

@@ -50,3 +50,25 @@ def test_without_a_coefficient_the_reference_changes_neither_loss_nor_weights(cu
         assert alone[0].isfinite() and alone[1].isfinite().all()
         assert torch.equal(alone[0], watched[0]) and torch.equal(alone[1], watched[1])
         assert torch.equal(alone[3], watched[3]) and not watched[2].isfinite()
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("kl_coef", [0.0, 0.1])
+@pytest.mark.parametrize("which", ["row_loss", "reference"])
+def test_infinitely_far_from_the_reference(cuda_lib, rows, kl_coef, which):
+    """exp(d) - 1 - d is infinite for d = inf, and for -inf; the other rows are as they were."""
+    now, ref = _rand(rows, 3, 0.0, 4.0), _rand(rows, 5, 0.0, 4.0)
+    old, a = now.clone(), torch.ones(rows, device="cuda")
+    before = policy_loss(now, old, a, ref_row_loss=ref, kl_coef=kl_coef)
+    (now if which == "row_loss" else ref)[7] = INF
+    loss, weights, kl, _ = policy_loss(now, old, a, ref_row_loss=ref, kl_coef=kl_coef)
+    assert kl.item() == INF
+    others = torch.arange(rows, device="cuda") != 7
+    assert torch.equal(weights[others], before[1][others])
+    if kl_coef:
+        assert loss.item() == INF
+        # the ratio is 0 or 1, and exp(d) - 1 infinite or -1
+        want = INF if which == "row_loss" else (1 - kl_coef) / rows
+        assert weights[7].item() == pytest.approx(want, rel=1e-6)
+    else:
+        assert loss.isfinite()
