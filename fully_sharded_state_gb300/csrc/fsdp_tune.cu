@@ -261,11 +261,26 @@ __device__ __forceinline__ Pair pair_of(const TuneParams &p, Two sg, Two sp, int
     return r;
 }
 
-// exp(d) - 1 - d; its series where the two would cancel.
+// Beyond kFar exp(v) is multiplied into a result before it leaves fp32: it is
+// taken as exp(v / 2) twice, with the factors between, so that a result is
+// infinite only where fp32 does not hold it. (exp(64) is 2^92: up to there
+// factors of 2^35 have room.) lo: what rounding left of v.
+constexpr float kFar = 64.0f;
+__device__ __forceinline__ float far_exp(float v, float lo, float a, float k)
+{
+    const float half = expf(0.5f * v), r = half * a * k * half;
+    return fabsf(r) < CUDART_INF_F ? fmaf(r, lo, r) : r;
+}
+
+// KL estimates are summed at 2^-40 of their size, which is exact: the mean of
+// 2^31 of them is infinite only where fp32 does not hold it.
+constexpr float kKlUnit = 1.0f / (float)(1ull << 40);
+
+// exp(d) - 1 - d up to kFar; its series where the two would cancel.
 __device__ __forceinline__ float kl_of(float d, float expm1_d)
 {
     if (fabsf(d) >= 0.25f)
-        return expm1_d < CUDART_INF_F ? expm1_d - d : expm1_d;  // d may be infinite too
+        return expm1_d - d;
     float s = 1.0f / 40320.0f;
     s = fmaf(s, d, 1.0f / 5040.0f);
     s = fmaf(s, d, 1.0f / 720.0f);
@@ -276,29 +291,48 @@ __device__ __forceinline__ float kl_of(float d, float expm1_d)
     return s * d * d;
 }
 
-// A row of the policy loss: its term, its slope, its KL estimate.
+// A row of the policy loss: its term and its slope, which count k times, its KL
+// estimate in kKlUnit.
 struct PolicyRow {
-    float term, slope, kl;
+    float term, slope, k, kl;
     bool cut;
 };
-__device__ __forceinline__ PolicyRow policy_row(const TuneParams &p, float now, float old, float ref, float a)
+__device__ __forceinline__ PolicyRow policy_row(const TuneParams &p, float now, float old, float ref, float a, float k)
 {
-    PolicyRow r{0.0f, 0.0f, 0.0f, false};
+    PolicyRow r{0.0f, 0.0f, k, 0.0f, false};
     const Two l = difference(old, now);
     r.cut = a > 0.0f ? above(l, p.log_high) : a < 0.0f && above(p.log_low, l);
     if (a != 0.0f) {
-        // what rounding l left; an infinite e has none of it (inf - inf where it is below 0)
-        const float e = expf(l.hi), ratio = e < CUDART_INF_F ? fmaf(e, l.lo, e) : e;
+        const float e = expf(l.hi), ratio = fmaf(e, l.lo, e);
         r.term = -(r.cut ? (a > 0.0f ? p.high : p.low) : ratio) * a;
         r.slope = r.cut ? 0.0f : ratio * a;
     }
+    float d = 0.0f, g = 0.0f;
     if (p.ref) {
-        const float d = now - ref, g = expm1f(d);
+        d = now - ref;
+        g = expm1f(d);
         r.kl = kl_of(d, g);
-        if (p.kl_coef != 0.0f) {  // else the KL is only watched: 0 times an infinite one is no part of the loss
-            r.term = fmaf(p.kl_coef, r.kl, r.term);
-            r.slope = fmaf(p.kl_coef, g, r.slope);
+    }
+    // without a coefficient the KL is only watched: 0 times an infinite one is no part of the loss
+    const float coef = p.kl_coef;
+    if (l.hi > kFar || d > kFar) {
+        const bool far = l.hi > kFar && a != 0.0f && !r.cut;
+        const float ratio = far ? far_exp(l.hi, l.lo, a, k) : 0.0f;
+        r.term = far ? -ratio : r.term * k;
+        r.slope = far ? ratio : r.slope * k;
+        if (coef != 0.0f) {
+            const float v = d > kFar ? far_exp(d, 0.0f, coef, k) : 0.0f;
+            r.term += d > kFar ? v : coef * r.kl * k;
+            r.slope += d > kFar ? v : coef * g * k;
         }
+        r.k = 1.0f;
+        r.kl = d > kFar ? far_exp(d, 0.0f, kKlUnit, 1.0f) : r.kl * kKlUnit;
+    } else {
+        if (coef != 0.0f) {
+            r.term = fmaf(coef, r.kl, r.term);
+            r.slope = fmaf(coef, g, r.slope);
+        }
+        r.kl *= kKlUnit;
     }
     return r;
 }
@@ -306,7 +340,7 @@ __device__ __forceinline__ PolicyRow policy_row(const TuneParams &p, float now, 
 __device__ __forceinline__ void policy_results(const TuneParams &p, Two loss, Two kl, int clipped, int counted, bool bad)
 {
     *p.loss = bad ? CUDART_NAN_F : loss.hi;
-    *p.kl = bad ? CUDART_NAN_F : kl.hi / (float)max(counted, 1);
+    *p.kl = bad ? CUDART_NAN_F : kl.hi / (float)max(counted, 1) / kKlUnit;
     *p.clipped = bad ? CUDART_NAN_F : (float)clipped / (float)max(counted, 1);
 }
 
@@ -471,10 +505,10 @@ __global__ void __launch_bounds__(kOneBlock) small_kernel(const TuneParams p)
             const int r = i * kOneBlock + t;
             float weight = 0.0f;
             if (in[i]) {
-                const PolicyRow q = policy_row(p, now[i], other[i], third[i], p.by_sequence ? p.advantages[seq[i]] : adv[i]);
                 const float k = p.reduction == FSDP_POLICY_SEQUENCE ? per * share[seq[i]] : per;
-                weight = q.slope * k;
-                loss = fmaf(q.term, k, loss);
+                const PolicyRow q = policy_row(p, now[i], other[i], third[i], p.by_sequence ? p.advantages[seq[i]] : adv[i], k);
+                weight = q.slope * q.k;
+                loss = fmaf(q.term, q.k, loss);
                 kl += q.kl;
                 clipped += q.cut;
             }
@@ -763,10 +797,10 @@ __global__ void __launch_bounds__(kThreads) row_kernel(const TuneParams p)
                     const int r = b0 + i * 32 + lane;
                     float weight = part[i];
                     if (!kPreference && in[i]) {
-                        const PolicyRow q = policy_row(p, now[i], old[i], ref[i], adv[i]);
                         const float k = part[i] * per;
-                        weight = q.slope * k;
-                        loss_c = fmaf(q.term, k, loss_c);
+                        const PolicyRow q = policy_row(p, now[i], old[i], ref[i], adv[i], k);
+                        weight = q.slope * q.k;
+                        loss_c = fmaf(q.term, q.k, loss_c);
                         kl_c += q.kl;
                         clipped += q.cut;
                     }

@@ -215,9 +215,10 @@ typedef enum { FSDP_POLICY_MEAN = 0, FSDP_POLICY_SUM = 1, FSDP_POLICY_SEQUENCE =
  * that count, their sum, or the mean over the sequences with such rows of their
  * means. sequences and offsets [sequences + 1] int64 may be 0 and NULL: then
  * all rows are one's, and the last reduction is refused. advantages: [rows], or
- * [sequences] where
- * by_sequence is not 0. kl, clipped [1], fp32: the mean of exp(d) - 1 - d and
- * the share of clipped rows, both over the rows that count. */
+ * [sequences] where by_sequence is not 0. kl, clipped [1], fp32: the mean of
+ * exp(d) - 1 - d and the share of clipped rows, both over the rows that count.
+ * exp(l) and exp(d) may pass fp32's range: what comes of a row is infinite only
+ * where fp32 does not hold it with A or kl_coef and the row's part of the mean. */
 fsdp_status fsdp_policy_loss(int64_t rows, int64_t sequences, const float *row_loss,
                              const float *old_row_loss, const float *ref_row_loss,
                              const float *advantages, int by_sequence, const int64_t *offsets,
