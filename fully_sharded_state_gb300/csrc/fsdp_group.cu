@@ -1329,17 +1329,22 @@ bool starts_on_16(const void *p, int64_t ld, int64_t stride)
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0 && stride % 8 == 0;
 }
 
-// Whether a backward pass takes both products in one kernel: over few rows,
-// where its tiles are as good as any, and few weights, where a launch counts.
-// 300 rows at 4 experts of 512 x 512 take 8.7 us so and 10.4 in two kernels,
-// 1024 at 64 of 1024 x 512 33.1 and 36.3, 1500 at 5 of 513 x 1001 29.7 and 32.0;
-// but 64 rows at 8 of 4096 x 4096 107 and 103, and 2 rows at 8 of 14336 x 4096,
-// nearly all of which is zeros for dW, 249 and 210.
+// Whether a backward pass takes both products in one kernel: that saves a launch
+// and fills one product's last tiles with the other's, but its tiles are narrow
+// (dx 32 or 64 rows, dW one CTA) and its sums whole. Each bound lies where the two
+// cross: the one kernel's time over the two kernels', geometric means over 2,800 sizes
+// of 1 to 512 experts, those inside the other bounds.
+//   rows of an expert   512 0.88, 1024 0.98, 1536 1.06, 4096 1.25: dW in parts is shorter
+//   rows n k            2^30 0.90, 2^31 0.97, 2^31.5 1.00, 2^32 1.11: wider tiles are
+//   weights             2^25 0.93, 2^25.5 0.97, 2^26.25 1.01
+//   n, dx's K           1024 0.91, 2048 0.97, 4096 1.05: dx's few tiles are long
+//   rows k              2^22 0.95, 2^22.5 0.88, 2^23 1.07, 2^24 1.39: its dx leaves two bytes at a time
 bool takes_both(const GroupArgs &a)
 {
     const int64_t used = a.experts < a.rows ? a.experts : a.rows;
-    return (a.rows <= 64 * used || (double)a.rows * (double)a.n * (double)a.k <= 8e8) &&
-           a.experts * a.n * a.k <= int64_t(1) << 25;
+    return a.rows <= 1024 * used && a.n <= 40 * kBK && a.rows * a.k <= int64_t(7) << 20 &&
+           (double)a.rows * (double)a.n * (double)a.k <= 3e9 &&
+           a.experts * a.n * a.k <= int64_t(50) << 20;
 }
 
 // The workspace of one call, and its forms.
@@ -1360,9 +1365,7 @@ GroupPlan group_plan(const GroupArgs &a, bool backward, bool x_on_16, bool dy_on
     if (backward) {
         q.dx = form_of(kInput, a.experts, a.rows, 0, a.k, a.n);
         q.dw = form_of(kWeight, a.experts, a.rows, a.n, a.k, 0);
-        // one kernel's sums are whole: of 32 and 64 K blocks at most where parts would be shorter
-        const int64_t used = a.experts < a.rows ? a.experts : a.rows;
-        q.both = a.rows > 0 && !(q.dw.split && a.rows > 32 * kBK * used) && !(q.dx.split && a.n > 64 * kBK) && takes_both(a);
+        q.both = a.rows > 0 && takes_both(a);
     } else {
         q.y = form_of(kForward, a.experts, a.rows, 0, a.n, a.k);
     }
