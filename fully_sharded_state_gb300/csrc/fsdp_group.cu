@@ -1141,9 +1141,12 @@ GroupForm group_form(int mode, int64_t experts, double average, int64_t outer, i
         const double mma = nk * std::fmax((double)(kTM + columns / ctas) * 128 / (few ? 45 : 70), 2.0 * (double)columns);
         double cost = (mma > epi ? waves * mma + epi : waves * epi + mma) + 2500;
         bool split = false;
-        if (few && ctas == 1 && tn <= 128 && mma > (mode == kWeight ? 20000 : 30000)) {
-            // the parts' stores, and the launch that adds them up. The caller's thread
-            // takes 3 us for it, which a forward call alone would show
+        if (few && ctas == 1 && tn <= 128 && mma > (mode == kForward ? 30000 : 40000)) {
+            // the parts' stores, and the launch that adds them up, which the caller's
+            // thread takes 3 us for. With and without parts, by the clocks of a tile's
+            // loads and multiplications (810 sizes of 1 to 4 experts, inputs from memory or
+            // from L2 alike; time over time, geometric means): forward 16,000 1.7, 23,000 1.3, 32,000
+            // 1.1, 45,000 0.9, 64,000 0.74; dx 1.5, 1.3, 1.2, 1.06, 0.83; dW 1.6, 1.5, 1.3, 1.1, 0.86
             const double splits = std::fmin((double)kMostSplits, std::floor(slots / tiles)), c = mma / splits + 2 * epi + 2500 + 9000;
             split = c < cost;
             cost = split ? c : cost;

@@ -34,3 +34,14 @@ def test_a_few_more_experts_or_rows_go_the_same_way(n, k):
     for experts in range(1, (1 << 25) // (n * k) + 3):
         for rows in (experts, 16 * experts, 48 * experts):
             assert tune.grouped_plan(rows, experts, n, k, True)[0]["kind"] == "both", (rows, experts)
+
+
+# whether dW's sums are taken in parts and joined
+WHOLE = [(3000, 1, 256, 256), (6000, 2, 128, 128), (12000, 4, 64, 64)]  # 21.1 and 30.9, 20.6 and 29.1, 21.4 and 30.2
+PARTS = [(16384, 2, 128, 1024), (32768, 4, 256, 256), (8192, 1, 64, 64)]  # 50.8 and 35.5, 51.3 and 31.5, 34.8 and 25.9
+
+
+@pytest.mark.parametrize("shape", WHOLE + PARTS, ids=str)
+def test_sums_whole_or_in_parts(shape):
+    dw, = [q for q in tune.grouped_plan(*shape, True) if q["kind"] == "mode" and q["mode"] == 2]
+    assert dw["split"] == (shape in PARTS)
