@@ -1337,7 +1337,8 @@ bool starts_on_16(const void *p, int64_t ld, int64_t stride)
 // (dx 32 or 64 rows, dW one CTA) and its sums whole. Each bound lies where the two
 // cross: the one kernel's time over the two kernels', geometric means over 2,800 sizes
 // of 1 to 512 experts, those inside the other bounds.
-//   rows of an expert   512 0.88, 1024 0.98, 1536 1.06, 4096 1.25: dW in parts is shorter
+//   rows of an expert   512 0.92, 1024 1.00, 1536 1.07, 4096 1.30: dW in parts is shorter;
+//                       of little work later (2^24 products: 1536 0.91, 2048 0.95, 3000 1.04)
 //   rows n k            2^30 0.90, 2^31 0.97, 2^31.5 1.00, 2^32 1.11: wider tiles are
 //   weights             2^25 0.93, 2^25.5 0.97, 2^26.25 1.01
 //   n, dx's K           1024 0.91, 2048 0.97, 4096 1.05: dx's few tiles are long
@@ -1345,9 +1346,9 @@ bool starts_on_16(const void *p, int64_t ld, int64_t stride)
 bool takes_both(const GroupArgs &a)
 {
     const int64_t used = a.experts < a.rows ? a.experts : a.rows;
-    return a.rows <= 1024 * used && a.n <= 40 * kBK && a.rows * a.k <= int64_t(7) << 20 &&
-           (double)a.rows * (double)a.n * (double)a.k <= 3e9 &&
-           a.experts * a.n * a.k <= int64_t(50) << 20;
+    const double products = (double)a.rows * (double)a.n * (double)a.k;
+    return a.rows <= (products <= (double)(1 << 24) ? 2048 : 1024) * used && a.n <= 40 * kBK &&
+           a.rows * a.k <= int64_t(7) << 20 && products <= 3e9 && a.experts * a.n * a.k <= int64_t(50) << 20;
 }
 
 // The workspace of one call, and its forms.

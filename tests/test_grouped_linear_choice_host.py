@@ -13,7 +13,7 @@ ONE = [(1024, 64, 1024, 512),  # 33 and 36
        (24576, 256, 256, 256),  # 33.1 and 52.7
        (9216, 96, 512, 512),  # 33.3 and 39.6
        (300, 4, 512, 512), (1001, 5, 513, 1001),
-       (1024, 1, 64, 64)]  # 8.9 and 11.6
+       (1024, 1, 64, 64), (1536, 1, 64, 64), (2048, 1, 16, 64)]  # 8.9 and 11.6, 10.7 and 13.3, 12.7 and 15.2
 TWO = [(4, 1, 4096, 4096), (16, 4, 4096, 1024), (20, 4, 4096, 2304),  # a long dx: 32.2 and 28.0, 31.7 and 28.0, 43 and 39
        (8192, 16, 64, 4096), (2048, 2, 64, 4096),  # a wide dx: 60.0 and 38.0, 24.3 and 18.7
        (4096, 4, 4096, 4096),
