@@ -1037,9 +1037,9 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
 // ------------------------------------------------------------------ prep ----
 
 // Matrices to copy so that their rows start on 16 bytes, piece by piece of 8
-// elements, four of a thread on their way at a time, whatever the rows' length
-// (a warp per row took 94 us for 113 matrices of 1854 x 390, and 37 for one of
-// 84 x 15805).
+// elements, one of a thread at a time, whatever the rows' length (a warp per row
+// took 94 us for 113 matrices of 1854 x 390, and 37 for one of 84 x 15805; with two
+// pieces of a thread on their way, forward over the 113 takes 130 us, not 109, with four 243).
 struct PackJob {
     const uint16_t *from;
     uint16_t *to;
@@ -1068,31 +1068,18 @@ __global__ void __launch_bounds__(256, 8) group_pack_kernel(const __grid_constan
 {
     launch_wait();
     launch_next();
-    constexpr int kFlight = 1;
     const int64_t step = (int64_t)gridDim.x * 256;
     for (int j = 0; j < p.jobs; j++) {
         const PackJob &q = p.job[j];
         const uint16_t *end = q.from + (over(over(q.pieces - 1, q.per_row), q.per_matrix)) * q.stride + (q.rows - 1) * q.ld + q.cols;
-        for (int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x; i0 < q.pieces; i0 += kFlight * step) {
-            Piece v[kFlight];
-            uint16_t *to[kFlight];
-#pragma unroll
-            for (int f = 0; f < kFlight; f++) {
-                const int64_t i = i0 + f * step;
-                to[f] = nullptr;
-                if (i >= q.pieces)
-                    continue;
-                const int64_t row = over(i, q.per_row), z = over(row, q.per_matrix);
-                const int col = (int)(i - row * q.per_row.d) * 8;
-                if (q.weights && !may_have_rows(p.offsets, z))
-                    continue;
-                to[f] = q.to + row * q.ld_to + col;
-                v[f].load(q.from + z * q.stride + (row - z * q.rows) * q.ld + col, q.cols - col, q.from, end);
-            }
-#pragma unroll
-            for (int f = 0; f < kFlight; f++)
-                if (to[f])
-                    *reinterpret_cast<uint4 *>(to[f]) = v[f].get();
+        for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < q.pieces; i += step) {
+            const int64_t row = over(i, q.per_row), z = over(row, q.per_matrix);
+            const int col = (int)(i - row * q.per_row.d) * 8;
+            if (q.weights && !may_have_rows(p.offsets, z))
+                continue;
+            Piece v;
+            v.load(q.from + z * q.stride + (row - z * q.rows) * q.ld + col, q.cols - col, q.from, end);
+            *reinterpret_cast<uint4 *>(q.to + row * q.ld_to + col) = v.get();
         }
     }
 }
