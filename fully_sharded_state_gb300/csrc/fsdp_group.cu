@@ -19,12 +19,12 @@
 // copy that dx's idle warps make (copy_tails).
 //
 // Many rows an expert are bound by the tensor cores, at the clock that the power
-// limit leaves: 16384 rows at 8 experts of 14336 x 4096 forward in 1,195 to 1,240
-// us, 1,550 to 1,610 TFLOP/s (alone and cool 1,815, the tensor pipe active for 92
-// % of the time), backward of 4096 x 14336 in 2,365 to 2,430. Few rows are bound
-// by the weights' way from memory: 2 rows at two of 8 experts of 14336 x 4096 in
-// 38 to 42 us, 5.6 to 6.0 TB/s; 1024 rows at 64 of 1024 x 512 forward in 14.6 us,
-// backward in 33, where each tile's way through the block shows.
+// limit leaves: 16384 rows at 8 experts of 14336 x 4096 forward in 1,180 to 1,240
+// us, 1,550 to 1,630 TFLOP/s (alone and cool 1,815, the tensor pipe active for 92
+// % of the time), backward of 4096 x 14336 in 2,340 to 2,430. Few rows are bound
+// by the weights' way from memory: a row at each of two experts of 14336 x 4096 in
+// 42 us, 5.6 TB/s; 1024 rows at 64 of 1024 x 512 forward in 15 us, backward in 33,
+// where a block's start, its first loads and its last epilogue show.
 #include <cuda_runtime.h>
 
 #include <cmath>
