@@ -174,7 +174,8 @@ fsdp_status fsdp_grouped_linear_backward_workspace(int64_t rows, int64_t experts
  * residual, whatever the strides. What is dropped counts for nothing, infinite
  * or NaN. offset_more: NULL, or an int64 on the device that is added to offset
  * (mod 2^64) when the kernel runs, for calls that are captured and replayed.
- * x, residual, y: dtype. p in [0, 1]; p = 1 drops everything. */
+ * x, residual, y: dtype. p in [0, 1]; T = 0 (p = 1, or nearer to it than 2^-17)
+ * drops everything. */
 fsdp_status fsdp_dropout(int64_t rows, int64_t cols, const void *x, int64_t ldx,
                          const void *residual, int64_t ldr, fsdp_dtype dtype, double p,
                          uint64_t seed, uint64_t offset, const int64_t *offset_more, void *y,
