@@ -32,7 +32,7 @@ def test_one_kernel_or_two(shape):
 def test_a_few_more_experts_or_rows_go_the_same_way(n, k):
     """Whatever their number, up to and past 2^25 weights."""
     for experts in range(1, (1 << 25) // (n * k) + 3):
-        for rows in (experts, 16 * experts, 48 * experts):
+        for rows in (experts, 15 * experts, 47 * experts):
             assert tune.grouped_plan(rows, experts, n, k, True)[0]["kind"] == "both", (rows, experts)
 
 
